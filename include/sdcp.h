@@ -77,7 +77,8 @@ extern "C" {
 #define SDCP_OK           0
 #define SDCP_E_INVALID    1  /* null pointer, B < 0, V < 1, unknown dtype, sizes overflow */
 #define SDCP_E_WORKSPACE  2  /* workspace null, too small or not 256-byte aligned */
-#define SDCP_E_ALIGN      3  /* a logits pointer is not aligned to its element size */
+#define SDCP_E_ALIGN      3  /* a logits pointer is not aligned to its element size, or a pointer
+                                or stride of the cache calls not to 16 bytes */
 #define SDCP_E_TOO_LARGE  4  /* V above SDCP_MAX_VOCAB or a row count above INT32_MAX */
 #define SDCP_E_LAUNCH     5  /* a CUDA launch failed (cudaGetLastError after launch) */
 #define SDCP_E_DEVICE     6  /* no usable CUDA device / device query failed */
@@ -363,6 +364,182 @@ int sdcp_commit_batch(int32_t B, const int32_t* m_offsets, const int32_t* accept
                       const sdcp_commit_params* cparams, const uint32_t* stop_tokens,
                       sdcp_session_state* state, uint32_t load_percent, int32_t* action,
                       void* stream);
+
+/* ---- before a verify call: penalties, biases and grammar masks on logits ---------- */
+/* Which rows of a batch an array of logits holds: target rows (M_b + 1 of each session,
+ * session b's first row is m_offsets[b] + b) or draft rows (M_b of each, first row
+ * m_offsets[b]).  Row i of a session is the distribution after its first i drafts. */
+#define SDCP_ROWS_TARGET 0
+#define SDCP_ROWS_DRAFT  1
+
+/* The logit controls of one session, 32 bytes, device memory, naturally aligned. */
+typedef struct sdcp_logit_controls {
+  float repetition;       /* > 0 and finite; 1 = none: a seen token's positive logit is divided
+                             by it, any other multiplied */
+  float frequency;        /* finite; taken off a logit times the token's number of outputs */
+  float presence;         /* finite; taken off once for a token with at least one output */
+  uint32_t history_len;   /* tokens of the session's history row: prompt, then outputs */
+  uint32_t prompt_len;    /* the first prompt_len of them are the prompt */
+  uint32_t bias_offset;   /* its biases are entries bias_offset .. bias_offset + bias_count - 1 */
+  uint32_t bias_count;    /*   of bias_tokens / bias_values, token ids strictly rising */
+  uint32_t reserved;
+} sdcp_logit_controls;
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the target or the draft rows of
+ * a ragged batch, before sdcp_verify_batch reads them.  For token t of row i of session b, with
+ *   c = the number of t among the session's outputs (history[prompt_len .. history_len)) and
+ *       its drafts x[0 .. i-1],
+ *   seen = t is in the prompt, or c > 0,
+ * the logit l becomes, in binary32 arithmetic and in this order,
+ *   seen:  l = l > 0 ? l / repetition : l * repetition;
+ *   l = l - frequency * c;   c > 0:  l = l - presence;   biased:  l = l + bias(t);
+ *   masked:  l = -inf (whatever it was, NaN included)
+ * and is rounded once to dtype.  A logit nothing applies to is copied bit for bit.
+ *
+ * logits        device, [rows][V] of dtype; rows = total_drafts + B (SDCP_ROWS_TARGET) or
+ *               total_drafts (SDCP_ROWS_DRAFT).
+ * out           device out, [rows][V] of dtype.  May be logits itself (in place: logits that
+ *               nothing applies to are then neither read nor written), else must not overlap.
+ * m_offsets, total_drafts, draft_tokens   as for sdcp_verify_batch; M_b in 0..SDCP_MAX_M.
+ *               draft_tokens may be NULL when total_drafts is 0.
+ * controls      device, [B].
+ * history       device, [B][history_stride] int32 token ids, the prompt first; may be NULL when
+ *               history_stride is 0.  Ids outside [0, V), here and among the drafts, count for
+ *               nothing.
+ * bias_tokens, bias_values   device, [n_bias] int32 / float; NULL when n_bias is 0.
+ * masks         device, [n_masks][mask_stride] uint32, mask_stride >= ceil(V / 32): bit t % 32 of
+ *               word t / 32 set = token t may be chosen.  NULL when n_masks is 0.
+ * mask_rows     device, [rows] int32: the mask of each row, -1 = none.  NULL: no row has one.
+ * status        device out, [B] int32: SDCP_S_OK; SDCP_S_LIMIT (M_b above SDCP_MAX_M);
+ *               SDCP_S_BAD_PARAMS (controls out of range, history_len above history_stride,
+ *               prompt_len above history_len, biases out of the arrays' range or not strictly
+ *               rising ids of [0, V), a mask index outside -1 .. n_masks - 1, or inconsistent
+ *               offsets).  The rows of such a session are filled with NaN, so that
+ *               sdcp_verify_batch commits nothing for it (with inconsistent offsets no row is
+ *               known to be the session's own, and none is written).
+ * A row whose mask leaves no token holds only -inf; sdcp_verify_batch reports it as
+ * SDCP_S_BAD_PARAMS.  No workspace; deterministic.  Returns SDCP_OK or SDCP_E_*.
+ */
+int sdcp_adjust_logits(const void* logits, void* out, int dtype, int64_t V, int32_t B, int rows,
+                       const int32_t* m_offsets, int64_t total_drafts, const int32_t* draft_tokens,
+                       const sdcp_logit_controls* controls, const int32_t* history,
+                       int64_t history_stride, const int32_t* bias_tokens, const float* bias_values,
+                       int64_t n_bias, const uint32_t* masks, int64_t mask_stride, int64_t n_masks,
+                       const int32_t* mask_rows, int32_t* status, void* stream);
+
+/* ---- scoring a round: a paged cache of keys and values in 4 bits ------------------ */
+/*
+ * A session's keys and values live in pages of page_tokens tokens; token t of session b is slot
+ * t % page_tokens of page page_table[b][t / page_tokens].  One array holds all pages:
+ *   pages[n_pages][kv_heads][2][block]   (uint8; 0 = keys, 1 = values)
+ * and a block, of P = page_tokens tokens and D = head_dim channels, is
+ *   codes  [D / 32][P][16 bytes]  then  scales [P][D / 32 bytes],
+ * so block = P (D / 2 + D / 32) bytes: 4.25 bits a channel.  The 16 bytes of a group of 32
+ * channels are four little-endian 32-bit words of 8 channels; channel e of a word is the four
+ * bits from 4 (e / 2 + 4 (e % 2)), holding n + 8 with n in -7..7.  A scale byte 8 e + m in
+ * 8..167 is s = (1 + m / 8) 2^(e - 15); the channel's value is n s (exact in bfloat16).
+ * Quantisation: s is the smallest scale >= (the group's largest magnitude) / 7 (the nearest end
+ * of the range where there is none: magnitudes above 420 saturate), n = x / s rounded to nearest
+ * even, clamped to -7..7; a NaN becomes 0.
+ */
+typedef struct sdcp_kv_cache {   /* host struct */
+  uint32_t struct_size;          /* sizeof(sdcp_kv_cache) */
+  int32_t n_pages;
+  int32_t page_tokens;           /* a power of two, 16..1024 */
+  int32_t kv_heads;              /* 1..256 */
+  int32_t head_dim;              /* 64 or 128 */
+  int32_t max_pages;             /* row length of page_table */
+  const int32_t* page_table;     /* device, [B][max_pages]; entries past a session's last token
+                                    are not read */
+  uint8_t* pages;                /* device, 16-byte aligned, n_pages * sdcp_kv_page_bytes bytes */
+} sdcp_kv_cache;
+
+/* Bytes of one page (all heads, keys and values); 0 for a geometry that is not supported. */
+size_t sdcp_kv_page_bytes(int32_t page_tokens, int32_t kv_heads, int32_t head_dim);
+
+#define SDCP_ROTARY_HALF        0  /* channel j turns with channel j + rot_dim / 2 */
+#define SDCP_ROTARY_INTERLEAVED 1  /* channel 2 j turns with channel 2 j + 1 */
+
+/* The position rotation: the first rot_dim channels of a head turn, the others stay.  Pair j at
+ * position t becomes (x1 cos - x2 sin, x2 cos + x1 sin), each product and sum rounded to binary32;
+ * the table carries the base, its scaling for long contexts and any factor on cos and sin. */
+typedef struct sdcp_rotary {     /* host struct */
+  uint32_t struct_size;          /* sizeof(sdcp_rotary) */
+  int32_t layout;                /* SDCP_ROTARY_* */
+  int32_t rot_dim;               /* even, 2..head_dim */
+  int32_t n_positions;           /* rows of the table */
+  const float* table;            /* device, [n_positions][rot_dim]: rot_dim / 2 cosines, then sines */
+} sdcp_rotary;
+
+/*
+ * Appends the keys and values of one round to the cache, turned by their positions on the way,
+ * and turns the queries with them.  The round of session b is its M_b + 1 target rows
+ * (m_offsets[b] + b + i); row i is the token at position kv_len[b] + i.  M_b = 0 is a single
+ * token, and M_b has no upper limit here (a prompt is one long round).  After the verdict the
+ * caller adds n_out[b] to kv_len[b]; what was rejected is overwritten by the next round.
+ *
+ * cache         the cache (host struct); sessions of one batch share no page they write to.
+ * m_offsets, total_drafts   as for sdcp_verify_batch.
+ * kv_len        device, [B] int32: tokens cached before the round.
+ * k, v          device, [total_drafts + B] rows of kv_heads * head_dim elements of dtype, rows
+ *               k_stride / v_stride elements apart; q (or NULL) likewise with q_heads heads.
+ *               16-byte aligned, strides a multiple of 16 bytes.
+ * rotary        host struct, or NULL: no rotation.
+ * q_out         device out, [total_drafts + B][q_heads][head_dim] of dtype, contiguous, 16-byte
+ *               aligned; NULL exactly when q is.  Must not overlap q.
+ * status        device out, [B] int32: SDCP_S_OK; SDCP_S_LIMIT (a position past the page table's
+ *               row or the rotary table); SDCP_S_BAD_PARAMS (a negative kv_len, a page outside
+ *               [0, n_pages) or inconsistent offsets).  A session that is not SDCP_S_OK writes
+ *               nothing to the cache; its rows of q_out are unspecified.
+ */
+int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
+                   int64_t total_drafts, const int32_t* kv_len, int dtype, const void* k,
+                   int64_t k_stride, const void* v, int64_t v_stride, const sdcp_rotary* rotary,
+                   const void* q, int64_t q_stride, int32_t q_heads, void* q_out, int32_t* status,
+                   void* stream);
+
+/*
+ * Stretches of cached tokens as values (a session that moves to another verifier, a check of a
+ * cache): tokens start[b] .. start[b] + n_b - 1 of session b, n_b = offsets[b+1] - offsets[b],
+ * become rows offsets[b] .. of k_out and v_out, [n_tokens][kv_heads][head_dim] of dtype (either
+ * may be NULL), 16-byte aligned.  offsets is device, [B+1] int32, offsets[0] = 0, non-decreasing,
+ * offsets[B] = n_tokens (given by the host as well); start is device, [B] int32.  status as for
+ * sdcp_append_kv; the rows of a session that is not SDCP_S_OK are zero.
+ */
+int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* offsets, int64_t n_tokens,
+                 const int32_t* start, int dtype, void* k_out, void* v_out, int32_t* status,
+                 void* stream);
+
+/* Bytes of device workspace sdcp_attend_kv needs; 0 for invalid sizes. */
+size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_heads,
+                                   int32_t kv_heads, int32_t head_dim);
+
+/*
+ * Attention of one round's rows over the cache.  Row i of session b attends the positions
+ *   max(0, kv_len[b] + i + 1 - window) .. kv_len[b] + i      (window 0: from 0)
+ * so each row sees the cached context, the round's earlier rows and itself (sdcp_append_kv has
+ * put them there).  Query head h reads cached head h / (q_heads / kv_heads):
+ *   out[row][h] = sum_t softmax_t(scale * q[row][h] . key_t) value_t.
+ * Scores, the softmax's statistics and the sums are binary32; out is rounded once.
+ *
+ * q             device, [total_drafts + B] rows of q_heads * head_dim bfloat16, q_stride elements
+ *               apart (16-byte aligned, stride a multiple of 8); q_heads a multiple of kv_heads.
+ * scale         finite; usually 1 / sqrt(head_dim).
+ * window        0 = none, else the number of positions a row sees, itself included.
+ * out           device out, [total_drafts + B][q_heads][head_dim] bfloat16, contiguous, 16-byte
+ *               aligned.
+ * status        device out, [B] int32, as for sdcp_append_kv (only the pages a row attends are
+ *               looked at); the rows of a session that is not SDCP_S_OK are zero.
+ * workspace     device scratch of sdcp_attend_workspace_bytes bytes, 256-byte aligned, no
+ *               initialisation needed.
+ * M_b has no upper limit here.  A query row holding NaN or infinities gives NaN in its own
+ * output row alone.  Deterministic.
+ */
+int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
+                   int64_t total_drafts, const int32_t* kv_len, const void* q, int64_t q_stride,
+                   int32_t q_heads, float scale, int32_t window, void* out, int32_t* status,
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Host-side split of one ragged batch into n_parts contiguous blocks of sessions for

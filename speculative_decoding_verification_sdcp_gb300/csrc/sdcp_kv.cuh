@@ -1,0 +1,99 @@
+// sdcp_kv.cuh - the paged 4-bit cache of keys and values: geometry, the checks of its sessions,
+// the lookup of a row's session, and the code that the cache kernels share.
+#pragma once
+
+#include "sdcp_device.cuh"
+
+namespace sdcp {
+
+constexpr int kKvGroup = 32;  // channels that share a scale
+
+// The cache as the kernels see it (checked on the host by kv_view).
+struct KvView {
+  uint8_t* pages;
+  const int32_t* page_table;
+  int32_t n_pages;
+  int32_t max_pages;
+  int32_t heads;
+  int32_t log_page;   // page_tokens = 1 << log_page
+  int32_t block;      // bytes of one head's keys or values in a page
+  int64_t page;       // bytes of a page
+
+  __device__ __forceinline__ int32_t page_tokens() const { return 1 << log_page; }
+};
+
+// SDCP_OK and the view, or the error of an unusable description.
+int kv_view(const sdcp_kv_cache* cache, KvView* out);
+
+// How a call's sessions lie on the cache.
+struct KvSessions {
+  int32_t B;
+  const int32_t* offsets;  // [B+1]
+  int64_t total;           // offsets[B]
+  int32_t extra;           // rows of a session beyond its offsets' difference (1: target rows)
+  const int32_t* start;    // [B] position of a session's first row
+  int32_t window;          // positions a row sees (0: from the start); -1: rows see themselves alone
+  int32_t limit;           // positions below this only (the rotary table); INT32_MAX: none
+};
+
+// Checks every session and writes its status: one CTA each, before the call's main kernel, which
+// reads status[b].  Offsets in order and in range, a start that is not negative, the last position
+// inside the page table's row and the limit, every page that the rows touch inside the pool.
+cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* status, cudaStream_t stream);
+
+// Launches `kernel` so that its blocks may start while the stream's previous kernel drains; it
+// orders itself behind that kernel with wait_for_previous().
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// The session of a row of a ragged list: the last b with offsets[b] + b * extra <= row, found by a
+// whole warp, 32 candidates a step.  Offsets out of order give some session; the caller checks.
+__device__ __forceinline__ int32_t session_of(const int32_t* offsets, int32_t B, int32_t extra, int64_t row) {
+  const uint32_t lane = threadIdx.x & 31u;
+  int32_t lo = 0, len = B;  // the answer is in [lo, lo + len)
+  while (len > 1) {
+    const int32_t step = (len + 31) / 32;
+    const int32_t b = lo + (int32_t)lane * step;
+    const bool le = b < lo + len && (int64_t)offsets[b] + (int64_t)b * extra <= row;
+    const int32_t k = 31 - __clz((int)(__ballot_sync(0xFFFFFFFFu, le) | 1u));
+    len = min(step, lo + len - (lo + k * step));
+    lo += k * step;
+  }
+  return lo;
+}
+
+// Scale bytes 8 e + m stand for (1 + m / 8) 2^(e - 15): the three mantissa bits and the exponent
+// of a binary32 whose exponent is re-biased by 112.
+constexpr uint32_t kScaleLow = 8u, kScaleHigh = 167u, kScaleBias = 112u << 3;
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float((byte + kScaleBias) << 20); }
+// The smallest scale >= most / 7 (most >= 0, may be infinite), as its byte.
+__device__ __forceinline__ uint32_t scale_byte(float most) {
+  const uint32_t u = __float_as_uint(__fdiv_rn(most, 7.0f)) + 0xFFFFFu;
+  const int32_t v = (int32_t)(u >> 20) - (int32_t)kScaleBias;
+  return (uint32_t)min(max(v, (int32_t)kScaleLow), (int32_t)kScaleHigh);
+}
+
+// Bytes in a block: a group's 16 bytes of codes of token slot t, and its scale byte.
+__device__ __forceinline__ int32_t code_at(int32_t group, int32_t slot, int32_t log_page) {
+  return ((group << log_page) + slot) << 4;
+}
+template <int D>
+__device__ __forceinline__ int32_t scale_at(int32_t group, int32_t slot, int32_t log_page) {
+  return (D / 2 << log_page) + slot * (D / kKvGroup) + group;
+}
+
+}  // namespace sdcp

@@ -20,6 +20,8 @@ SDCP_RULE_GREEDY, SDCP_RULE_SPECULATIVE_SAMPLING = 1, 2
 S_OK, S_BAD_PROPOSAL, S_LIMIT, S_BAD_PARAMS, S_Q_UNAVAILABLE, S_INTERNAL = 0, 1, 2, 3, 4, 5
 ROW_INVALID, ROW_X_KEPT, ROW_SKIPPED, ROW_FALLBACK = 1, 2, 4, 8
 MAX_M = 64
+ROWS_TARGET, ROWS_DRAFT = 0, 1
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 # sdcp_session_params (32 bytes) and sdcp_row_stat (32 bytes) as numpy records.
 PARAMS_DTYPE = np.dtype([("rule_id", "<u4"), ("temperature_milli", "<u4"), ("top_k", "<u4"),
@@ -41,6 +43,10 @@ COMMIT_PARAMS_DTYPE = np.dtype([("max_new", "<u4"), ("stop_offset", "<u4"), ("st
                                 ("m_restore", "<u4"), ("reserved", "<u4")])
 STATE_DTYPE = np.dtype([("digest", "u1", (32,)), ("committed", "<u4"), ("c", "<u4"), ("g", "<u4"),
                         ("j", "<u4"), ("m_cap", "<u4"), ("reserved", "<u4", (3,))])
+# sdcp_logit_controls (32 bytes)
+CONTROLS_DTYPE = np.dtype([("repetition", "<f4"), ("frequency", "<f4"), ("presence", "<f4"),
+                           ("history_len", "<u4"), ("prompt_len", "<u4"), ("bias_offset", "<u4"),
+                           ("bias_count", "<u4"), ("reserved", "<u4")])
 assert COMMIT_PARAMS_DTYPE.itemsize == 48 and STATE_DTYPE.itemsize == 64
 
 
@@ -48,6 +54,19 @@ class VerifyOptions(ctypes.Structure):
     """sdcp_verify_options."""
     _fields_ = [("struct_size", ctypes.c_uint32), ("rng_id", ctypes.c_uint32),
                 ("session_ids", ctypes.c_void_p), ("q_rows", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """sdcp_kv_cache."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("pages", ctypes.c_void_p)]
+
+
+class RotaryDesc(ctypes.Structure):
+    """sdcp_rotary."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("n_positions", ctypes.c_int32), ("table", ctypes.c_void_p)]
 
 
 class SdcpError(RuntimeError):
@@ -83,6 +102,19 @@ def _load():
     L.sdcp_commit_batch.restype = ctypes.c_int
     L.sdcp_split_sessions.argtypes = [vp, vp, i32, i32, vp]
     L.sdcp_split_sessions.restype = ctypes.c_int
+    L.sdcp_adjust_logits.argtypes = [vp, vp, ctypes.c_int, i64, i32, ctypes.c_int, vp, i64, vp, vp, vp, i64,
+                                     vp, vp, i64, vp, i64, i64, vp, vp, vp]
+    L.sdcp_adjust_logits.restype = ctypes.c_int
+    L.sdcp_kv_page_bytes.argtypes = [i32, i32, i32]
+    L.sdcp_kv_page_bytes.restype = sz
+    L.sdcp_append_kv.argtypes = [vp, i32, vp, i64, vp, ctypes.c_int, vp, i64, vp, i64, vp, vp, i64, i32, vp, vp, vp]
+    L.sdcp_append_kv.restype = ctypes.c_int
+    L.sdcp_read_kv.argtypes = [vp, i32, vp, i64, vp, ctypes.c_int, vp, vp, vp, vp]
+    L.sdcp_read_kv.restype = ctypes.c_int
+    L.sdcp_attend_workspace_bytes.argtypes = [i32, i64, i32, i32, i32]
+    L.sdcp_attend_workspace_bytes.restype = sz
+    L.sdcp_attend_kv.argtypes = [vp, i32, vp, i64, vp, vp, i64, i32, ctypes.c_float, i32, vp, vp, vp, sz, vp]
+    L.sdcp_attend_kv.restype = ctypes.c_int
     L.sdcp_strerror.argtypes = [ctypes.c_int]
     L.sdcp_strerror.restype = ctypes.c_char_p
     L.sdcp_abi_version.argtypes = []
@@ -249,6 +281,177 @@ def sdcp_row_stats(target_logits, draft_logits, m_offsets, total_drafts, draft_t
                                 _ptr(m_offsets), int(total_drafts), _ptr(draft_tokens), _ptr(params_dev),
                                 _ptr(stats_out), _ptr(workspace), workspace.numel(), s)
     _check(rc, "sdcp_row_stats")
+
+
+def controls_tensor(controls: np.ndarray, device) -> torch.Tensor:
+    raw = np.ascontiguousarray(controls, dtype=CONTROLS_DTYPE).view(np.uint8)
+    return torch.from_numpy(raw.copy()).to(device)
+
+
+def _is(t, dtype, what):
+    """The library reads raw memory: a tensor of another type or with gaps is refused here."""
+    if t is not None and (t.dtype != dtype or not t.is_contiguous()):
+        raise TypeError("%s must be a contiguous %s tensor" % (what, dtype))
+    return t
+
+
+def sdcp_adjust_logits(logits, out, m_offsets, total_drafts, draft_tokens, controls_dev, history, status,
+                       rows=ROWS_TARGET, bias_tokens=None, bias_values=None, masks=None, mask_rows=None,
+                       stream=None):
+    """Penalties, biases and grammar masks on target or draft rows: logits [rows, V] -> out (which
+    may be logits).  controls_dev: CONTROLS_DTYPE records as a uint8 tensor; history: int32
+    [B, stride] or None; bias_tokens / bias_values: int32 / float32 [n]; masks: int32 [n_masks,
+    words], one bit a token; mask_rows: int32 [rows], -1 = none; status: int32 [B], written."""
+    V = logits.shape[1]
+    B = status.shape[0]
+    code = dtype_code(logits)
+    n_rows = int(total_drafts) + (B if rows == ROWS_TARGET else 0)
+    if not logits.is_contiguous() or not out.is_contiguous() or out.dtype != logits.dtype or out.shape != logits.shape:
+        raise TypeError("logits and out must be contiguous tensors of one shape and type")
+    if logits.shape[0] < n_rows or (mask_rows is not None and mask_rows.numel() < n_rows):
+        raise ValueError("the batch has %d rows" % n_rows)
+    _is(m_offsets, torch.int32, "m_offsets"), _is(draft_tokens, torch.int32, "draft_tokens"), _is(status, torch.int32, "status")
+    _is(history, torch.int32, "history"), _is(bias_tokens, torch.int32, "bias_tokens"), _is(bias_values, torch.float32, "bias_values")
+    _is(masks, torch.int32, "masks"), _is(mask_rows, torch.int32, "mask_rows"), _is(controls_dev, torch.uint8, "controls_dev")
+    if (m_offsets.numel() < B + 1 or controls_dev.numel() < B * 32 or (history is not None and history.shape[0] < B)
+            or (draft_tokens is not None and draft_tokens.numel() < int(total_drafts))):
+        raise ValueError("m_offsets, controls, history and draft tokens must cover the %d sessions" % B)
+    if bias_tokens is not None and (bias_values is None or bias_values.numel() != bias_tokens.numel()):
+        raise ValueError("bias_tokens and bias_values must have the same length")
+    s = _stream_handle(logits.device) if stream is None else ctypes.c_void_p(stream)
+    with _on(logits):
+        rc = lib.sdcp_adjust_logits(_ptr(logits), _ptr(out), code, V, B, int(rows), _ptr(m_offsets), int(total_drafts),
+                                    _ptr(draft_tokens), _ptr(controls_dev), _ptr(history),
+                                    0 if history is None else history.shape[1], _ptr(bias_tokens), _ptr(bias_values),
+                                    0 if bias_tokens is None else bias_tokens.numel(), _ptr(masks),
+                                    0 if masks is None else masks.shape[1], 0 if masks is None else masks.shape[0],
+                                    _ptr(mask_rows), _ptr(status), s)
+    _check(rc, "sdcp_adjust_logits")
+
+
+class KvCache:
+    """The pages of a 4-bit cache of keys and values (sdcp_kv_cache): a uint8 tensor [n_pages,
+    kv_heads, 2, bytes], allocated here or given."""
+
+    def __init__(self, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device, pages=None):
+        n = int(lib.sdcp_kv_page_bytes(page_tokens, kv_heads, head_dim))
+        if n == 0 or n_pages < 1:
+            raise SdcpError("unsupported cache geometry (%d pages of %d tokens, %d heads of %d)"
+                            % (n_pages, page_tokens, kv_heads, head_dim))
+        shape = (n_pages, kv_heads, 2, n // (2 * kv_heads))
+        if pages is None:
+            pages = torch.zeros(shape, dtype=torch.uint8, device=device)
+        if tuple(pages.shape) != shape:
+            raise ValueError("pages must have the shape %s" % (shape,))
+        self.pages = _is(pages, torch.uint8, "pages")
+        self.n_pages, self.page_tokens, self.kv_heads, self.head_dim = n_pages, page_tokens, kv_heads, head_dim
+
+    def desc(self, page_table, B):
+        """The description of the cache with a batch's page table (int32 [B, max_pages])."""
+        if _is(page_table, torch.int32, "page_table").shape[0] < B:
+            raise ValueError("page_table must have a row for each of the %d sessions" % B)
+        return KvCacheDesc(ctypes.sizeof(KvCacheDesc), self.n_pages, self.page_tokens, self.kv_heads, self.head_dim,
+                           page_table.shape[1], page_table.data_ptr(), self.pages.data_ptr())
+
+
+class Rotary:
+    """A rotation table (sdcp_rotary): float32 [n_positions, rot_dim], rot_dim / 2 cosines and then
+    as many sines of each position."""
+
+    def __init__(self, table: torch.Tensor, layout: int = ROTARY_HALF):
+        self.table = _is(table, torch.float32, "table")
+        self.desc = RotaryDesc(ctypes.sizeof(RotaryDesc), int(layout), table.shape[1], table.shape[0], table.data_ptr())
+
+
+def _heads(t, rows, heads, dim, what):
+    """Row stride of a [rows, heads, dim] view whose rows may lie apart."""
+    if t.dim() != 3 or t.shape[0] < rows or t.shape[1:] != (heads, dim) or t.stride()[1:] != (dim, 1):
+        raise ValueError("%s must be [%d, %d, %d] with contiguous rows" % (what, rows, heads, dim))
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def sdcp_append_kv(cache, page_table, m_offsets, total_drafts, kv_len, k, v, status, rotary=None, q=None,
+                   q_out=None, stream=None):
+    """Appends a round's keys and values, k and v [total_drafts + B, kv_heads, head_dim], at
+    kv_len[b] .. of each session, turned by their positions; q [.., q_heads, head_dim] is turned
+    into q_out.  The rows of k, v and q may be views of a fused projection's output."""
+    B = status.shape[0]
+    rows = int(total_drafts) + B
+    code = dtype_code(k)
+    if v.dtype != k.dtype or (q is not None and (q.dtype != k.dtype or q_out is None or q_out.dtype != k.dtype)):
+        raise TypeError("q, k, v and q_out must have one type")
+    ks, vs = _heads(k, rows, cache.kv_heads, cache.head_dim, "k"), _heads(v, rows, cache.kv_heads, cache.head_dim, "v")
+    n_q = 0 if q is None else q.shape[1]
+    qs = 0 if q is None else _heads(q, rows, n_q, cache.head_dim, "q")
+    if q is not None and (not q_out.is_contiguous() or q_out.shape[0] < rows or q_out.shape[1:] != q.shape[1:]):
+        raise ValueError("q_out must be contiguous and have q's shape")
+    _is(m_offsets, torch.int32, "m_offsets"), _is(kv_len, torch.int32, "kv_len"), _is(status, torch.int32, "status")
+    if m_offsets.numel() < B + 1 or kv_len.numel() < B:
+        raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
+    desc = cache.desc(page_table, B)
+    s = _stream_handle(k.device) if stream is None else ctypes.c_void_p(stream)
+    with _on(k):
+        rc = lib.sdcp_append_kv(ctypes.byref(desc), B, _ptr(m_offsets), int(total_drafts), _ptr(kv_len),
+                                code, _ptr(k), ks, _ptr(v), vs, None if rotary is None else ctypes.byref(rotary.desc),
+                                _ptr(q), qs, n_q, _ptr(q_out), _ptr(status), s)
+    _check(rc, "sdcp_append_kv")
+
+
+def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, status, stream=None):
+    """Cached tokens as values: tokens start[b] .. of session b into rows offsets[b] ..
+    offsets[b+1] - 1 of k_out and v_out [n_tokens, kv_heads, head_dim] (either may be None)."""
+    B = status.shape[0]
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs or any(t.dtype != outs[0].dtype for t in outs):
+        raise TypeError("k_out and v_out must have one type, and one of them must be given")
+    for t in outs:
+        if not t.is_contiguous() or t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1:] != (cache.kv_heads, cache.head_dim):
+            raise ValueError("outputs must be contiguous [n_tokens, kv_heads, head_dim] tensors")
+    _is(offsets, torch.int32, "offsets"), _is(start, torch.int32, "start"), _is(status, torch.int32, "status")
+    if offsets.numel() < B + 1 or start.numel() < B:
+        raise ValueError("offsets and start must cover the %d sessions" % B)
+    desc = cache.desc(page_table, B)
+    s = _stream_handle(status.device) if stream is None else ctypes.c_void_p(stream)
+    with _on(status):
+        rc = lib.sdcp_read_kv(ctypes.byref(desc), B, _ptr(offsets), int(n_tokens), _ptr(start),
+                              dtype_code(outs[0]), _ptr(k_out), _ptr(v_out), _ptr(status), s)
+    _check(rc, "sdcp_read_kv")
+
+
+def sdcp_attend_workspace_bytes(B: int, total_drafts: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.sdcp_attend_workspace_bytes(B, total_drafts, q_heads, kv_heads, head_dim))
+
+
+def alloc_attend_workspace(B: int, total_drafts: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    n = sdcp_attend_workspace_bytes(B, total_drafts, q_heads, kv_heads, head_dim)
+    if n == 0:
+        raise SdcpError("invalid sizes for the workspace (B=%d, total=%d, heads %d / %d of %d)"
+                        % (B, total_drafts, q_heads, kv_heads, head_dim))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, status, workspace, scale=None,
+                   window=0, stream=None):
+    """Attention of a round's rows, q [total_drafts + B, q_heads, head_dim] bfloat16 (rows may lie
+    apart), over the cache: row i of session b sees positions up to kv_len[b] + i (the last
+    `window` of them; 0: all).  scale defaults to 1 / sqrt(head_dim)."""
+    B = status.shape[0]
+    rows = int(total_drafts) + B
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise TypeError("q and out must be torch.bfloat16")
+    qs = _heads(q, rows, q.shape[1], cache.head_dim, "q")
+    if not out.is_contiguous() or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
+        raise ValueError("out must be contiguous and have q's shape")
+    _is(m_offsets, torch.int32, "m_offsets"), _is(kv_len, torch.int32, "kv_len"), _is(status, torch.int32, "status")
+    if m_offsets.numel() < B + 1 or kv_len.numel() < B:
+        raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
+    desc = cache.desc(page_table, B)
+    s = _stream_handle(q.device) if stream is None else ctypes.c_void_p(stream)
+    with _on(q):
+        rc = lib.sdcp_attend_kv(ctypes.byref(desc), B, _ptr(m_offsets), int(total_drafts), _ptr(kv_len),
+                                _ptr(q), qs, q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), int(window),
+                                _ptr(out), _ptr(status), _ptr(workspace), workspace.numel(), s)
+    _check(rc, "sdcp_attend_kv")
 
 
 def sdcp_split_sessions(m_offsets: np.ndarray, params: np.ndarray | None, n_parts: int) -> np.ndarray:
