@@ -21,43 +21,16 @@ int kv_view(const sdcp_kv_cache* c, KvView* out) {
 
 namespace {
 
-constexpr int kCheckThreads = 128;
-
 __global__ void __launch_bounds__(kCheckThreads) kv_check_kernel(const KvView kv, const KvSessions s, int32_t* status) {
   let_next_start();
-  const int32_t b = (int32_t)blockIdx.x;
-  const int32_t lo = s.offsets[b], hi = s.offsets[b + 1], start = s.start[b];
-  int32_t st = SDCP_S_OK;
-  if (lo < 0 || hi < lo || (int64_t)hi > s.total || start < 0) {
-    st = SDCP_S_BAD_PARAMS;
-  } else {
-    const int64_t end = (int64_t)start + (hi - lo) + s.extra;  // one past the last position
-    const int64_t cap = min((int64_t)kv.max_pages << kv.log_page, (int64_t)s.limit);
-    if (end == start) {
-      st = SDCP_S_OK;  // no rows
-    } else if (end > cap) {
-      st = SDCP_S_LIMIT;
-    } else {
-      const int64_t first = s.window < 0 ? start : s.window == 0 ? 0 : max((int64_t)0, (int64_t)start + 1 - s.window);
-      bool bad = false;
-      for (int64_t p = (first >> kv.log_page) + threadIdx.x; p <= (end - 1) >> kv.log_page; p += kCheckThreads) {
-        const int32_t page = kv.page_table[(int64_t)b * kv.max_pages + p];
-        bad |= page < 0 || page >= kv.n_pages;
-      }
-      if (__syncthreads_or(bad)) st = SDCP_S_BAD_PARAMS;
-    }
-  }
-  if (threadIdx.x == 0) status[b] = st;
+  const int32_t st = kv_session_status(kv, s, (int32_t)blockIdx.x);
+  if (threadIdx.x == 0) status[blockIdx.x] = st;
 }
-
-}  // namespace
 
 cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* status, cudaStream_t stream) {
   kv_check_kernel<<<(unsigned)s.B, kCheckThreads, 0, stream>>>(kv, s, status);
   return cudaGetLastError();
 }
-
-namespace {
 
 // ---- append ---------------------------------------------------------------------------
 
@@ -104,7 +77,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
   const int64_t row = blockIdx.x;
   wait_for_previous();
-  const int32_t b = session_of(a.s.offsets, a.s.B, 1, row);
+  const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
   const int64_t i = row - a.s.offsets[b] - b;
   if (a.status[b] != SDCP_S_OK || i < 0 || i > (int64_t)a.s.offsets[b + 1] - a.s.offsets[b]) return;
   const int32_t pos = a.s.start[b] + (int32_t)i;
@@ -222,7 +195,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
     int64_t at = -1;
     int32_t slot = 0;
     if (row < a.s.total) {
-      const int32_t b = session_of(a.s.offsets, a.s.B, 0, row);
+      const int32_t b = find_session(a.s.offsets, a.s.B, row, false);
       const int64_t i = row - a.s.offsets[b];
       if (a.status[b] == SDCP_S_OK && i >= 0 && row < a.s.offsets[b + 1]) {
         const int32_t pos = a.s.start[b] + (int32_t)i;

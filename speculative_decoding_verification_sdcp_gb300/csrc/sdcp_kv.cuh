@@ -36,10 +36,25 @@ struct KvSessions {
   int32_t limit;           // positions below this only (the rotary table); INT32_MAX: none
 };
 
-// Checks every session and writes its status: one CTA each, before the call's main kernel, which
-// reads status[b].  Offsets in order and in range, a start that is not negative, the last position
-// inside the page table's row and the limit, every page that the rows touch inside the pool.
-cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* status, cudaStream_t stream);
+// The status of session b, found by a whole block of kCheckThreads: offsets in order and in range,
+// a start that is not negative, the last position inside the page table's row and the limit, every
+// page that the rows touch inside the pool.  A kernel of one block a session writes status[] before
+// the call's main kernel, which reads it.
+constexpr int kCheckThreads = 128;
+__device__ __forceinline__ int32_t kv_session_status(const KvView& kv, const KvSessions& s, int32_t b) {
+  const int32_t lo = s.offsets[b], hi = s.offsets[b + 1], start = s.start[b];
+  if (lo < 0 || hi < lo || (int64_t)hi > s.total || start < 0) return SDCP_S_BAD_PARAMS;
+  const int64_t end = (int64_t)start + (hi - lo) + s.extra;  // one past the last position
+  if (end == start) return SDCP_S_OK;                        // no rows
+  if (end > min((int64_t)kv.max_pages << kv.log_page, (int64_t)s.limit)) return SDCP_S_LIMIT;
+  const int64_t first = s.window < 0 ? start : s.window == 0 ? 0 : max((int64_t)0, (int64_t)start + 1 - s.window);
+  bool bad = false;
+  for (int64_t p = (first >> kv.log_page) + threadIdx.x; p <= (end - 1) >> kv.log_page; p += kCheckThreads) {
+    const int32_t page = kv.page_table[(int64_t)b * kv.max_pages + p];
+    bad |= page < 0 || page >= kv.n_pages;
+  }
+  return __syncthreads_or(bad) ? SDCP_S_BAD_PARAMS : SDCP_S_OK;
+}
 
 // Launches `kernel` so that its blocks may start while the stream's previous kernel drains; it
 // orders itself behind that kernel with wait_for_previous().
@@ -59,22 +74,6 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
 }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// The session of a row of a ragged list: the last b with offsets[b] + b * extra <= row, found by a
-// whole warp, 32 candidates a step.  Offsets out of order give some session; the caller checks.
-__device__ __forceinline__ int32_t session_of(const int32_t* offsets, int32_t B, int32_t extra, int64_t row) {
-  const uint32_t lane = threadIdx.x & 31u;
-  int32_t lo = 0, len = B;  // the answer is in [lo, lo + len)
-  while (len > 1) {
-    const int32_t step = (len + 31) / 32;
-    const int32_t b = lo + (int32_t)lane * step;
-    const bool le = b < lo + len && (int64_t)offsets[b] + (int64_t)b * extra <= row;
-    const int32_t k = 31 - __clz((int)(__ballot_sync(0xFFFFFFFFu, le) | 1u));
-    len = min(step, lo + len - (lo + k * step));
-    lo += k * step;
-  }
-  return lo;
-}
 
 // Scale bytes 8 e + m stand for (1 + m / 8) 2^(e - 15): the three mantissa bits and the exponent
 // of a binary32 whose exponent is re-biased by 112.
