@@ -48,6 +48,13 @@ constexpr uint32_t kTmemS = 64, kTmemO = 160;
 constexpr float kLift = 7.0f;     // a weight is 2^kLift at its reference
 constexpr float kTop = 15.0f;     // and 2^kTop at most
 
+// How a session's work is cut: kv heads x `chunks` items of at most `w` columns, `tiles` units each:
+// the most tiles any chunk needs (its own may be fewer), after kItemUnits for the item itself.
+struct SessionPlan {
+  int32_t w, chunks, tiles;
+};
+constexpr int32_t kItemUnits = 2;  // what an item's start and end cost, in tiles
+
 struct AttendArgs {
   KvView kv;
   KvSessions s;
@@ -58,7 +65,8 @@ struct AttendArgs {
   __nv_bfloat16* out;
   int32_t* status;
   uint32_t* error;   // non-zero: a bounded wait gave up
-  int64_t* units;    // [B] tiles of a session
+  int64_t* units;    // [B] units of a session: kv heads x chunks x tiles; 0 for a refused one
+  SessionPlan* plans;  // [B]
   int64_t* prefix;   // [B+1]
   float* parts;      // [kMaxCtas * 2] of Part<D>
   int32_t ctas;
@@ -70,25 +78,21 @@ template <int D> struct Part {
   float l[kCols];
 };
 
-// How a session's work is cut: `items` = kv heads x chunks of at most `w` columns, `tiles` each
-// (the most any of its chunks needs; a chunk's own tiles may be fewer).
-struct SessionPlan {
-  int64_t cols;
-  int32_t w;
-  int64_t chunks;
-  int64_t tiles;
-};
 __device__ __forceinline__ SessionPlan session_plan(int32_t len, int32_t rows, int32_t share, int32_t window) {
   SessionPlan p;
-  p.cols = (int64_t)rows * share;
-  p.chunks = (p.cols + kCols - 1) / kCols;
-  const int64_t even = (p.cols + p.chunks - 1) / p.chunks;
+  const int64_t cols = (int64_t)rows * share;
+  p.chunks = (int32_t)((cols + kCols - 1) / kCols);
+  const int64_t even = (cols + p.chunks - 1) / p.chunks;
   p.w = (int32_t)((even + 15) / 16 * 16);
-  p.chunks = (p.cols + p.w - 1) / p.w;
+  p.chunks = (int32_t)((cols + p.w - 1) / p.w);
   int64_t span = (int64_t)len + rows;
   if (window > 0) span = min(span, (int64_t)window - 1 + (p.w + share - 2) / share + 1 + 31);
-  p.tiles = (span + kTile - 1) / kTile;
+  p.tiles = (int32_t)((span + kTile - 1) / kTile) + kItemUnits;
   return p;
+}
+// a / b where both are rarely beyond 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // The line of tiles over the CTAs: CTA k has [first(k), first(k + 1)).
@@ -98,13 +102,13 @@ struct Line {
   __device__ __forceinline__ Line(int64_t t, int32_t most) {
     total = t;
     ctas = (int32_t)min((int64_t)most, max(t, (int64_t)1));
-    each = t / ctas;
-    more = t % ctas;
+    each = quotient(t, ctas);
+    more = t - each * ctas;
   }
   __device__ __forceinline__ int64_t first(int32_t k) const { return k * each + min((int64_t)k, more); }
   __device__ __forceinline__ int32_t cta_of(int64_t t) const {
     const int64_t big = more * (each + 1);
-    return t < big ? (int32_t)(t / (each + 1)) : (int32_t)(more + (t - big) / each);
+    return t < big ? (int32_t)quotient(t, each + 1) : (int32_t)(more + quotient(t - big, each));
   }
 };
 
@@ -186,6 +190,30 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// Sums of eight values over a warp: each exchange halves the values a lane carries, and lanes
+// 0..7 end with the sum of value `lane`.
+__device__ __forceinline__ float warp_sum8(const float* x, int lane) {
+  float y[4], z[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float keep = (lane & 4) ? x[k + 4] : x[k], give = (lane & 4) ? x[k] : x[k + 4];
+    y[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float keep = (lane & 2) ? y[k + 2] : y[k], give = (lane & 2) ? y[k] : y[k + 2];
+    z[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+  }
+  const float keep = (lane & 1) ? z[1] : z[0], give = (lane & 1) ? z[0] : z[1];
+  float s = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  return s;
+}
+
+// Byte g of w in both halves of a word.
+__device__ __forceinline__ uint32_t twice(uint32_t w, int g) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * g); }
+
 // A word of eight codes as pairs of numbers n s.  bfloat16: the four bits in the low end of
 // 128 + 8 + n; the pairs of a word lie four bits apart.
 __device__ __forceinline__ void word_bf16(uint32_t w, uint32_t s, uint32_t c, uint32_t* r) {
@@ -219,7 +247,8 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
     int64_t units = 0;
     if (st == SDCP_S_OK) {
       const SessionPlan p = session_plan(a.s.start[b], a.s.offsets[b + 1] - a.s.offsets[b] + 1, a.q_heads / a.kv.heads, a.s.window);
-      units = p.chunks * p.tiles * a.kv.heads;
+      units = (int64_t)p.chunks * p.tiles * a.kv.heads;
+      a.plans[b] = p;
     }
     a.units[b] = units;
     if (b == 0) *a.error = 0u;
@@ -239,6 +268,7 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
   __shared__ __align__(16) float s_nm[kCols];    // kLift - m: what a scaled score is shifted by
   __shared__ __align__(16) float s_f[kCols];     // factors of a rescale
   __shared__ __align__(16) int32_t s_last[kCols];  // last position of a column
+  __shared__ int32_t s_row[kCols], s_at[kCols];    // a column's row, and its place among the output's heads
   __shared__ float s_red[4][kCols];
   __shared__ uint64_t s_bar_s, s_bar_o;
   __shared__ uint32_t s_tmem;
@@ -315,73 +345,96 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
   uint32_t ph_s = 0, ph_o = 0;  // phases of the two barriers
   bool dead = false;
 
+  // where the line enters its first item; from there on it walks
+  SessionPlan pl = a.plans[b];
+  int64_t item = quotient(t - base, pl.tiles);
+  int32_t unit0 = (int32_t)(t - base - item * pl.tiles);
+  int32_t kvh = (int32_t)quotient(item, pl.chunks), chunk = (int32_t)(item - (int64_t)kvh * pl.chunks);
+  int32_t off = a.s.offsets[b], rows = a.s.offsets[b + 1] - off + 1, len = a.s.start[b];
+
   while (t < t_end && !dead) {
-    while (t >= base + a.units[b]) base += a.units[b++];
-    const int32_t off = a.s.offsets[b], rows = a.s.offsets[b + 1] - off + 1, len = a.s.start[b];
-    const SessionPlan pl = session_plan(len, rows, share, a.s.window);
-    const int64_t item = (t - base) / pl.tiles;
-    const int64_t tile0 = (t - base) % pl.tiles;
-    const int64_t tiles = min(pl.tiles - tile0, t_end - t);  // of this item, here
-    const bool whole = tiles == pl.tiles;
+    if (kvh == a.kv.heads) {  // the next session that has work
+      do ++b;
+      while (a.units[b] == 0);
+      pl = a.plans[b];
+      off = a.s.offsets[b], rows = a.s.offsets[b + 1] - off + 1, len = a.s.start[b];
+      kvh = 0;
+    }
+    const int32_t units = (int32_t)min((int64_t)(pl.tiles - unit0), t_end - t);  // of this item, here
+    const bool whole = units == pl.tiles;
     const int32_t slot = cta * 2 + (t == line.first(cta) ? 0 : 1);
-    const int32_t kvh = (int32_t)(item / pl.chunks);
-    const int64_t c0 = (item % pl.chunks) * pl.w;
-    const int32_t n = (int32_t)min((int64_t)pl.w, pl.cols - c0);
+    const int64_t c0 = (int64_t)chunk * pl.w;
+    const int32_t n = (int32_t)min((int64_t)pl.w, (int64_t)rows * share - c0);
     const int32_t n16 = (n + 15) / 16;      // blocks of 16 columns; a group of threads has eight of each
-    const int32_t i0 = (int32_t)(c0 / share), i1 = (int32_t)((c0 + n - 1) / share);
-    const int32_t end = len + i1 + 1;       // one past the last position any column sees
-    const int32_t lowest = a.s.window > 0 ? (int32_t)max((int64_t)0, (int64_t)len + i0 + 1 - a.s.window) : 0;
-    const int32_t begin = lowest & ~31;     // the first tile's start; tokens below `lowest` are not read
-    const int64_t real = ((int64_t)end - begin + kTile - 1) / kTile;  // tiles that hold something
-    const int32_t k0 = (int32_t)tile0, k1 = (int32_t)min(tile0 + tiles, real);
+    const int32_t i0 = (int32_t)quotient(c0, share), g0 = (int32_t)(c0 - (int64_t)i0 * share);
+    const int32_t i1 = i0 + (g0 + n - 1) / share;
+    const uint32_t end = (uint32_t)(len + i1) + 1u;  // one past the last position any column sees
+    const uint32_t lowest = a.s.window > 0 ? (uint32_t)max((int64_t)0, (int64_t)len + i0 + 1 - a.s.window) : 0u;
+    const uint32_t begin = lowest & ~31u;            // the first tile's start; tokens below `lowest` are not read
+    const int32_t real = (int32_t)((end - begin + kTile - 1) / kTile);  // tiles that hold something
+    const int32_t k0 = max(unit0 - kItemUnits, 0), k1 = min(max(unit0 + units - kItemUnits, 0), real);
     const int64_t row0 = (int64_t)off + b;
-    t += tiles;
+    const int32_t head_now = kvh;
+    t += units;
+    unit0 = 0;
+    if (++chunk == pl.chunks) {
+      chunk = 0;
+      ++kvh;
+    }
 
     // queries of the columns, zero past them, and the columns' state
     __syncthreads();
+    if (tid < kCols) {
+      const int32_t r = (g0 + tid) / share;
+      s_row[tid] = r;
+      s_at[tid] = r * a.q_heads + g0 + tid - r * share;
+      s_nm[tid] = tid < n ? INFINITY : kLift;
+      s_last[tid] = tid < n ? len + i0 + r : INT_MAX;
+    }
+    __syncthreads();
+    const __nv_bfloat16* const q0 = a.q + (row0 + i0) * a.q_stride + (int64_t)head_now * share * D;
     for (int k = tid; k < n16 * 16 * (D / 8); k += kThreads2) {
       const int j = k / (D / 8), ch = k % (D / 8);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (j < n) {
-        const int64_t col = c0 + j;
-        v = *reinterpret_cast<const uint4*>(a.q + (row0 + col / share) * a.q_stride + ((int64_t)kvh * share + col % share) * D + ch * 8);
-      }
+      if (j < n) v = *reinterpret_cast<const uint4*>(q0 + s_row[j] * a.q_stride + (s_at[j] - s_row[j] * a.q_heads) * D + ch * 8);
       *reinterpret_cast<uint4*>(s_q + (ch / 8) * (kCols * 128) + j * 128 + (((ch & 7) ^ (j & 7)) << 4)) = v;
-    }
-    if (tid < kCols) {
-      s_nm[tid] = tid < n ? INFINITY : kLift;
-      s_last[tid] = tid < n ? len + (int32_t)((c0 + tid) / share) : INT_MAX;
     }
     fence_async_smem();
     float l[kColsHalf];
 #pragma unroll
     for (int j = 0; j < kColsHalf; ++j) l[j] = 0.0f;
     const uint32_t idesc_n = (uint32_t)(n16 * 16 / 8) << 17;
-    const uint8_t* const head = a.kv.pages + ((int64_t)kvh * 2 + wg) * a.kv.block;
+    const uint8_t* const head = a.kv.pages + ((int64_t)head_now * 2 + wg) * a.kv.block;
     const int32_t* const table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
 
     // a tile ahead: the page of the next token, and its codes
     uint4 code[kGroups];
     uint32_t scales = 0;
     int32_t next_page = 0;
+    const uint32_t group_bytes = 16u << a.kv.log_page, slot_mask = (1u << a.kv.log_page) - 1u;
     auto find_page = [&](int32_t k) {
-      const int64_t pos = (int64_t)begin + (int64_t)k * kTile + tok;
+      const uint32_t pos = begin + (uint32_t)k * kTile + (uint32_t)tok;
       if (k < k1 && pos >= lowest && pos < end) next_page = table[pos >> a.kv.log_page];
     };
     auto fetch = [&](int32_t k) {
-      const int64_t pos = (int64_t)begin + (int64_t)k * kTile + tok;
-      scales = 0u;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) code[g] = make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t pos = begin + (uint32_t)k * kTile + (uint32_t)tok;
+      scales = 0u;  // a token that is not read becomes finite numbers, whose weight is zero
       if (k < k1 && pos >= lowest && pos < end) {
+        const uint32_t slot_in = pos & slot_mask;
         const uint8_t* blk = head + (int64_t)next_page * a.kv.page;
-        const int32_t slot_in = (int32_t)pos & (a.kv.page_tokens() - 1);
+        const uint8_t* at = blk + slot_in * 16u;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) code[g] = *reinterpret_cast<const uint4*>(blk + code_at(g, slot_in, a.kv.log_page));
-        if (D == 128) scales = *reinterpret_cast<const uint32_t*>(blk + scale_at<D>(0, slot_in, a.kv.log_page));
-        else scales = *reinterpret_cast<const uint16_t*>(blk + scale_at<D>(0, slot_in, a.kv.log_page));
+        for (int g = 0; g < kGroups; ++g) {
+          code[g] = *reinterpret_cast<const uint4*>(at);
+          at += group_bytes;
+        }
+        blk += (D / 2 << a.kv.log_page) + slot_in * (D / kKvGroup);
+        if (D == 128) scales = *reinterpret_cast<const uint32_t*>(blk);
+        else scales = *reinterpret_cast<const uint16_t*>(blk);
       }
     };
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) code[g] = make_uint4(0u, 0u, 0u, 0u);
     find_page(k0);
     fetch(k0);
     find_page(k0 + 1);
@@ -389,14 +442,12 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
 
     for (int32_t k = k0; k < k1; ++k) {
       const bool first = k == k0;
-      const int64_t pos = (int64_t)begin + (int64_t)k * kTile + tok;
+      const uint32_t lo = begin + (uint32_t)k * kTile, pos = lo + (uint32_t)tok;
       // keys to tensor memory, then S; values to shared memory (once the previous O product has read it)
       if (wg == 0) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const uint32_t byte = (scales >> (8 * g)) & 0xFFu;
-          uint32_t s = byte ? (byte + kScaleBias) << 4 : 0u;
-          s |= s << 16;
+          const uint32_t s = twice(scales, g) * 16u + (kScaleBias << 4) * 0x10001u;
           const uint32_t c = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
           uint32_t r[16];
           word_bf16(code[g].x, s, c, r);
@@ -426,9 +477,7 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
         unsigned char* const dst = s_v + tok * 128;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const uint32_t byte = (scales >> (8 * g)) & 0xFFu;
-          uint32_t s = byte << 7;
-          s |= s << 16;
+          const uint32_t s = twice(scales, g) << 7;
           const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
           const uint32_t c = fma_f16x2(s, 0xE408E408u, 0u), c16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
           const uint32_t w[4] = {code[g].x, code[g].y, code[g].z, code[g].w};
@@ -448,13 +497,13 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
       dead |= !mbar_wait_for(&s_bar_s, ph_s, nullptr);
       ph_s ^= 1u;
       fence_after();
-      const int64_t lo = (int64_t)begin + (int64_t)k * kTile;
-      const bool masked = lo + kTile - 1 > (int64_t)len + i0 || (a.s.window > 0 && lo < (int64_t)len + i1 + 1 - a.s.window);
+      const bool masked = lo + kTile - 1 > (uint32_t)(len + i0) || (uint32_t)(len + i1) - lo >= win;
       uint32_t w16[kColsHalf / 2];
       float top = -INFINITY;
       unsigned char* const dst_p = s_p + tok * 128;
+      const int place = (wg ^ (tok & 7)) << 4;  // of a block of eight columns in its 128 bytes: block 2 cb + wg
       auto weights = [&](int cb, bool judge) {
-        const int j0 = wg * n16 * 8 + cb * 8;
+        const int j0 = cb * 16 + wg * 8;
         float x[8];
         tmem_ld8(tmem + my_lanes + kTmemS + j0, x);
         const float4 n0 = *reinterpret_cast<const float4*>(&s_nm[j0]), n1 = *reinterpret_cast<const float4*>(&s_nm[j0 + 4]);
@@ -466,7 +515,7 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
           const int32_t last[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if ((uint32_t)last[j] - (uint32_t)pos >= win) x[j] = -INFINITY;
+            if ((uint32_t)last[j] - pos >= win) x[j] = -INFINITY;
         }
         if (judge) {
 #pragma unroll
@@ -474,25 +523,27 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) w16[cb * 4 + j] = pack_f16x2(ex2(x[2 * j]), ex2(x[2 * j + 1]));
-        *reinterpret_cast<uint4*>(dst_p + (j0 >> 6) * (kTile * 128) + ((((j0 >> 3) & 7) ^ (tok & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(dst_p + (cb >> 2) * (kTile * 128) + (place ^ ((2 * cb & 7) << 4))) =
             make_uint4(w16[cb * 4], w16[cb * 4 + 1], w16[cb * 4 + 2], w16[cb * 4 + 3]);
       };
+      if (!first) {  // no reference yet on the first one
 #pragma unroll
-      for (int cb = 0; cb < kColsHalf / 8; ++cb)
-        if (cb < n16) weights(cb, true);
+        for (int cb = 0; cb < kColsHalf / 8; ++cb)
+          if (cb < n16) weights(cb, true);
+      }
       if (dead) s_dead = 1;
       fence_async_smem();
       fence_before();
-      if (__syncthreads_or(top > kTop)) {
+      if (__syncthreads_or(top > kTop || first)) {
         // slow path: the columns' maxima over the tile, new references, O and the sums rescaled
         fence_after();
         for (int cb = 0; cb < n16; ++cb) {
-          const int j0 = wg * n16 * 8 + cb * 8;
+          const int j0 = cb * 16 + wg * 8;
           float x[8];
           tmem_ld8(tmem + my_lanes + kTmemS + j0, x);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float y = masked && (uint32_t)s_last[j0 + j] - (uint32_t)pos >= win ? -INFINITY : x[j] * a.c;
+            const float y = masked && (uint32_t)s_last[j0 + j] - pos >= win ? -INFINITY : x[j] * a.c;
             const float m = warp_max(y);
             if (lane == 0) s_red[warp & 3][j0 + j] = m;
           }
@@ -510,7 +561,7 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
 #pragma unroll
         for (int cb = 0; cb < kColsHalf / 8; ++cb)
           if (cb < n16) {
-            const int j0 = wg * n16 * 8 + cb * 8;
+            const int j0 = cb * 16 + wg * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) l[cb * 8 + j] *= s_f[j0 + j];
             if (!first) {
@@ -539,8 +590,11 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
         mma_commit(&s_bar_o);
       }
 #pragma unroll
-      for (int j = 0; j < kColsHalf / 2; ++j)
-        if (j < n16 * 4) add_halves(w16[j], l[2 * j], l[2 * j + 1]);
+      for (int cb = 0; cb < kColsHalf / 8; ++cb)
+        if (cb < n16) {
+#pragma unroll
+          for (int j = cb * 4; j < cb * 4 + 4; ++j) add_halves(w16[j], l[2 * j], l[2 * j + 1]);
+        }
     }
     if (dead) break;
 
@@ -553,38 +607,36 @@ __global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a
 #pragma unroll
     for (int cb = 0; cb < kColsHalf / 8; ++cb)
       if (cb < n16) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float x = l[cb * 8 + j];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-          if (lane == 0) s_red[warp & 3][wg * n16 * 8 + cb * 8 + j] = x;
-        }
+        const float x = warp_sum8(&l[cb * 8], lane);
+        if (lane < 8) s_red[warp & 3][cb * 16 + wg * 8 + lane] = x;
       }
     if (dead) s_dead = 1;
     __syncthreads();
     dead = s_dead != 0;
     if (dead) break;
     Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + slot;
-    if (!whole && tid < kCols) {
-      part->m[tid] = -s_nm[tid];
-      part->l[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+    if (tid < kCols) {
+      const float sum = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+      s_f[tid] = __fdividef(1.0f, sum);
+      if (!whole) {
+        part->m[tid] = -s_nm[tid];
+        part->l[tid] = sum;
+      }
     }
+    __syncthreads();
+    __nv_bfloat16* const out0 = a.out + ((row0 + i0) * a.q_heads + (int64_t)head_now * share) * D + tok;
     for (int cb = 0; cb < n16; ++cb) {
-      const int j0 = wg * n16 * 8 + cb * 8;
+      const int j0 = cb * 16 + wg * 8;
       float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       if (k1 > k0) tmem_ld8(tmem + my_lanes + kTmemO + j0, o);
       if (tok < D) {
+        if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (!whole) {
-            part->o[j0 + j][tok] = o[j];
-          } else if (j0 + j < n) {
-            const float sum = (s_red[0][j0 + j] + s_red[1][j0 + j]) + (s_red[2][j0 + j] + s_red[3][j0 + j]);
-            const int64_t col = c0 + j0 + j;
-            a.out[((row0 + col / share) * a.q_heads + (int64_t)kvh * share + col % share) * D + tok] =
-                __float2bfloat16_rn(__fdividef(o[j], sum));
-          }
+          for (int j = 0; j < 8; ++j) part->o[j0 + j][tok] = o[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j0 + j < n) out0[(int64_t)s_at[j0 + j] * D] = __float2bfloat16_rn(o[j] * s_f[j0 + j]);
         }
       }
     }
@@ -620,8 +672,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   const Part<D>* const parts = reinterpret_cast<const Part<D>*>(a.parts);
   for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); at < rows * a.q_heads;
        at += (int64_t)gridDim.x * (kJoinThreads / 32)) {
-    const int64_t row = at / a.q_heads;
-    const int32_t h = (int32_t)(at % a.q_heads);
+    const int64_t row = quotient(at, a.q_heads);
+    const int32_t h = (int32_t)(at - row * a.q_heads);
     const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
     const int32_t off = a.s.offsets[b], last = a.s.offsets[b + 1] - off;
     const int64_t i = row - off - b;
@@ -630,10 +682,12 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 #pragma unroll
     for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
     if (!failed && a.units[b] > 0 && i >= 0 && i <= last) {
-      const SessionPlan pl = session_plan(a.s.start[b], last + 1, share, a.s.window);
-      const int64_t col = i * share + h % share;
-      const int64_t first = a.prefix[b] + ((int64_t)(h / share) * pl.chunks + col / pl.w) * pl.tiles;
-      const int32_t j = (int32_t)(col % pl.w);
+      const SessionPlan pl = a.plans[b];
+      const int32_t kvh = h / share;
+      const int64_t col = i * share + (h - kvh * share);
+      const int64_t part = quotient(col, pl.w);
+      const int64_t first = a.prefix[b] + ((int64_t)kvh * pl.chunks + part) * pl.tiles;
+      const int32_t j = (int32_t)(col - part * pl.w);
       const int32_t c_lo = line.cta_of(first), c_hi = line.cta_of(first + pl.tiles - 1);
       if (c_lo == c_hi) continue;
       float m = -INFINITY;
@@ -704,7 +758,7 @@ extern "C" size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, i
                                               int32_t kv_heads, int32_t head_dim) {
   if (B < 0 || total_drafts < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
-  return kHeader + round256(((size_t)B * 2 + 1) * sizeof(int64_t)) +
+  return kHeader + round256((size_t)B * sizeof(SessionPlan)) + round256(((size_t)B * 2 + 1) * sizeof(int64_t)) +
          (size_t)kMaxCtas * 2 * (head_dim == 128 ? sizeof(Part<128>) : sizeof(Part<64>));
 }
 
@@ -718,7 +772,7 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   if (rc != SDCP_OK) return rc;
   const size_t need = sdcp_attend_workspace_bytes(B, total_drafts, q_heads, cache->kv_heads, cache->head_dim);
   if (need == 0 || window < 0 || !isfinite(scale)) return SDCP_E_INVALID;
-  if (total_drafts + B > (int64_t)INT32_MAX / 2) return SDCP_E_TOO_LARGE;
+  if (total_drafts + B > (int64_t)INT32_MAX / 2 || q_heads > (1 << 20)) return SDCP_E_TOO_LARGE;
   if (B == 0) return SDCP_OK;
   const int32_t D = cache->head_dim;
   if (!m_offsets || !kv_len || !q || !out || !status) return SDCP_E_INVALID;
@@ -728,11 +782,14 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   DeviceInfo di;
   if (!device_info(&di) || !attend_ready()) return SDCP_E_DEVICE;
   char* w = static_cast<char*>(workspace);
-  int64_t* lines = reinterpret_cast<int64_t*>(w + kHeader);
+  char* const plans = w + kHeader;
+  char* const lines = plans + round256((size_t)B * sizeof(SessionPlan));
+  int64_t* const units = reinterpret_cast<int64_t*>(lines);
   const KvSessions s{B, m_offsets, total_drafts, 1, kv_len, window, INT32_MAX};
   const AttendArgs a{kv, s, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
-                     static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), lines, lines + B,
-                     reinterpret_cast<float*>(w + kHeader + round256(((size_t)B * 2 + 1) * sizeof(int64_t))),
+                     static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), units,
+                     reinterpret_cast<SessionPlan*>(plans), units + B,
+                     reinterpret_cast<float*>(lines + round256(((size_t)B * 2 + 1) * sizeof(int64_t))),
                      min(2 * di.sms, kMaxCtas)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? launch_attend<128>(a, di.sms, st) : launch_attend<64>(a, di.sms, st);
