@@ -20,31 +20,40 @@
 // the queries are), values and weights binary16: a weight keeps 11 bits.
 //
 // The reference m only has to keep the weights in range: weights are 2^7 at m, and m moves only
-// when a weight would pass 2^15 (binary16 ends below 2^16), which after a head's first tile is rare.
-// The weights of a tile are therefore computed at once with the m at hand; a block-wide vote, taken
-// at the barrier that the tile needs anyway, sends it through the slow path that finds the tile's
-// column maxima, rescales O and repeats the weights.  The sum of weights is of the rounded ones, in
-// binary32, a partial sum per thread and column.
+// when a weight would pass 2^15 (binary16 ends below 2^16), which after an item's first tile is rare.
+// The weights of a tile are therefore computed at once with the m at hand; a vote of the threads that
+// compute them sends the tile through the slow path that finds its column maxima, rescales O and
+// repeats the weights.  The sum of weights is of the rounded ones, in binary32, a partial sum per
+// thread and column.
+//
+// What bounds it is the instructions of the turning and of the weights, so the steps run side by
+// side in warps of their own, two tiles deep: four warps turn keys, four turn values (each copies its
+// tokens' codes to shared memory two tiles ahead, across items), eight compute weights, one issues S,
+// one O, one brings the next items' queries and one plans the items.  They meet on mbarriers only.
+// Each role's loop is kept short: with five different streams of instructions on a scheduler, long
+// unrolled ones starved for instructions (the turning loops unrolled over both buffers and all groups
+// made the kernel 1.5 times slower).
 //
 // Work: the tiles of all (session, cached head, block of columns) items in one line, cut evenly
-// over the CTAs (two an SM), whatever the lengths.  A CTA's first and last items may be parts; their
+// over the CTAs (one an SM), whatever the lengths.  A CTA's first and last items may be parts; their
 // O, m and sum go to the workspace, and a second kernel joins them in the order of the line.
 #include <climits>
 #include <math.h>
 #include <mutex>
+#include <type_traits>
 
 #include "sdcp_kv.cuh"
 
 namespace sdcp {
 namespace {
 
-constexpr int kThreads2 = 256;    // two groups of 128: keys and values; half of the columns each
-constexpr int kTile = 128;        // tokens of a tile
-constexpr int kCols = 96;         // columns of an item
+constexpr int kAttendThreads = 640;  // warps 0-3 keys, 4-7 values, 8-15 weights, 16 S, 17 O, 18 queries, 19 plan
+constexpr int kTile = 128;           // tokens of a tile
+constexpr int kCols = 96;            // columns of an item
 constexpr int kColsHalf = kCols / 2;
-constexpr int kMaxCtas = 320;     // CTAs a launch has at most (sizes the workspace)
-constexpr int kTmemCols = 256;    // tensor memory of a CTA: keys 0..63, S from 64, O from 160
-constexpr uint32_t kTmemS = 64, kTmemO = 160;
+constexpr int kMaxCtas = 160;        // CTAs a launch has at most (sizes the workspace)
+constexpr int kTmemCols = 512;       // tensor memory: keys of two tiles, S of two tiles, O
+constexpr uint32_t kTmemK = 0, kTmemS = 128, kTmemO = 320;
 constexpr float kLift = 7.0f;     // a weight is 2^kLift at its reference
 constexpr float kTop = 15.0f;     // and 2^kTop at most
 
@@ -140,8 +149,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t at, float (&r)[8]) {
                : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
                : "r"(at)
                : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -211,6 +220,9 @@ __device__ __forceinline__ float warp_sum8(const float* x, int lane) {
   return s;
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 // Byte g of w in both halves of a word.
 __device__ __forceinline__ uint32_t twice(uint32_t w, int g) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * g); }
 
@@ -234,8 +246,184 @@ template <int D> struct AttendSmem {
   static constexpr int kQ = kAtoms * kCols * 128;       // queries: [atom][column][128 bytes]
   static constexpr int kV = kAtoms * kTile * 128;       // values: [atom][token][128 bytes]
   static constexpr int kP = 2 * kTile * 128;            // weights: [atom of 64 columns][token][128 bytes]
-  static constexpr size_t kBytes = (size_t)kQ + kV + kP + 1024;  // and the alignment to 1024
+  static constexpr int kC = kTile * (D / 2 + 4);         // codes of a tile's keys or values, and a word of scales a token
+  static constexpr size_t kBytes = 2 * (size_t)(kQ + kV + kP + 2 * kC) + 1024;  // two of each, and the alignment to 1024
 };
+
+// One step of a CTA's way along the line: an item, or the part of it that is the CTA's.
+struct Item {
+  int32_t b, off, len, kvh;
+  int32_t n, i0, g0;            // columns, and the row and head of the first
+  uint32_t lowest, begin, end;  // positions: first read, first of tile 0, one past the last
+  int32_t k0, k1;               // tiles
+  int32_t slot;                 // of the parts
+  int32_t whole;                // all of the item's tiles are here
+};
+// The way itself, walked by the planning warp, which publishes the items in a ring: the divisions
+// stay out of the other warps' registers and off their way.
+struct Walk {
+  int64_t t, t_end, t_first;
+  SessionPlan pl;
+  int32_t b, off, rows, len, kvh, chunk, unit0;
+  __device__ __forceinline__ void load(const AttendArgs& a) {
+    pl = a.plans[b];
+    off = a.s.offsets[b];
+    rows = a.s.offsets[b + 1] - off + 1;
+    len = a.s.start[b];
+  }
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Line& line, int32_t session, int64_t base) {
+    t = t_first = line.first((int32_t)blockIdx.x);
+    t_end = line.first((int32_t)blockIdx.x + 1);
+    b = session;
+    load(a);
+    const int64_t item = quotient(t - base, pl.tiles);
+    unit0 = (int32_t)(t - base - item * pl.tiles);
+    kvh = (int32_t)quotient(item, pl.chunks);
+    chunk = (int32_t)(item - (int64_t)kvh * pl.chunks);
+  }
+  // the next item; false at the end of the CTA's part
+  __device__ __forceinline__ bool next(const AttendArgs& a, Item& it) {
+    if (t >= t_end) return false;
+    if (kvh == a.kv.heads) {  // the next session that has work
+      do ++b;
+      while (a.units[b] == 0);
+      load(a);
+      kvh = 0;
+    }
+    const int32_t share = a.q_heads / a.kv.heads;
+    const int32_t units = (int32_t)min((int64_t)(pl.tiles - unit0), t_end - t);
+    const int64_t c0 = (int64_t)chunk * pl.w;
+    it.b = b, it.off = off, it.len = len, it.kvh = kvh;
+    it.n = (int32_t)min((int64_t)pl.w, (int64_t)rows * share - c0);
+    it.i0 = (int32_t)quotient(c0, share);
+    it.g0 = (int32_t)(c0 - (int64_t)it.i0 * share);
+    const int32_t i1 = it.i0 + (it.g0 + it.n - 1) / share;
+    it.end = (uint32_t)(len + i1) + 1u;
+    it.lowest = a.s.window > 0 ? (uint32_t)max((int64_t)0, (int64_t)len + it.i0 + 1 - a.s.window) : 0u;
+    it.begin = it.lowest & ~31u;
+    const int32_t real = (int32_t)((it.end - it.begin + kTile - 1) / kTile);
+    it.k0 = max(unit0 - kItemUnits, 0);
+    it.k1 = min(max(unit0 + units - kItemUnits, 0), real);
+    it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
+    it.whole = units == pl.tiles;
+    t += units;
+    unit0 = 0;
+    if (++chunk == pl.chunks) {
+      chunk = 0;
+      ++kvh;
+    }
+    return true;
+  }
+};
+constexpr int kItems = 4;                          // of the ring
+constexpr int kItemReaders = 4 + 4 + 8 + 2 + 1;    // warps that read an item
+
+// The barriers and small arrays of a CTA.  Tile i of a CTA uses buffer i & 1 of keys, S, values and
+// weights, item j buffer j & 1 of the queries and column arrays; a buffer's n-th use has parity n & 1.
+struct AttendShared {
+  __align__(16) float nm[2][kCols];      // kLift - m: what a scaled score is shifted by
+  __align__(16) int32_t last[2][kCols];  // last position of a column
+  int32_t at[2][kCols];                  // a column's place among the output's heads
+  __align__(16) float f[kCols];          // factors of a rescale; reciprocal sums
+  float red[4][kCols];
+  uint64_t k_full[2], s_full[2], s_free[2], v_full[2], p_full[2], pv_done[2], q_full[2], q_free[2], o_free, drained[2];
+  long long scan[kAttendThreads / 32];
+  long long base;
+  int32_t session;
+  uint32_t tmem;
+  int dead;
+  Item item[kItems];          // an item without tiles ends them
+  uint64_t item_full[kItems], item_free[kItems];
+};
+// Item j of the CTA, for a whole warp: false at the end, or when a wait gave up.
+__device__ __forceinline__ bool item_at(AttendShared& sh, uint32_t j) {
+  if (!mbar_wait_for(&sh.item_full[j % kItems], (j / kItems) & 1u, &sh.dead)) {
+    sh.dead = 1;
+    return false;
+  }
+  const Item& it = sh.item[j % kItems];
+  return it.k0 < it.k1;
+}
+// The warp is done with item j.
+__device__ __forceinline__ void item_done(AttendShared& sh, uint32_t j) {
+  __syncwarp();
+  if ((threadIdx.x & 31u) == 0) mbar_arrive(&sh.item_free[j % kItems]);
+}
+
+// The tokens of one thread of a turning group, tile after tile across the items: the page of the
+// next tile's token is asked for when the codes of the one before are.  The codes go to the thread's
+// own places in shared memory: [group][token][16 bytes], then [token][a word with
+// its scales].
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int D> struct TokenStream {
+  static constexpr int kGroups = D / kKvGroup;
+  const AttendArgs& a;
+  AttendShared& sh;
+  bool live, here;
+  int32_t which, left, page;  // left: tiles of the item after the one at hand
+  uint32_t j, pos, lowest, end;
+  const uint8_t* head;
+  const int32_t* table;
+  __device__ __forceinline__ TokenStream(const AttendArgs& args, AttendShared& shared, int which_) : a(args), sh(shared), which(which_) {
+    left = 0;
+    j = 0;
+    step();
+  }
+  __device__ __forceinline__ void step() {
+    if (left == 0) {
+      live = item_at(sh, j);
+      if (!live) return;
+      const Item& it = sh.item[j % kItems];
+      left = it.k1 - it.k0;
+      lowest = it.lowest;
+      end = it.end;
+      pos = it.begin + (uint32_t)it.k0 * kTile + (threadIdx.x & 127u);
+      head = a.kv.pages + ((int64_t)it.kvh * 2 + which) * a.kv.block;
+      table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
+      item_done(sh, j++);
+    } else {
+      pos += kTile;
+    }
+    --left;
+    here = pos >= lowest && pos < end;
+    if (here) page = table[pos >> a.kv.log_page];
+  }
+  // starts the copy of the tile at hand (a token past the ends keeps old codes, with scale byte zero:
+  // finite numbers, whose weight is zero); then on to the next.  One group of copies a call.
+  __device__ __forceinline__ bool take(uint32_t codes, uint32_t scales) {
+    const bool had = live;
+    if (had) {
+      if (here) {
+        const uint32_t slot = pos & ((1u << a.kv.log_page) - 1u);
+        const uint8_t* blk = head + (int64_t)page * a.kv.page;
+        const uint8_t* at = blk + slot * 16u;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          copy_async16(codes + (uint32_t)g * (kTile * 16), at);
+          at += 16u << a.kv.log_page;
+        }
+        // four scale bytes of a token, or two each of a pair of tokens
+        copy_async4(scales, blk + (D / 2 << a.kv.log_page) + ((slot * kGroups) & ~3u));
+      } else {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(scales), "r"(0u) : "memory");
+      }
+      step();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return had;
+  }
+};
+
+template <int kRegs> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+// Registers a thread: 640 x 96 at launch; 256 x 80 (turning), 256 x 128 (weights) and 128 x 56 (the
+// rest) are 60416 of those 61440.
+constexpr int kTurnRegs = 80, kWeightRegs = 128, kRestRegs = 56;
 
 // ---- plan: statuses and tiles of the sessions ---------------------------------------------
 __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const AttendArgs a) {
@@ -256,401 +444,504 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
 }
 
 // ---- the products -------------------------------------------------------------------------
-template <int D>
-__global__ void __launch_bounds__(kThreads2, 2) attend_kernel(const AttendArgs a) {
-  using Sm = AttendSmem<D>;
+// Keys (kKeys) to tensor memory as bfloat16, or values to shared memory as binary16.
+template <int D, bool kKeys>
+__device__ __forceinline__ void turn_tokens(const AttendArgs& a, AttendShared& sh, unsigned char* s_v, unsigned char* s_c, uint32_t tmem) {
   constexpr int kGroups = D / kKvGroup;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* const s_q = sm;
-  unsigned char* const s_v = sm + Sm::kQ;
-  unsigned char* const s_p = s_v + Sm::kV;
-  __shared__ __align__(16) float s_nm[kCols];    // kLift - m: what a scaled score is shifted by
-  __shared__ __align__(16) float s_f[kCols];     // factors of a rescale
-  __shared__ __align__(16) int32_t s_last[kCols];  // last position of a column
-  __shared__ int32_t s_row[kCols], s_at[kCols];    // a column's row, and its place among the output's heads
-  __shared__ float s_red[4][kCols];
-  __shared__ uint64_t s_bar_s, s_bar_o;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_dead;
-  __shared__ long long s_scan[kThreads2 / 32];
-  __shared__ long long s_total, s_base;
-  __shared__ int32_t s_session;
-
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wg = tid >> 7, tok = tid & 127;
-  const int32_t cta = (int32_t)blockIdx.x;
-  wait_for_previous();
-
-  // this CTA's part of the line: a prefix sum over the sessions, a stretch of them per thread
-  {
-    const int32_t per = (a.s.B + kThreads2 - 1) / kThreads2;
-    const int32_t b0 = min(tid * per, a.s.B), b1 = min(b0 + per, a.s.B);
-    long long mine = 0;
-    for (int32_t b = b0; b < b1; ++b) mine += a.units[b];
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += y;
+  using Sm = AttendSmem<D>;
+  const int lane = (int)(threadIdx.x & 31u), tok = (int)(threadIdx.x & 127u);
+  TokenStream<D> stream(a, sh, kKeys ? 0 : 1);
+  const uint32_t codes = smem_u32(s_c) + (uint32_t)((kKeys ? 0 : 2) * Sm::kC + tok * 16);
+  const uint32_t scales = smem_u32(s_c) + (uint32_t)((kKeys ? 0 : 2) * Sm::kC + kGroups * kTile * 16 + tok * 4);
+  uint32_t lives = stream.take(codes, scales) ? 1u : 0u;
+  lives |= stream.take(codes + Sm::kC, scales + Sm::kC) ? 2u : 0u;
+  const uint32_t tmem_dst = tmem + kTmemK + ((uint32_t)((threadIdx.x >> 5) & 3u) << 21);  // 32 lanes, in bits 16 up
+  const uint32_t smem_dst = smem_u32(s_v) + (uint32_t)tok * 128u + ((uint32_t)(tok & 7) << 4);
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t e = i & 1u;
+    if (!((lives >> e) & 1u)) return;
+    // the buffer's previous use: the product that read it is done
+    if (i >= 2 && !mbar_wait_for(kKeys ? &sh.s_full[e] : &sh.pv_done[e], ((i >> 1) - 1u) & 1u, &sh.dead)) {
+      sh.dead = 1;
+      return;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    if (tid == 0) s_dead = 0;
-    __syncthreads();
-    long long before = 0, all = 0;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    uint32_t sb;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sb) : "r"(scales + e * Sm::kC) : "memory");
+    if (D == 64) sb >>= (tok & 1) * 16;  // tiles start at even tokens
+    if (kKeys) fence_after();
+#pragma unroll 1
+    for (int g = 0; g < kGroups; ++g, sb >>= 8) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(codes + e * Sm::kC + (uint32_t)g * (kTile * 16))
+                   : "memory");
+      if (kKeys) {
+        const uint32_t s = twice(sb, 0) * 16u + (kScaleBias << 4) * 0x10001u;
+        const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
+        uint32_t r[16];
 #pragma unroll
-    for (int w = 0; w < kThreads2 / 32; ++w) {
-      if (w < warp) before += s_scan[w];
-      all += s_scan[w];
-    }
-    const long long start = before + incl - mine;
-    const Line line(all, a.ctas);
-    if (cta == 0) {
-      long long at = start;
-      for (int32_t b = b0; b < b1; ++b) {
-        a.prefix[b] = at;
-        at += a.units[b];
+        for (int x = 0; x < 4; ++x) word_bf16(w[x], s, m, r + 4 * x);
+        tmem_st16(tmem_dst + e * 64u + (uint32_t)g * 16u, r);
+      } else {
+        const uint32_t s = twice(sb, 0) << 7;
+        const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
+        const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
+        const uint32_t dst = (smem_dst ^ ((uint32_t)(g & 1) << 6)) + e * Sm::kV + (uint32_t)(g >> 1) * (kTile * 128);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t r[4];
+          word_f16(w[x], s, m, s16, m16, r);
+          st_shared16(dst ^ (uint32_t)(x << 4), r[0], r[1], r[2], r[3]);
+        }
       }
-      if (tid == 0) a.prefix[a.s.B] = all;
     }
-    if (tid == 0) s_total = all;
-    if (cta >= line.ctas || all == 0) return;
-    const int64_t mine0 = line.first(cta);
-    if (mine0 >= start && mine0 < start + mine) {
-      long long at = start;
-      int32_t b = b0;
-      while (mine0 >= at + a.units[b]) at += a.units[b++];
-      s_session = b;
-      s_base = at;
+    if (kKeys) {
+      tmem_wait_st();
+      fence_before();
+    } else {
+      fence_async_smem();
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(kKeys ? &sh.k_full[e] : &sh.v_full[e]);
+    lives = (lives & ~(1u << e)) | (stream.take(codes + e * Sm::kC, scales + e * Sm::kC) ? 1u << e : 0u);
   }
-  if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
-  if (tid == 0) {
-    mbar_init(&s_bar_s, 1);
-    mbar_init(&s_bar_o, 1);
-    fence_barrier_init();
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = s_tmem;
-  const uint32_t my_lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes of tensor memory, in bits 16 up
-  const Line line(s_total, a.ctas);
-  int64_t t = line.first(cta);
-  const int64_t t_end = line.first(cta + 1);
-  int32_t b = s_session;
-  int64_t base = s_base;
-  const int32_t share = a.q_heads / a.kv.heads;
+}
+
+// The weights of the tiles, and an item's end: O and the sums to the output or to a part.
+template <int D>
+__device__ __forceinline__ void weigh(const AttendArgs& a, AttendShared& sh, unsigned char* s_p, uint32_t tmem) {
+  const int tid = (int)threadIdx.x - 256, lane = tid & 31, warp = tid >> 5;
+  const int wg = tid >> 7, tok = tid & 127;
+  const uint32_t my_lanes = (uint32_t)(warp & 3) << 21;
   const uint32_t win = a.s.window > 0 ? (uint32_t)a.s.window : 0x80000000u;
-  uint32_t ph_s = 0, ph_o = 0;  // phases of the two barriers
+  // block 2 cb + wg of eight columns, swizzled in the token's 128 bytes
+  const uint32_t dst_p = smem_u32(s_p) + (uint32_t)tok * 128u + ((uint32_t)(wg ^ (tok & 7)) << 4);
+  auto meet = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  auto any = [](bool p) {
+    uint32_t r;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }" : "=r"(r) : "r"((uint32_t)p) : "memory");
+    return r != 0;
+  };
+  uint32_t i = 0, j = 0;  // tiles and items so far
   bool dead = false;
-
-  // where the line enters its first item; from there on it walks
-  SessionPlan pl = a.plans[b];
-  int64_t item = quotient(t - base, pl.tiles);
-  int32_t unit0 = (int32_t)(t - base - item * pl.tiles);
-  int32_t kvh = (int32_t)quotient(item, pl.chunks), chunk = (int32_t)(item - (int64_t)kvh * pl.chunks);
-  int32_t off = a.s.offsets[b], rows = a.s.offsets[b + 1] - off + 1, len = a.s.start[b];
-
-  while (t < t_end && !dead) {
-    if (kvh == a.kv.heads) {  // the next session that has work
-      do ++b;
-      while (a.units[b] == 0);
-      pl = a.plans[b];
-      off = a.s.offsets[b], rows = a.s.offsets[b + 1] - off + 1, len = a.s.start[b];
-      kvh = 0;
-    }
-    const int32_t units = (int32_t)min((int64_t)(pl.tiles - unit0), t_end - t);  // of this item, here
-    const bool whole = units == pl.tiles;
-    const int32_t slot = cta * 2 + (t == line.first(cta) ? 0 : 1);
-    const int64_t c0 = (int64_t)chunk * pl.w;
-    const int32_t n = (int32_t)min((int64_t)pl.w, (int64_t)rows * share - c0);
-    const int32_t n16 = (n + 15) / 16;      // blocks of 16 columns; a group of threads has eight of each
-    const int32_t i0 = (int32_t)quotient(c0, share), g0 = (int32_t)(c0 - (int64_t)i0 * share);
-    const int32_t i1 = i0 + (g0 + n - 1) / share;
-    const uint32_t end = (uint32_t)(len + i1) + 1u;  // one past the last position any column sees
-    const uint32_t lowest = a.s.window > 0 ? (uint32_t)max((int64_t)0, (int64_t)len + i0 + 1 - a.s.window) : 0u;
-    const uint32_t begin = lowest & ~31u;            // the first tile's start; tokens below `lowest` are not read
-    const int32_t real = (int32_t)((end - begin + kTile - 1) / kTile);  // tiles that hold something
-    const int32_t k0 = max(unit0 - kItemUnits, 0), k1 = min(max(unit0 + units - kItemUnits, 0), real);
-    const int64_t row0 = (int64_t)off + b;
-    const int32_t head_now = kvh;
-    t += units;
-    unit0 = 0;
-    if (++chunk == pl.chunks) {
-      chunk = 0;
-      ++kvh;
-    }
-
-    // queries of the columns, zero past them, and the columns' state
-    __syncthreads();
-    if (tid < kCols) {
-      const int32_t r = (g0 + tid) / share;
-      s_row[tid] = r;
-      s_at[tid] = r * a.q_heads + g0 + tid - r * share;
-      s_nm[tid] = tid < n ? INFINITY : kLift;
-      s_last[tid] = tid < n ? len + i0 + r : INT_MAX;
-    }
-    __syncthreads();
-    const __nv_bfloat16* const q0 = a.q + (row0 + i0) * a.q_stride + (int64_t)head_now * share * D;
-    for (int k = tid; k < n16 * 16 * (D / 8); k += kThreads2) {
-      const int j = k / (D / 8), ch = k % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (j < n) v = *reinterpret_cast<const uint4*>(q0 + s_row[j] * a.q_stride + (s_at[j] - s_row[j] * a.q_heads) * D + ch * 8);
-      *reinterpret_cast<uint4*>(s_q + (ch / 8) * (kCols * 128) + j * 128 + (((ch & 7) ^ (j & 7)) << 4)) = v;
-    }
-    fence_async_smem();
+  for (;; ++j) {
+    const bool more = item_at(sh, j);
+    if (any(!more)) return;
+    const Item& it = sh.item[j % kItems];
+    Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
+    const int32_t n16 = (it.n + 15) / 16;  // blocks of 16 columns; a group of threads has eight of each
+    const uint32_t qb = j & 1u;
+    float* const nm_of = sh.nm[qb];
+    const int32_t* const last_of = sh.last[qb];
+    dead |= !mbar_wait_for(&sh.q_full[qb], (j >> 1) & 1u, &sh.dead);
     float l[kColsHalf];
 #pragma unroll
-    for (int j = 0; j < kColsHalf; ++j) l[j] = 0.0f;
-    const uint32_t idesc_n = (uint32_t)(n16 * 16 / 8) << 17;
-    const uint8_t* const head = a.kv.pages + ((int64_t)head_now * 2 + wg) * a.kv.block;
-    const int32_t* const table = a.kv.page_table + (int64_t)b * a.kv.max_pages;
+    for (int x = 0; x < kColsHalf; ++x) l[x] = 0.0f;
 
-    // a tile ahead: the page of the next token, and its codes
-    uint4 code[kGroups];
-    uint32_t scales = 0;
-    int32_t next_page = 0;
-    const uint32_t group_bytes = 16u << a.kv.log_page, slot_mask = (1u << a.kv.log_page) - 1u;
-    auto find_page = [&](int32_t k) {
-      const uint32_t pos = begin + (uint32_t)k * kTile + (uint32_t)tok;
-      if (k < k1 && pos >= lowest && pos < end) next_page = table[pos >> a.kv.log_page];
-    };
-    auto fetch = [&](int32_t k) {
-      const uint32_t pos = begin + (uint32_t)k * kTile + (uint32_t)tok;
-      scales = 0u;  // a token that is not read becomes finite numbers, whose weight is zero
-      if (k < k1 && pos >= lowest && pos < end) {
-        const uint32_t slot_in = pos & slot_mask;
-        const uint8_t* blk = head + (int64_t)next_page * a.kv.page;
-        const uint8_t* at = blk + slot_in * 16u;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          code[g] = *reinterpret_cast<const uint4*>(at);
-          at += group_bytes;
-        }
-        blk += (D / 2 << a.kv.log_page) + slot_in * (D / kKvGroup);
-        if (D == 128) scales = *reinterpret_cast<const uint32_t*>(blk);
-        else scales = *reinterpret_cast<const uint16_t*>(blk);
-      }
-    };
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) code[g] = make_uint4(0u, 0u, 0u, 0u);
-    find_page(k0);
-    fetch(k0);
-    find_page(k0 + 1);
-    __syncthreads();
-
-    for (int32_t k = k0; k < k1; ++k) {
-      const bool first = k == k0;
-      const uint32_t lo = begin + (uint32_t)k * kTile, pos = lo + (uint32_t)tok;
-      // keys to tensor memory, then S; values to shared memory (once the previous O product has read it)
-      if (wg == 0) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t s = twice(scales, g) * 16u + (kScaleBias << 4) * 0x10001u;
-          const uint32_t c = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
-          uint32_t r[16];
-          word_bf16(code[g].x, s, c, r);
-          word_bf16(code[g].y, s, c, r + 4);
-          word_bf16(code[g].z, s, c, r + 8);
-          word_bf16(code[g].w, s, c, r + 12);
-          tmem_st16(tmem + my_lanes + g * 16, r);
-        }
-        tmem_wait_st();
-        fence_before();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (tid == 0) {
-          fence_after();
-          const uint64_t bq = smem_matrix(s_q, 0, 1024);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            mma_tmem_a(tmem + kTmemS, tmem + x * 8, bq + (uint64_t)(((x / 4) * (kCols * 128) + (x % 4) * 32) >> 4),
-                       kIdescF32 | kIdescBf16 | kIdescM128 | idesc_n, x > 0);
-          mma_commit(&s_bar_s);
-        }
-      }
-      if (!first) {
-        dead |= !mbar_wait_for(&s_bar_o, ph_o, nullptr);
-        ph_o ^= 1u;
-      }
-      if (wg == 1) {
-        unsigned char* const dst = s_v + tok * 128;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t s = twice(scales, g) << 7;
-          const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
-          const uint32_t c = fma_f16x2(s, 0xE408E408u, 0u), c16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
-          const uint32_t w[4] = {code[g].x, code[g].y, code[g].z, code[g].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t r[4];
-            word_f16(w[x], s, c, s16, c16, r);
-            const int ch = (g & 1) * 4 + x;
-            *reinterpret_cast<uint4*>(dst + (g >> 1) * (kTile * 128) + ((ch ^ (tok & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
-          }
-        }
-      }
-      fetch(k + 1);
-      find_page(k + 2);
-
-      // weights of this group's columns with the references at hand
-      dead |= !mbar_wait_for(&s_bar_s, ph_s, nullptr);
-      ph_s ^= 1u;
+    bool first = true;
+    uint32_t lo = it.begin + (uint32_t)it.k0 * kTile;
+    const uint32_t low_last = (uint32_t)(it.len + it.i0), high_last = it.end - 1u;  // of the columns
+    for (int32_t left = it.k1 - it.k0; left > 0; --left, ++i, lo += kTile, first = false) {
+      const uint32_t buf = i & 1u, pos = lo + (uint32_t)tok;
+      const bool masked = lo + kTile - 1 > low_last || high_last - lo >= win;
+      dead |= !mbar_wait_for(&sh.s_full[buf], (i >> 1) & 1u, &sh.dead);
+      if (i >= 2) dead |= !mbar_wait_for(&sh.pv_done[buf], ((i >> 1) - 1u) & 1u, &sh.dead);
       fence_after();
-      const bool masked = lo + kTile - 1 > (uint32_t)(len + i0) || (uint32_t)(len + i1) - lo >= win;
+      const uint32_t s_at = tmem + my_lanes + kTmemS + buf * kCols + (uint32_t)wg * 8u;
+      const uint32_t p_at = dst_p + buf * AttendSmem<D>::kP;
       uint32_t w16[kColsHalf / 2];
       float top = -INFINITY;
-      unsigned char* const dst_p = s_p + tok * 128;
-      const int place = (wg ^ (tok & 7)) << 4;  // of a block of eight columns in its 128 bytes: block 2 cb + wg
-      auto weights = [&](int cb, bool judge) {
+      // weights of this group's columns with the references at hand
+      auto block = [&](int cb, float (&x)[8], auto with_mask) {
         const int j0 = cb * 16 + wg * 8;
-        float x[8];
-        tmem_ld8(tmem + my_lanes + kTmemS + j0, x);
-        const float4 n0 = *reinterpret_cast<const float4*>(&s_nm[j0]), n1 = *reinterpret_cast<const float4*>(&s_nm[j0 + 4]);
+        const float4 n0 = *reinterpret_cast<const float4*>(&nm_of[j0]), n1 = *reinterpret_cast<const float4*>(&nm_of[j0 + 4]);
         const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], a.c, nm[j]);
-        if (masked) {
-          const int4 e0 = *reinterpret_cast<const int4*>(&s_last[j0]), e1 = *reinterpret_cast<const int4*>(&s_last[j0 + 4]);
+        for (int y = 0; y < 8; ++y) x[y] = fmaf(x[y], a.c, nm[y]);
+        if (with_mask) {
+          const int4 e0 = *reinterpret_cast<const int4*>(&last_of[j0]), e1 = *reinterpret_cast<const int4*>(&last_of[j0 + 4]);
           const int32_t last[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((uint32_t)last[j] - pos >= win) x[j] = -INFINITY;
-        }
-        if (judge) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
+          for (int y = 0; y < 8; ++y)
+            if ((uint32_t)last[y] - pos >= win) x[y] = -INFINITY;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w16[cb * 4 + j] = pack_f16x2(ex2(x[2 * j]), ex2(x[2 * j + 1]));
-        *reinterpret_cast<uint4*>(dst_p + (cb >> 2) * (kTile * 128) + (place ^ ((2 * cb & 7) << 4))) =
-            make_uint4(w16[cb * 4], w16[cb * 4 + 1], w16[cb * 4 + 2], w16[cb * 4 + 3]);
+        for (int y = 0; y < 8; ++y) top = fmaxf(top, x[y]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) w16[cb * 4 + y] = pack_f16x2(ex2(x[2 * y]), ex2(x[2 * y + 1]));
+        st_shared16((p_at ^ (uint32_t)((2 * cb & 7) << 4)) + (uint32_t)(cb >> 2) * (kTile * 128), w16[cb * 4], w16[cb * 4 + 1],
+                    w16[cb * 4 + 2], w16[cb * 4 + 3]);
+      };
+      auto weights = [&](auto with_mask) {
+#pragma unroll
+        for (int cb = 0; cb < kColsHalf / 8; cb += 2)
+          if (cb < n16) {
+            float x[8], y[8];
+            tmem_ld8(s_at + (uint32_t)cb * 16u, x);
+            if (cb + 1 < n16) tmem_ld8(s_at + (uint32_t)cb * 16u + 16u, y);
+            tmem_wait_ld();
+            block(cb, x, with_mask);
+            if (cb + 1 < n16) block(cb + 1, y, with_mask);
+          }
       };
       if (!first) {  // no reference yet on the first one
-#pragma unroll
-        for (int cb = 0; cb < kColsHalf / 8; ++cb)
-          if (cb < n16) weights(cb, true);
+        if (masked) weights(std::true_type{});
+        else weights(std::false_type{});
       }
-      if (dead) s_dead = 1;
-      fence_async_smem();
-      fence_before();
-      if (__syncthreads_or(top > kTop || first)) {
+      if (any(top > kTop || first || dead)) {
         // slow path: the columns' maxima over the tile, new references, O and the sums rescaled
-        fence_after();
+        if (any(dead)) break;
+        if (!first) {
+          dead |= !mbar_wait_for(&sh.pv_done[buf ^ 1u], ((i - 1u) >> 1) & 1u, &sh.dead);
+          fence_after();
+        }
         for (int cb = 0; cb < n16; ++cb) {
           const int j0 = cb * 16 + wg * 8;
           float x[8];
-          tmem_ld8(tmem + my_lanes + kTmemS + j0, x);
+          tmem_ld8(s_at + (uint32_t)cb * 16u, x);
+          tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = masked && (uint32_t)s_last[j0 + j] - pos >= win ? -INFINITY : x[j] * a.c;
-            const float m = warp_max(y);
-            if (lane == 0) s_red[warp & 3][j0 + j] = m;
+          for (int y = 0; y < 8; ++y) {
+            const float z = masked && (uint32_t)last_of[j0 + y] - pos >= win ? -INFINITY : x[y] * a.c;
+            const float m = warp_max(z);
+            if (lane == 0) sh.red[warp & 3][j0 + y] = m;
           }
         }
-        __syncthreads();
-        if (tid < n) {
-          const float m = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
-          const float nm0 = s_nm[tid], nm1 = fminf(nm0, kLift - m);
-          s_nm[tid] = nm1;
-          s_f[tid] = nm0 == nm1 ? 1.0f : ex2(nm1 - nm0);
-        } else if (tid < kCols) {
-          s_f[tid] = 1.0f;
+        meet();
+        if (tid < kCols) {
+          float f = 1.0f;
+          if (tid < it.n) {
+            const float m = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
+            const float nm0 = nm_of[tid], nm1 = fminf(nm0, kLift - m);
+            nm_of[tid] = nm1;
+            f = nm0 == nm1 ? 1.0f : ex2(nm1 - nm0);
+          }
+          sh.f[tid] = f;
         }
-        __syncthreads();
+        meet();
 #pragma unroll
         for (int cb = 0; cb < kColsHalf / 8; ++cb)
           if (cb < n16) {
             const int j0 = cb * 16 + wg * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) l[cb * 8 + j] *= s_f[j0 + j];
+            for (int y = 0; y < 8; ++y) l[cb * 8 + y] *= sh.f[j0 + y];
             if (!first) {
               float o[8];
-              tmem_ld8(tmem + my_lanes + kTmemO + j0, o);
+              const uint32_t o_at = tmem + my_lanes + kTmemO + (uint32_t)j0;
+              tmem_ld8(o_at, o);
+              tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] *= s_f[j0 + j];
-              tmem_st8(tmem + my_lanes + kTmemO + j0, o);
+              for (int y = 0; y < 8; ++y) o[y] *= sh.f[j0 + y];
+              tmem_st8(o_at, o);
             }
-            weights(cb, false);
           }
+        weights(std::true_type{});
         tmem_wait_st();
-        fence_async_smem();
-        fence_before();
-        __syncthreads();
       }
-      dead = s_dead != 0;
-      if (dead) break;
-      if (tid == 128) {
-        fence_after();
-        const uint64_t av = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024), bp = smem_matrix(s_p, kTile * 128, 1024);
-#pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)
-          mma_smem_a(tmem + kTmemO, av + (uint64_t)(x * 2048 >> 4), bp + (uint64_t)(x * 2048 >> 4),
-                     kIdescF32 | kIdescTransposeBoth | kIdescM128 | idesc_n, !first || x > 0);
-        mma_commit(&s_bar_o);
+      fence_async_smem();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.s_free[buf]);
+        mbar_arrive(&sh.p_full[buf]);
       }
 #pragma unroll
       for (int cb = 0; cb < kColsHalf / 8; ++cb)
         if (cb < n16) {
 #pragma unroll
-          for (int j = cb * 4; j < cb * 4 + 4; ++j) add_halves(w16[j], l[2 * j], l[2 * j + 1]);
+          for (int x = cb * 4; x < cb * 4 + 4; ++x) add_halves(w16[x], l[2 * x], l[2 * x + 1]);
         }
     }
-    if (dead) break;
-
-    // O, references and sums of the item's columns
-    if (k1 > k0) {
-      dead |= !mbar_wait_for(&s_bar_o, ph_o, nullptr);
-      ph_o ^= 1u;
-      fence_after();
+    if (!dead) dead |= !mbar_wait_for(&sh.pv_done[(i - 1u) & 1u], ((i - 1u) >> 1) & 1u, &sh.dead);
+    if (any(dead)) {
+      sh.dead = 1;
+      return;
     }
+    // O, references and sums of the item's columns
+    fence_after();
 #pragma unroll
     for (int cb = 0; cb < kColsHalf / 8; ++cb)
       if (cb < n16) {
         const float x = warp_sum8(&l[cb * 8], lane);
-        if (lane < 8) s_red[warp & 3][cb * 16 + wg * 8 + lane] = x;
+        if (lane < 8) sh.red[warp & 3][cb * 16 + wg * 8 + lane] = x;
       }
-    if (dead) s_dead = 1;
-    __syncthreads();
-    dead = s_dead != 0;
-    if (dead) break;
-    Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + slot;
+    meet();
     if (tid < kCols) {
-      const float sum = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
-      s_f[tid] = __fdividef(1.0f, sum);
-      if (!whole) {
-        part->m[tid] = -s_nm[tid];
+      const float sum = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
+      sh.f[tid] = __fdividef(1.0f, sum);
+      if (!it.whole) {
+        part->m[tid] = -nm_of[tid];
         part->l[tid] = sum;
       }
     }
-    __syncthreads();
-    __nv_bfloat16* const out0 = a.out + ((row0 + i0) * a.q_heads + (int64_t)head_now * share) * D + tok;
+    meet();
+    __nv_bfloat16* const out0 = a.out + (((int64_t)it.off + it.b + it.i0) * a.q_heads + (int64_t)it.kvh * (a.q_heads / a.kv.heads)) * D + tok;
+    const int32_t* const at_of = sh.at[qb];
     for (int cb = 0; cb < n16; ++cb) {
       const int j0 = cb * 16 + wg * 8;
-      float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (k1 > k0) tmem_ld8(tmem + my_lanes + kTmemO + j0, o);
+      float o[8];
+      tmem_ld8(tmem + my_lanes + kTmemO + (uint32_t)j0, o);
+      tmem_wait_ld();
       if (tok < D) {
-        if (!whole) {
+        if (!it.whole) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) part->o[j0 + j][tok] = o[j];
+          for (int y = 0; y < 8; ++y) part->o[j0 + y][tok] = o[y];
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j0 + j < n) out0[(int64_t)s_at[j0 + j] * D] = __float2bfloat16_rn(o[j] * s_f[j0 + j]);
+          for (int y = 0; y < 8; ++y)
+            if (j0 + y < it.n) out0[(int64_t)at_of[j0 + y] * D] = __float2bfloat16_rn(o[y] * sh.f[j0 + y]);
         }
       }
     }
     fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.o_free);
+      mbar_arrive(&sh.q_free[qb]);
+    }
+    item_done(sh, j);
+    meet();  // red and f are free again
   }
+}
+
+// One thread issues the products: S of the tiles,
+template <int D>
+__device__ __forceinline__ void multiply_keys(AttendShared& sh, unsigned char* s_q, uint32_t tmem) {
+  using Sm = AttendSmem<D>;
+  const uint64_t q_mat = smem_matrix(s_q, 0, 1024);
+  uint32_t i = 0;
+  bool ok = true;
+  for (uint32_t j = 0; ok && item_at(sh, j); ++j) {
+    const Item& it = sh.item[j % kItems];
+    const uint32_t idesc = kIdescF32 | kIdescM128 | kIdescBf16 | (uint32_t)((it.n + 15) / 16 * 2) << 17;
+    const uint32_t qb = j & 1u;
+    const int32_t tiles = it.k1 - it.k0;
+    mbar_arrive(&sh.item_free[j % kItems]);
+    ok = mbar_wait_for(&sh.q_full[qb], (j >> 1) & 1u, &sh.dead);
+    for (int32_t k = 0; ok && k < tiles; ++k, ++i) {
+      const uint32_t buf = i & 1u, par = (i >> 1) & 1u;
+      ok = mbar_wait_for(&sh.k_full[buf], par, &sh.dead) && (i < 2 || mbar_wait_for(&sh.s_free[buf], par ^ 1u, &sh.dead));
+      if (!ok) break;
+      fence_after();
+      const uint64_t bq = q_mat + (uint64_t)(qb * Sm::kQ >> 4);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+        mma_tmem_a(tmem + kTmemS + buf * kCols, tmem + kTmemK + buf * 64u + (uint32_t)x * 8u,
+                   bq + (uint64_t)(((x / 4) * (kCols * 128) + (x % 4) * 32) >> 4), idesc, x > 0);
+      mma_commit(&sh.s_full[buf]);
+      if (k == tiles - 1) mma_commit(&sh.q_free[qb]);
+    }
+  }
+  if (!ok) {
+    sh.dead = 1;
+    // the products under way end before the tensor memory is given back
+    mma_commit(&sh.drained[0]);
+    (void)mbar_wait_for(&sh.drained[0], 0u, nullptr);
+  }
+}
+// and, in another warp, O += values x weights.
+template <int D>
+__device__ __forceinline__ void multiply_values(AttendShared& sh, unsigned char* s_v, unsigned char* s_p, uint32_t tmem) {
+  using Sm = AttendSmem<D>;
+  const uint64_t v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024), p_mat = smem_matrix(s_p, kTile * 128, 1024);
+  uint32_t i = 0;
+  bool ok = true;
+  for (uint32_t j = 0; ok && item_at(sh, j); ++j) {
+    const Item& it = sh.item[j % kItems];
+    const uint32_t idesc = kIdescF32 | kIdescM128 | kIdescTransposeBoth | (uint32_t)((it.n + 15) / 16 * 2) << 17;
+    const int32_t tiles = it.k1 - it.k0;
+    mbar_arrive(&sh.item_free[j % kItems]);
+    if (j > 0) ok = mbar_wait_for(&sh.o_free, (j - 1u) & 1u, &sh.dead);
+    for (int32_t k = 0; ok && k < tiles; ++k, ++i) {
+      const uint32_t buf = i & 1u, par = (i >> 1) & 1u;
+      ok = mbar_wait_for(&sh.v_full[buf], par, &sh.dead) && mbar_wait_for(&sh.p_full[buf], par, &sh.dead);
+      if (!ok) break;
+      fence_after();
+      const uint64_t av = v_mat + (uint64_t)(buf * Sm::kV >> 4), bp = p_mat + (uint64_t)(buf * Sm::kP >> 4);
+#pragma unroll
+      for (int x = 0; x < kTile / 16; ++x)
+        mma_smem_a(tmem + kTmemO, av + (uint64_t)(x * 2048 >> 4), bp + (uint64_t)(x * 2048 >> 4), idesc, k > 0 || x > 0);
+      mma_commit(&sh.pv_done[buf]);
+    }
+  }
+  if (!ok) {
+    sh.dead = 1;
+    mma_commit(&sh.drained[1]);
+    (void)mbar_wait_for(&sh.drained[1], 0u, nullptr);
+  }
+}
+
+// Queries and column arrays of the items, one item ahead of the products.
+template <int D>
+__device__ __forceinline__ void bring_queries(const AttendArgs& a, AttendShared& sh, unsigned char* s_q) {
+  const int lane = (int)(threadIdx.x & 31u);
+  const int32_t share = a.q_heads / a.kv.heads;
+  for (uint32_t j = 0; item_at(sh, j); ++j) {
+    const Item& it = sh.item[j % kItems];
+    const uint32_t qb = j & 1u;
+    if (j >= 2 && !mbar_wait_for(&sh.q_free[qb], ((j >> 1) - 1u) & 1u, &sh.dead)) {
+      sh.dead = 1;
+      return;
+    }
+    for (int x = lane; x < kCols; x += 32) {
+      const int32_t r = (it.g0 + x) / share;
+      sh.at[qb][x] = r * a.q_heads + it.g0 + x - r * share;
+      sh.nm[qb][x] = x < it.n ? INFINITY : kLift;
+      sh.last[qb][x] = x < it.n ? it.len + it.i0 + r : INT_MAX;
+    }
+    const __nv_bfloat16* const q0 = a.q + ((int64_t)it.off + it.b + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
+    const int32_t cols = (it.n + 15) / 16 * 16;
+    constexpr int kStep = 32 / (D / 8);  // columns a warp brings at once
+    const int ch = lane % (D / 8);
+    unsigned char* const dst = s_q + qb * AttendSmem<D>::kQ + (ch / 8) * (kCols * 128);
+#pragma unroll 4
+    for (int col = lane / (D / 8); col < cols; col += kStep) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (col < it.n) {
+        const int32_t r = (it.g0 + col) / share;
+        v = *reinterpret_cast<const uint4*>(q0 + r * a.q_stride + (it.g0 + col - r * share) * D + ch * 8);
+      }
+      *reinterpret_cast<uint4*>(dst + col * 128 + (((ch & 7) ^ (col & 7)) << 4)) = v;
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full[qb]);
+    item_done(sh, j);
+  }
+}
+
+// Plans the items, a ring ahead; a part that holds no tile of its item is marked at once.
+template <int D>
+__device__ __forceinline__ void plan_items(const AttendArgs& a, AttendShared& sh, const Line& line) {
+  const int lane = (int)(threadIdx.x & 31u);
+  Walk walk;
+  walk.begin(a, line, sh.session, sh.base);
+  bool more = true;
+  for (uint32_t j = 0; more; ++j) {
+    Item it;
+    while ((more = walk.next(a, it)) && it.k0 >= it.k1) {
+      Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
+      for (int x = lane; x < kCols; x += 32) {
+        part->m[x] = -INFINITY;
+        part->l[x] = 0.0f;
+      }
+    }
+    if (j >= kItems && !mbar_wait_for(&sh.item_free[j % kItems], ((j / kItems) - 1u) & 1u, &sh.dead)) {
+      sh.dead = 1;
+      return;
+    }
+    if (!more) it.k0 = it.k1 = 0;
+    if (lane == 0) {
+      sh.item[j % kItems] = it;
+      mbar_arrive(&sh.item_full[j % kItems]);
+    }
+    __syncwarp();
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendArgs a) {
+  using Sm = AttendSmem<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const s_q = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* const s_v = s_q + 2 * Sm::kQ;
+  unsigned char* const s_p = s_v + 2 * Sm::kV;
+  unsigned char* const s_c = s_p + 2 * Sm::kP;
+  __shared__ AttendShared sh;
+
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t cta = (int32_t)blockIdx.x;
+  wait_for_previous();
+
+  // this CTA's part of the line: a prefix sum over the sessions, a stretch of them per thread
+  const int32_t per = (a.s.B + kAttendThreads - 1) / kAttendThreads;
+  const int32_t b0 = min(tid * per, a.s.B), b1 = min(b0 + per, a.s.B);
+  long long mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += a.units[b];
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  if (tid == 0) sh.dead = 0;
   __syncthreads();
-  if (s_dead != 0) {
-    // a product that never completed: give it the time of one more bounded wait, then report
-    (void)mbar_wait_for(&s_bar_s, ph_s, nullptr);
-    (void)mbar_wait_for(&s_bar_o, ph_o, nullptr);
-    if (tid == 0) atomicOr(a.error, 1u);
-    __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttendThreads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    all += sh.scan[w];
   }
-  if (warp == 0) tmem_free(tmem, kTmemCols);
+  const long long start = before + incl - mine;
+  const Line line(all, a.ctas);
+  if (cta == 0) {
+    long long at = start;
+    for (int32_t b = b0; b < b1; ++b) {
+      a.prefix[b] = at;
+      at += a.units[b];
+    }
+    if (tid == 0) a.prefix[a.s.B] = all;
+  }
+  if (cta >= line.ctas || all == 0) return;
+  const int64_t here = line.first(cta);
+  if (here >= start && here < start + mine) {
+    long long at = start;
+    int32_t b = b0;
+    while (here >= at + a.units[b]) at += a.units[b++];
+    sh.session = b;
+    sh.base = at;
+  }
+  if (warp == 16) tmem_alloc(&sh.tmem, kTmemCols);
+  if (tid == 0) {
+#pragma unroll
+    for (int e = 0; e < kItems; ++e) {
+      mbar_init(&sh.item_full[e], 1);
+      mbar_init(&sh.item_free[e], kItemReaders);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&sh.k_full[e], 4);   // a turning warp each
+      mbar_init(&sh.v_full[e], 4);
+      mbar_init(&sh.s_full[e], 1);   // the products themselves
+      mbar_init(&sh.pv_done[e], 1);
+      mbar_init(&sh.s_free[e], 8);   // a weighing warp each
+      mbar_init(&sh.p_full[e], 8);
+      mbar_init(&sh.q_full[e], 1);
+      mbar_init(&sh.q_free[e], 9);   // the item's last S product, and the weighing warps
+    }
+    mbar_init(&sh.o_free, 8);
+    mbar_init(&sh.drained[0], 1);
+    mbar_init(&sh.drained[1], 1);
+    fence_barrier_init();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+  if (warp < 4) {
+    fewer_registers<kTurnRegs>();
+    turn_tokens<D, true>(a, sh, s_v, s_c, tmem);
+  } else if (warp < 8) {
+    fewer_registers<kTurnRegs>();
+    turn_tokens<D, false>(a, sh, s_v, s_c, tmem);
+  } else if (warp < 16) {
+    more_registers<kWeightRegs>();
+    weigh<D>(a, sh, s_p, tmem);
+  } else {
+    fewer_registers<kRestRegs>();
+    if (warp == 19) plan_items<D>(a, sh, line);
+    else if (warp == 18) bring_queries<D>(a, sh, s_q);
+    else if (lane == 0 && warp == 16) multiply_keys<D>(sh, s_q, tmem);
+    else if (lane == 0) multiply_values<D>(sh, s_v, s_p, tmem);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && sh.dead != 0) atomicOr(a.error, 1u);
+  if (warp == 16) tmem_free(tmem, kTmemCols);
 }
 
 // ---- the joining of parts -----------------------------------------------------------------
@@ -742,7 +1033,7 @@ cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st) {
   attend_plan_kernel<<<(unsigned)a.s.B, kCheckThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(attend_kernel<D>, (unsigned)a.ctas, kThreads2, AttendSmem<D>::kBytes, st, a);
+  e = launch_after(attend_kernel<D>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D>::kBytes, st, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = a.s.total + a.s.B, warps = rows * a.q_heads;
   const int64_t blocks = min((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32), (int64_t)sms * 16);
@@ -790,7 +1081,7 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
                      static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), units,
                      reinterpret_cast<SessionPlan*>(plans), units + B,
                      reinterpret_cast<float*>(lines + round256(((size_t)B * 2 + 1) * sizeof(int64_t))),
-                     min(2 * di.sms, kMaxCtas)};
+                     min(di.sms, kMaxCtas)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? launch_attend<128>(a, di.sms, st) : launch_attend<64>(a, di.sms, st);
   return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
