@@ -26,17 +26,17 @@
 // repeats the weights.  The sum of weights is of the rounded ones, in binary32, a partial sum per
 // thread and column.
 //
-// What bounds it is the instructions of the turning and of the weights, so the steps run side by
-// side in warps of their own, two tiles deep: four warps turn keys, four turn values (each copies its
-// tokens' codes to shared memory two tiles ahead, across items), eight compute weights, one issues S,
-// one O, one brings the next items' queries and one plans the items.  They meet on mbarriers only.
-// Each role's loop is kept short: with five different streams of instructions on a scheduler, long
-// unrolled ones starved for instructions (the turning loops unrolled over both buffers and all groups
-// made the kernel 1.5 times slower).
+// What bounds it is the instructions of the turning and of the weights and their latencies, so
+// several CTAs share an SM, and within one the products run beside the other work: eight warps all
+// follow the same steps of a tile (turn half of the keys' channels each, then half of the values',
+// then weigh half of the columns each), and a ninth issues S as soon as the keys are there, behind
+// which the values are turned, and O behind the next tile's keys.  Loads are one tile ahead.  Roles
+// in warps of their own (keys, values, weights; one CTA an SM, two tiles deep) were slower (201 us
+// against X on attend_long): five streams of instructions on a scheduler starve one another.
 //
 // Work: the tiles of all (session, cached head, block of columns) items in one line, cut evenly
-// over the CTAs (one an SM), whatever the lengths.  A CTA's first and last items may be parts; their
-// O, m and sum go to the workspace, and a second kernel joins them in the order of the line.
+// over the CTAs, whatever the lengths.  A CTA's first and last items may be parts; their O, m and sum
+// go to the workspace, and a second kernel joins them in the order of the line.
 #include <climits>
 #include <math.h>
 #include <mutex>
@@ -47,13 +47,18 @@
 namespace sdcp {
 namespace {
 
-constexpr int kAttendThreads = 640;  // warps 0-3 keys, 4-7 values, 8-15 weights, 16 S, 17 O, 18 queries, 19 plan
-constexpr int kTile = 128;           // tokens of a tile
-constexpr int kCols = 96;            // columns of an item
-constexpr int kColsHalf = kCols / 2;
-constexpr int kMaxCtas = 160;        // CTAs a launch has at most (sizes the workspace)
-constexpr int kTmemCols = 512;       // tensor memory: keys of two tiles, S of two tiles, O
-constexpr uint32_t kTmemK = 0, kTmemS = 128, kTmemO = 320;
+constexpr int kComputeThreads = 256;                  // two groups of 128, a token of the tile each
+constexpr int kAttendThreads = kComputeThreads + 32;  // and the warp that issues the products
+constexpr int kTile = 128;                            // tokens of a tile
+constexpr int kMaxSms = 160;                          // sizes the workspace
+// Two shapes: at most 32 columns an item and three CTAs an SM, or at most 96 and two.
+template <int kColumns> struct Shape {
+  static constexpr int kCols = kColumns;
+  static constexpr int kHalf = kCols / 2;                   // columns of a thread
+  static constexpr int kCtas = kCols == 32 ? 3 : 2;         // of an SM
+  static constexpr uint32_t kTmemS = 64, kTmemO = 64 + kCols;  // tensor memory: keys, S, O
+  static constexpr int kTmemCols = kCols == 32 ? 128 : 256;
+};
 constexpr float kLift = 7.0f;     // a weight is 2^kLift at its reference
 constexpr float kTop = 15.0f;     // and 2^kTop at most
 
@@ -77,20 +82,21 @@ struct AttendArgs {
   int64_t* units;    // [B] units of a session: kv heads x chunks x tiles; 0 for a refused one
   SessionPlan* plans;  // [B]
   int64_t* prefix;   // [B+1]
-  float* parts;      // [kMaxCtas * 2] of Part<D>
+  float* parts;      // [ctas * 2] of Part
   int32_t ctas;
+  int32_t cols;      // columns an item has at most
 };
 
-template <int D> struct Part {
+template <int D, int kCols> struct Part {
   float o[kCols][D];
   float m[kCols];
   float l[kCols];
 };
 
-__device__ __forceinline__ SessionPlan session_plan(int32_t len, int32_t rows, int32_t share, int32_t window) {
+__device__ __forceinline__ SessionPlan session_plan(int32_t len, int32_t rows, int32_t share, int32_t window, int32_t most) {
   SessionPlan p;
   const int64_t cols = (int64_t)rows * share;
-  p.chunks = (int32_t)((cols + kCols - 1) / kCols);
+  p.chunks = (int32_t)((cols + most - 1) / most);
   const int64_t even = (cols + p.chunks - 1) / p.chunks;
   p.w = (int32_t)((even + 15) / 16 * 16);
   p.chunks = (int32_t)((cols + p.w - 1) / p.w);
@@ -164,6 +170,16 @@ __device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t a, uint64_t b, u
                "l"(b), "r"(idesc), "r"((uint32_t)add)
                : "memory");
 }
+// Bounded wait for a phase: polls without reading a clock or sleeping (waits here are a few hundred
+// cycles, a tile's step); false after kPolls, some seconds, or when another role has given up.
+constexpr uint32_t kPolls = 1u << 26;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile int* dead) {
+  for (uint32_t n = 0; n < kPolls; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 255u) == 255u && dead != nullptr && *dead) return false;
+  }
+  return false;
+}
 // A shared-memory matrix of 128-byte swizzled atoms (8 rows of 128 bytes).  lead: bytes between
 // atoms along the contiguous dimension (used where that is not the product's inner one); step:
 // bytes between atoms along the other.
@@ -183,9 +199,10 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+// (beyond the range: its end, so that what the slow path takes back is finite)
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 // sum += the low and the high half of w (binary16), each in binary32
@@ -223,31 +240,54 @@ __device__ __forceinline__ float warp_sum8(const float* x, int lane) {
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 // Byte g of w in both halves of a word.
 __device__ __forceinline__ uint32_t twice(uint32_t w, int g) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * g); }
+
+// (a & b) | c in one instruction, which the two constants would keep the compiler from.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 
 // A word of eight codes as pairs of numbers n s.  bfloat16: the four bits in the low end of
 // 128 + 8 + n; the pairs of a word lie four bits apart.
 __device__ __forceinline__ void word_bf16(uint32_t w, uint32_t s, uint32_t c, uint32_t* r) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = fma_bf16x2(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u, s, c);
+  for (int j = 0; j < 4; ++j) r[j] = fma_bf16x2(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), s, c);
 }
 // binary16: 1024 + 8 + n in the low four bits, or 1024 + 16 (8 + n) in the next four, with s / 16.
 __device__ __forceinline__ void word_f16(uint32_t w, uint32_t s, uint32_t c, uint32_t s16, uint32_t c16, uint32_t* r) {
   const uint32_t h = w >> 8;
-  r[0] = fma_f16x2((w & 0x000F000Fu) | 0x64006400u, s, c);
-  r[1] = fma_f16x2((w & 0x00F000F0u) | 0x64006400u, s16, c16);
-  r[2] = fma_f16x2((h & 0x000F000Fu) | 0x64006400u, s, c);
-  r[3] = fma_f16x2((h & 0x00F000F0u) | 0x64006400u, s16, c16);
+  r[0] = fma_f16x2(and_or(w, 0x000F000Fu, 0x64006400u), s, c);
+  r[1] = fma_f16x2(and_or(w, 0x00F000F0u, 0x64006400u), s16, c16);
+  r[2] = fma_f16x2(and_or(h, 0x000F000Fu, 0x64006400u), s, c);
+  r[3] = fma_f16x2(and_or(h, 0x00F000F0u, 0x64006400u), s16, c16);
 }
 
-template <int D> struct AttendSmem {
-  static constexpr int kAtoms = D / 64;                 // 128-byte atoms along the channels
-  static constexpr int kQ = kAtoms * kCols * 128;       // queries: [atom][column][128 bytes]
-  static constexpr int kV = kAtoms * kTile * 128;       // values: [atom][token][128 bytes]
-  static constexpr int kP = 2 * kTile * 128;            // weights: [atom of 64 columns][token][128 bytes]
-  static constexpr int kC = kTile * (D / 2 + 4);         // codes of a tile's keys or values, and a word of scales a token
-  static constexpr size_t kBytes = 2 * (size_t)(kQ + kV + kP + 2 * kC) + 1024;  // two of each, and the alignment to 1024
+template <int D, int kCols> struct AttendSmem {
+  static constexpr int kAtoms = D / 64;                        // 128-byte atoms along the channels
+  static constexpr int kQ = kAtoms * kCols * 128;              // queries: [atom][column][128 bytes]
+  static constexpr int kV = kAtoms * kTile * 128;              // values: [atom][token][128 bytes]
+  static constexpr int kP = (kCols + 63) / 64 * kTile * 128;   // weights: [atom of 64 columns][token][128 bytes]
+  static constexpr int kC = 2 * kTile * (D / 2 + 8);           // codes and scales of the next keys and values
+  static constexpr size_t kBytes = (size_t)kQ + kV + kP + kC + 1024;  // and the alignment to 1024
 };
 
 // One step of a CTA's way along the line: an item, or the part of it that is the CTA's.
@@ -259,8 +299,8 @@ struct Item {
   int32_t slot;                 // of the parts
   int32_t whole;                // all of the item's tiles are here
 };
-// The way itself, walked by the planning warp, which publishes the items in a ring: the divisions
-// stay out of the other warps' registers and off their way.
+// The way itself, walked by the ninth warp, an item ahead: the divisions stay out of the other
+// warps' registers and off their way.
 struct Walk {
   int64_t t, t_end, t_first;
   SessionPlan pl;
@@ -315,115 +355,22 @@ struct Walk {
     return true;
   }
 };
-constexpr int kItems = 4;                          // of the ring
-constexpr int kItemReaders = 4 + 4 + 8 + 2 + 1;    // warps that read an item
-
-// The barriers and small arrays of a CTA.  Tile i of a CTA uses buffer i & 1 of keys, S, values and
-// weights, item j buffer j & 1 of the queries and column arrays; a buffer's n-th use has parity n & 1.
-struct AttendShared {
-  __align__(16) float nm[2][kCols];      // kLift - m: what a scaled score is shifted by
-  __align__(16) int32_t last[2][kCols];  // last position of a column
-  int32_t at[2][kCols];                  // a column's place among the output's heads
-  __align__(16) float f[kCols];          // factors of a rescale; reciprocal sums
+// The barriers and small arrays of a CTA.
+template <int kCols> struct AttendShared {
+  __align__(16) float nm[kCols];      // kLift - m: what a scaled score is shifted by
+  __align__(16) int32_t last[kCols];  // last position of a column
+  int32_t at[kCols];                  // a column's place among the output's heads
+  __align__(16) float f[kCols];       // factors of a rescale; reciprocal sums
   float red[4][kCols];
-  uint64_t k_full[2], s_full[2], s_free[2], v_full[2], p_full[2], pv_done[2], q_full[2], q_free[2], o_free, drained[2];
+  uint64_t k_full, s_full, p_full, pv_done, drained;
   long long scan[kAttendThreads / 32];
   long long base;
   int32_t session;
   uint32_t tmem;
   int dead;
-  Item item[kItems];          // an item without tiles ends them
-  uint64_t item_full[kItems], item_free[kItems];
+  Walk walk;
+  Item item[2];  // item j in item[j & 1]; one without tiles ends them
 };
-// Item j of the CTA, for a whole warp: false at the end, or when a wait gave up.
-__device__ __forceinline__ bool item_at(AttendShared& sh, uint32_t j) {
-  if (!mbar_wait_for(&sh.item_full[j % kItems], (j / kItems) & 1u, &sh.dead)) {
-    sh.dead = 1;
-    return false;
-  }
-  const Item& it = sh.item[j % kItems];
-  return it.k0 < it.k1;
-}
-// The warp is done with item j.
-__device__ __forceinline__ void item_done(AttendShared& sh, uint32_t j) {
-  __syncwarp();
-  if ((threadIdx.x & 31u) == 0) mbar_arrive(&sh.item_free[j % kItems]);
-}
-
-// The tokens of one thread of a turning group, tile after tile across the items: the page of the
-// next tile's token is asked for when the codes of the one before are.  The codes go to the thread's
-// own places in shared memory: [group][token][16 bytes], then [token][a word with
-// its scales].
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int D> struct TokenStream {
-  static constexpr int kGroups = D / kKvGroup;
-  const AttendArgs& a;
-  AttendShared& sh;
-  bool live, here;
-  int32_t which, left, page;  // left: tiles of the item after the one at hand
-  uint32_t j, pos, lowest, end;
-  const uint8_t* head;
-  const int32_t* table;
-  __device__ __forceinline__ TokenStream(const AttendArgs& args, AttendShared& shared, int which_) : a(args), sh(shared), which(which_) {
-    left = 0;
-    j = 0;
-    step();
-  }
-  __device__ __forceinline__ void step() {
-    if (left == 0) {
-      live = item_at(sh, j);
-      if (!live) return;
-      const Item& it = sh.item[j % kItems];
-      left = it.k1 - it.k0;
-      lowest = it.lowest;
-      end = it.end;
-      pos = it.begin + (uint32_t)it.k0 * kTile + (threadIdx.x & 127u);
-      head = a.kv.pages + ((int64_t)it.kvh * 2 + which) * a.kv.block;
-      table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
-      item_done(sh, j++);
-    } else {
-      pos += kTile;
-    }
-    --left;
-    here = pos >= lowest && pos < end;
-    if (here) page = table[pos >> a.kv.log_page];
-  }
-  // starts the copy of the tile at hand (a token past the ends keeps old codes, with scale byte zero:
-  // finite numbers, whose weight is zero); then on to the next.  One group of copies a call.
-  __device__ __forceinline__ bool take(uint32_t codes, uint32_t scales) {
-    const bool had = live;
-    if (had) {
-      if (here) {
-        const uint32_t slot = pos & ((1u << a.kv.log_page) - 1u);
-        const uint8_t* blk = head + (int64_t)page * a.kv.page;
-        const uint8_t* at = blk + slot * 16u;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          copy_async16(codes + (uint32_t)g * (kTile * 16), at);
-          at += 16u << a.kv.log_page;
-        }
-        // four scale bytes of a token, or two each of a pair of tokens
-        copy_async4(scales, blk + (D / 2 << a.kv.log_page) + ((slot * kGroups) & ~3u));
-      } else {
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(scales), "r"(0u) : "memory");
-      }
-      step();
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    return had;
-  }
-};
-
-template <int kRegs> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-// Registers a thread: 640 x 96 at launch; 256 x 80 (turning), 256 x 128 (weights) and 128 x 56 (the
-// rest) are 60416 of those 61440.
-constexpr int kTurnRegs = 80, kWeightRegs = 128, kRestRegs = 56;
 
 // ---- plan: statuses and tiles of the sessions ---------------------------------------------
 __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const AttendArgs a) {
@@ -434,7 +381,7 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
     a.status[b] = st;
     int64_t units = 0;
     if (st == SDCP_S_OK) {
-      const SessionPlan p = session_plan(a.s.start[b], a.s.offsets[b + 1] - a.s.offsets[b] + 1, a.q_heads / a.kv.heads, a.s.window);
+      const SessionPlan p = session_plan(a.s.start[b], a.s.offsets[b + 1] - a.s.offsets[b] + 1, a.q_heads / a.kv.heads, a.s.window, a.cols);
       units = (int64_t)p.chunks * p.tiles * a.kv.heads;
       a.plans[b] = p;
     }
@@ -444,124 +391,233 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
 }
 
 // ---- the products -------------------------------------------------------------------------
-// Keys (kKeys) to tensor memory as bfloat16, or values to shared memory as binary16.
-template <int D, bool kKeys>
-__device__ __forceinline__ void turn_tokens(const AttendArgs& a, AttendShared& sh, unsigned char* s_v, unsigned char* s_c, uint32_t tmem) {
-  constexpr int kGroups = D / kKvGroup;
-  using Sm = AttendSmem<D>;
-  const int lane = (int)(threadIdx.x & 31u), tok = (int)(threadIdx.x & 127u);
-  TokenStream<D> stream(a, sh, kKeys ? 0 : 1);
-  const uint32_t codes = smem_u32(s_c) + (uint32_t)((kKeys ? 0 : 2) * Sm::kC + tok * 16);
-  const uint32_t scales = smem_u32(s_c) + (uint32_t)((kKeys ? 0 : 2) * Sm::kC + kGroups * kTile * 16 + tok * 4);
-  uint32_t lives = stream.take(codes, scales) ? 1u : 0u;
-  lives |= stream.take(codes + Sm::kC, scales + Sm::kC) ? 2u : 0u;
-  const uint32_t tmem_dst = tmem + kTmemK + ((uint32_t)((threadIdx.x >> 5) & 3u) << 21);  // 32 lanes, in bits 16 up
-  const uint32_t smem_dst = smem_u32(s_v) + (uint32_t)tok * 128u + ((uint32_t)(tok & 7) << 4);
-  for (uint32_t i = 0;; ++i) {
-    const uint32_t e = i & 1u;
-    if (!((lives >> e) & 1u)) return;
-    // the buffer's previous use: the product that read it is done
-    if (i >= 2 && !mbar_wait_for(kKeys ? &sh.s_full[e] : &sh.pv_done[e], ((i >> 1) - 1u) & 1u, &sh.dead)) {
-      sh.dead = 1;
+// The next item that has tiles; a part that holds no tile of its item is marked at once.  One thread.
+template <int D, int kCols>
+__device__ __forceinline__ void plan_item(const AttendArgs& a, AttendShared<kCols>& sh, uint32_t j) {
+  Item it;
+  bool more;
+  Walk walk = sh.walk;
+  while ((more = walk.next(a, it)) && it.k0 >= it.k1) {
+    Part<D, kCols>* const part = reinterpret_cast<Part<D, kCols>*>(a.parts) + it.slot;
+    for (int x = 0; x < kCols; ++x) {
+      part->m[x] = -INFINITY;
+      part->l[x] = 0.0f;
+    }
+  }
+  if (!more) it.k0 = it.k1 = 0;
+  sh.walk = walk;
+  sh.item[j & 1u] = it;
+}
+
+// The ninth warp: S of a tile when its keys are in tensor memory, O when its weights are in shared
+// memory (the values are there before the weights).  One thread.
+template <int D, int kCols>
+__device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols>& sh, const unsigned char* s_q, const unsigned char* s_v,
+                                         const unsigned char* s_p, uint32_t tmem) {
+  using Sm = AttendSmem<D, kCols>;
+  using Sh = Shape<kCols>;
+  const uint64_t q_mat = smem_matrix(s_q, 0, 1024), v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024),
+                 p_mat = smem_matrix(s_p, kTile * 128, 1024);
+  uint32_t i = 0;
+  for (uint32_t j = 0;; ++j) {
+    __syncthreads();  // item j is planned, and the previous one is done with
+    if (sh.dead) {    // products under way end before the tensor memory is given back
+      if ((threadIdx.x & 31u) == 0) {
+        mma_commit(&sh.drained);
+        (void)wait_phase(&sh.drained, 0u, nullptr);
+        atomicOr(a.error, 1u);
+      }
       return;
     }
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    uint32_t sb;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sb) : "r"(scales + e * Sm::kC) : "memory");
-    if (D == 64) sb >>= (tok & 1) * 16;  // tiles start at even tokens
-    if (kKeys) fence_after();
-#pragma unroll 1
-    for (int g = 0; g < kGroups; ++g, sb >>= 8) {
-      uint32_t w[4];
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(codes + e * Sm::kC + (uint32_t)g * (kTile * 16))
-                   : "memory");
-      if (kKeys) {
-        const uint32_t s = twice(sb, 0) * 16u + (kScaleBias << 4) * 0x10001u;
-        const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
-        uint32_t r[16];
+    const int32_t tiles = sh.item[j & 1u].k1 - sh.item[j & 1u].k0;
+    if (tiles <= 0) return;
+    const uint32_t idesc = kIdescF32 | kIdescM128 | (uint32_t)((sh.item[j & 1u].n + 15) / 16 * 2) << 17;
+    if ((threadIdx.x & 31u) == 0) {
+      plan_item<D, kCols>(a, sh, j + 1);
+      for (int32_t k = 0; k < tiles; ++k, ++i) {
+        const uint32_t par = i & 1u;
+        if (!wait_phase(&sh.k_full, par, &sh.dead)) { sh.dead = 1; break; }
+        fence_after();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) word_bf16(w[x], s, m, r + 4 * x);
-        tmem_st16(tmem_dst + e * 64u + (uint32_t)g * 16u, r);
-      } else {
-        const uint32_t s = twice(sb, 0) << 7;
-        const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
-        const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
-        const uint32_t dst = (smem_dst ^ ((uint32_t)(g & 1) << 6)) + e * Sm::kV + (uint32_t)(g >> 1) * (kTile * 128);
+        for (int x = 0; x < D / 16; ++x)
+          mma_tmem_a(tmem + Sh::kTmemS, tmem + (uint32_t)x * 8u, q_mat + (uint64_t)(((x / 4) * (kCols * 128) + (x % 4) * 32) >> 4),
+                     idesc | kIdescBf16, x > 0);
+        mma_commit(&sh.s_full);
+        if (!wait_phase(&sh.p_full, par, &sh.dead)) { sh.dead = 1; break; }
+        fence_after();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t r[4];
-          word_f16(w[x], s, m, s16, m16, r);
-          st_shared16(dst ^ (uint32_t)(x << 4), r[0], r[1], r[2], r[3]);
-        }
+        for (int x = 0; x < kTile / 16; ++x)
+          mma_smem_a(tmem + Sh::kTmemO, v_mat + (uint64_t)(x * 2048 >> 4), p_mat + (uint64_t)(x * 2048 >> 4), idesc | kIdescTransposeBoth,
+                     k > 0 || x > 0);
+        mma_commit(&sh.pv_done);
       }
     }
-    if (kKeys) {
-      tmem_wait_st();
-      fence_before();
-    } else {
-      fence_async_smem();
-    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(kKeys ? &sh.k_full[e] : &sh.v_full[e]);
-    lives = (lives & ~(1u << e)) | (stream.take(codes + e * Sm::kC, scales + e * Sm::kC) ? 1u << e : 0u);
   }
 }
 
-// The weights of the tiles, and an item's end: O and the sums to the output or to a part.
-template <int D>
-__device__ __forceinline__ void weigh(const AttendArgs& a, AttendShared& sh, unsigned char* s_p, uint32_t tmem) {
-  const int tid = (int)threadIdx.x - 256, lane = tid & 31, warp = tid >> 5;
+// The eight warps' steps.
+template <int D, int kCols>
+__device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<kCols>& sh, unsigned char* s_q, unsigned char* s_v,
+                                             unsigned char* s_p, unsigned char* s_c, uint32_t tmem) {
+  using Sm = AttendSmem<D, kCols>;
+  using Sh = Shape<kCols>;
+  constexpr int kOwn = D / kKvGroup / 2;  // channel groups of a thread
+  constexpr int kBlocks = Sh::kHalf / 8;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wg = tid >> 7, tok = tid & 127;
-  const uint32_t my_lanes = (uint32_t)(warp & 3) << 21;
+  const uint32_t my_lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes of tensor memory, in bits 16 up
   const uint32_t win = a.s.window > 0 ? (uint32_t)a.s.window : 0x80000000u;
-  // block 2 cb + wg of eight columns, swizzled in the token's 128 bytes
-  const uint32_t dst_p = smem_u32(s_p) + (uint32_t)tok * 128u + ((uint32_t)(wg ^ (tok & 7)) << 4);
+  const int32_t share = a.q_heads / a.kv.heads;
+  const uint32_t swizzled = (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);
+  // values: channels (wg * kOwn + g) * 32 of the token; weights: block 2 cb + wg of eight columns
+  const uint32_t v_at = smem_u32(s_v) + (D == 128 ? (uint32_t)(wg * kTile * 128) + swizzled : swizzled ^ ((uint32_t)wg << 6));
+  const uint32_t p_at = smem_u32(s_p) + (swizzled ^ ((uint32_t)wg << 4));
+  const uint32_t s_at = my_lanes + Sh::kTmemS + (uint32_t)(wg * 8);
   auto meet = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
   auto any = [](bool p) {
     uint32_t r;
     asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q; }" : "=r"(r) : "r"((uint32_t)p) : "memory");
     return r != 0;
   };
-  uint32_t i = 0, j = 0;  // tiles and items so far
-  bool dead = false;
-  for (;; ++j) {
-    const bool more = item_at(sh, j);
-    if (any(!more)) return;
-    const Item& it = sh.item[j % kItems];
-    Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
+  // the thread's codes of the next keys, [group][thread][16 bytes], then [thread][4 bytes] of scales; the values' after them
+  constexpr uint32_t kCodes = kComputeThreads * (kOwn * 16 + 4);
+  static_assert(2 * kCodes == Sm::kC, "codes");
+  const uint32_t c_at = smem_u32(s_c) + (uint32_t)tid * 16u, sb_at = smem_u32(s_c) + kComputeThreads * kOwn * 16 + (uint32_t)tid * 4u;
+  const int sb_shift = D == 128 ? wg * 16 : (tok & 1) * 16 + wg * 8;  // of the thread's own scales (tiles start at even tokens)
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at + kCodes), "r"(0u) : "memory");
+  uint32_t slot = 0;
+  uint32_t i = 0;  // tiles so far
+  bool dead = false;  // a wait gave up: the eight warps agree on it at a vote, all nine at an item's start
+  for (uint32_t j = 0;; ++j) {
+    __syncthreads();
+    if (sh.dead) return;
+    const Item& it = sh.item[j & 1u];
+    const int32_t tiles = it.k1 - it.k0;
+    if (tiles <= 0) return;
     const int32_t n16 = (it.n + 15) / 16;  // blocks of 16 columns; a group of threads has eight of each
-    const uint32_t qb = j & 1u;
-    float* const nm_of = sh.nm[qb];
-    const int32_t* const last_of = sh.last[qb];
-    dead |= !mbar_wait_for(&sh.q_full[qb], (j >> 1) & 1u, &sh.dead);
-    float l[kColsHalf];
+
+    // a tile ahead: the page of the next token, and the copy of the thread's share of its codes to
+    // the thread's own places in shared memory (a token that is not read keeps old codes: finite
+    // numbers, whose weight is zero)
+    const uint32_t lowest = it.lowest, end = it.end;
+    uint32_t pos = it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok, ahead = pos;
+    const uint8_t* const head = a.kv.pages + (int64_t)it.kvh * 2 * a.kv.block;
+    const int32_t* const table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
+    const uint8_t* blk = nullptr;  // of the next token, as `ahead`; null: nothing to read
+    int32_t left = tiles, page = 0;
+    auto find_page = [&] {
+      page = -1;
+      if (left > 0 && ahead >= lowest && ahead < end) page = table[ahead >> a.kv.log_page];
+    };
+    auto aim = [&] {  // at the token whose page is known
+      blk = page >= 0 ? head + (int64_t)page * a.kv.page : nullptr;
+      slot = ahead & ((1u << a.kv.log_page) - 1u);
+      ahead += kTile;
+      --left;
+    };
+    auto fetch = [&](int which) {
+      if (blk != nullptr) {
+        const uint8_t* const b0 = which ? blk + a.kv.block : blk;
+        const uint8_t* const c0 = b0 + ((((uint32_t)(wg * kOwn) << a.kv.log_page) + slot) << 4);
+        copy_async16(c_at + (uint32_t)which * kCodes, c0);
+        if (kOwn == 2) copy_async16(c_at + (uint32_t)which * kCodes + kComputeThreads * 16, c0 + (16u << a.kv.log_page));
+        // four scale bytes of a token, or two each of a pair of tokens
+        copy_async4(sb_at + (uint32_t)which * kCodes, b0 + (D / 2 << a.kv.log_page) + ((slot * (D / kKvGroup)) & ~3u));
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    find_page();
+    aim();
+    find_page();
+    fetch(0);
+    fetch(1);
+
+    // queries of the columns, zero past them, and the columns' state
+    if (tid < kCols) {
+      const int32_t r = (it.g0 + tid) / share;
+      sh.at[tid] = r * a.q_heads + it.g0 + tid - r * share;
+      sh.nm[tid] = tid < it.n ? INFINITY : kLift;
+      sh.last[tid] = tid < it.n ? it.len + it.i0 + r : INT_MAX;
+    }
+    {
+      const __nv_bfloat16* const q0 = a.q + ((int64_t)it.off + it.b + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
+      const int ch = tid % (D / 8);
+      unsigned char* const dst = s_q + (ch / 8) * (kCols * 128);
+      for (int col = tid / (D / 8); col < n16 * 16; col += kComputeThreads / (D / 8)) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (col < it.n) {
+          const int32_t r = (it.g0 + col) / share;
+          v = *reinterpret_cast<const uint4*>(q0 + r * a.q_stride + (it.g0 + col - r * share) * D + ch * 8);
+        }
+        *reinterpret_cast<uint4*>(dst + col * 128 + (((ch & 7) ^ (col & 7)) << 4)) = v;
+      }
+      fence_async_smem();  // seen by the first S product through the keys' barrier
+    }
+    const uint32_t low_last = (uint32_t)(it.len + it.i0), high_last = end - 1u;  // of the columns
+    float l[Sh::kHalf];
 #pragma unroll
-    for (int x = 0; x < kColsHalf; ++x) l[x] = 0.0f;
+    for (int x = 0; x < Sh::kHalf; ++x) l[x] = 0.0f;
 
     bool first = true;
-    uint32_t lo = it.begin + (uint32_t)it.k0 * kTile;
-    const uint32_t low_last = (uint32_t)(it.len + it.i0), high_last = it.end - 1u;  // of the columns
-    for (int32_t left = it.k1 - it.k0; left > 0; --left, ++i, lo += kTile, first = false) {
-      const uint32_t buf = i & 1u, pos = lo + (uint32_t)tok;
+    for (int32_t k = 0; k < tiles; ++k, ++i, pos += kTile, first = false) {
+      // keys to tensor memory (the previous S has read the ones before)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      uint32_t sb = ld_shared4(sb_at) >> sb_shift;
+#pragma unroll
+      for (int g = 0; g < kOwn; ++g) {
+        const uint4 c = ld_shared16(c_at + (uint32_t)g * (kComputeThreads * 16));
+        const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
+        const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
+        uint32_t r[16];
+        word_bf16(c.x, s, m, r);
+        word_bf16(c.y, s, m, r + 4);
+        word_bf16(c.z, s, m, r + 8);
+        word_bf16(c.w, s, m, r + 12);
+        tmem_st16(my_lanes + (uint32_t)((wg * kOwn + g) * 16), r);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full);
+      aim();
+      find_page();
+      fetch(0);
+      // values to shared memory, once the O product has read the ones before
+      if (i > 0) dead |= !wait_phase(&sh.pv_done, (i - 1u) & 1u, &sh.dead);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      sb = ld_shared4(sb_at + kCodes) >> sb_shift;
+#pragma unroll
+      for (int g = 0; g < kOwn; ++g) {
+        const uint4 c = ld_shared16(c_at + kCodes + (uint32_t)g * (kComputeThreads * 16));
+        const uint32_t s = twice(sb, g) << 7;
+        const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
+        const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t r[4];
+          word_f16(w[x], s, m, s16, m16, r);
+          st_shared16(v_at ^ (uint32_t)((g * 4 + x) << 4), r[0], r[1], r[2], r[3]);
+        }
+      }
+      fetch(1);
+
+      // weights of this group's columns with the references at hand; into the sums
+      const uint32_t lo = pos - (uint32_t)tok;
       const bool masked = lo + kTile - 1 > low_last || high_last - lo >= win;
-      dead |= !mbar_wait_for(&sh.s_full[buf], (i >> 1) & 1u, &sh.dead);
-      if (i >= 2) dead |= !mbar_wait_for(&sh.pv_done[buf], ((i >> 1) - 1u) & 1u, &sh.dead);
+      dead |= !wait_phase(&sh.s_full, i & 1u, &sh.dead);
       fence_after();
-      const uint32_t s_at = tmem + my_lanes + kTmemS + buf * kCols + (uint32_t)wg * 8u;
-      const uint32_t p_at = dst_p + buf * AttendSmem<D>::kP;
-      uint32_t w16[kColsHalf / 2];
       float top = -INFINITY;
-      // weights of this group's columns with the references at hand
-      auto block = [&](int cb, float (&x)[8], auto with_mask) {
+      auto block = [&](int cb, float(&x)[8], auto with_mask) {
         const int j0 = cb * 16 + wg * 8;
-        const float4 n0 = *reinterpret_cast<const float4*>(&nm_of[j0]), n1 = *reinterpret_cast<const float4*>(&nm_of[j0 + 4]);
+        const float4 n0 = *reinterpret_cast<const float4*>(&sh.nm[j0]), n1 = *reinterpret_cast<const float4*>(&sh.nm[j0 + 4]);
         const float nm[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
 #pragma unroll
         for (int y = 0; y < 8; ++y) x[y] = fmaf(x[y], a.c, nm[y]);
         if (with_mask) {
-          const int4 e0 = *reinterpret_cast<const int4*>(&last_of[j0]), e1 = *reinterpret_cast<const int4*>(&last_of[j0 + 4]);
+          const int4 e0 = *reinterpret_cast<const int4*>(&sh.last[j0]), e1 = *reinterpret_cast<const int4*>(&sh.last[j0 + 4]);
           const int32_t last[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
           for (int y = 0; y < 8; ++y)
@@ -569,67 +625,75 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, AttendShared& sh, uns
         }
 #pragma unroll
         for (int y = 0; y < 8; ++y) top = fmaxf(top, x[y]);
+        uint32_t w[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) w16[cb * 4 + y] = pack_f16x2(ex2(x[2 * y]), ex2(x[2 * y + 1]));
-        st_shared16((p_at ^ (uint32_t)((2 * cb & 7) << 4)) + (uint32_t)(cb >> 2) * (kTile * 128), w16[cb * 4], w16[cb * 4 + 1],
-                    w16[cb * 4 + 2], w16[cb * 4 + 3]);
+        for (int y = 0; y < 4; ++y) w[y] = pack_f16x2(ex2(x[2 * y]), ex2(x[2 * y + 1]));
+        st_shared16((p_at ^ (uint32_t)((2 * cb & 7) << 4)) + (uint32_t)(cb >> 2) * (kTile * 128), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) add_halves(w[y], l[cb * 8 + 2 * y], l[cb * 8 + 2 * y + 1]);
       };
       auto weights = [&](auto with_mask) {
+        float x[2][8];
+        tmem_ld8(s_at, x[0]);
+        tmem_wait_ld();
 #pragma unroll
-        for (int cb = 0; cb < kColsHalf / 8; cb += 2)
+        for (int cb = 0; cb < kBlocks; ++cb)
           if (cb < n16) {
-            float x[8], y[8];
-            tmem_ld8(s_at + (uint32_t)cb * 16u, x);
-            if (cb + 1 < n16) tmem_ld8(s_at + (uint32_t)cb * 16u + 16u, y);
+            if (cb + 1 < kBlocks && cb + 1 < n16) tmem_ld8(s_at + (uint32_t)(cb + 1) * 16u, x[(cb + 1) & 1]);
+            block(cb, x[cb & 1], with_mask);
             tmem_wait_ld();
-            block(cb, x, with_mask);
-            if (cb + 1 < n16) block(cb + 1, y, with_mask);
           }
       };
       if (!first) {  // no reference yet on the first one
         if (masked) weights(std::true_type{});
         else weights(std::false_type{});
       }
+      fence_async_smem();
+      fence_before();
       if (any(top > kTop || first || dead)) {
-        // slow path: the columns' maxima over the tile, new references, O and the sums rescaled
+        // slow path: the tile's weights out of the sums, its columns' maxima, new references, O and
+        // the sums rescaled, and the weights again
         if (any(dead)) break;
-        if (!first) {
-          dead |= !mbar_wait_for(&sh.pv_done[buf ^ 1u], ((i - 1u) >> 1) & 1u, &sh.dead);
-          fence_after();
-        }
-        for (int cb = 0; cb < n16; ++cb) {
-          const int j0 = cb * 16 + wg * 8;
-          float x[8];
-          tmem_ld8(s_at + (uint32_t)cb * 16u, x);
-          tmem_wait_ld();
+        fence_after();
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float z = masked && (uint32_t)last_of[j0 + y] - pos >= win ? -INFINITY : x[y] * a.c;
-            const float m = warp_max(z);
-            if (lane == 0) sh.red[warp & 3][j0 + y] = m;
+        for (int cb = 0; cb < kBlocks; ++cb)
+          if (cb < n16) {
+            const int j0 = cb * 16 + wg * 8;
+            float x[8];
+            tmem_ld8(s_at + (uint32_t)cb * 16u, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const bool hidden = masked && (uint32_t)sh.last[j0 + y] - pos >= win;
+              if (!first) {
+                const uint32_t w = pack_f16x2(hidden ? 0.0f : ex2(fmaf(x[y], a.c, sh.nm[j0 + y])), 0.0f);
+                l[cb * 8 + y] -= __half2float(__ushort_as_half((unsigned short)w));
+              }
+              const float m = warp_max(hidden ? -INFINITY : x[y] * a.c);
+              if (lane == 0) sh.red[warp & 3][j0 + y] = m;
+            }
           }
-        }
         meet();
         if (tid < kCols) {
           float f = 1.0f;
           if (tid < it.n) {
             const float m = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
-            const float nm0 = nm_of[tid], nm1 = fminf(nm0, kLift - m);
-            nm_of[tid] = nm1;
+            const float nm0 = sh.nm[tid], nm1 = fminf(nm0, kLift - m);
+            sh.nm[tid] = nm1;
             f = nm0 == nm1 ? 1.0f : ex2(nm1 - nm0);
           }
           sh.f[tid] = f;
         }
         meet();
 #pragma unroll
-        for (int cb = 0; cb < kColsHalf / 8; ++cb)
+        for (int cb = 0; cb < kBlocks; ++cb)
           if (cb < n16) {
             const int j0 = cb * 16 + wg * 8;
 #pragma unroll
             for (int y = 0; y < 8; ++y) l[cb * 8 + y] *= sh.f[j0 + y];
             if (!first) {
               float o[8];
-              const uint32_t o_at = tmem + my_lanes + kTmemO + (uint32_t)j0;
+              const uint32_t o_at = my_lanes + Sh::kTmemO + (uint32_t)j0;
               tmem_ld8(o_at, o);
               tmem_wait_ld();
 #pragma unroll
@@ -639,50 +703,42 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, AttendShared& sh, uns
           }
         weights(std::true_type{});
         tmem_wait_st();
+        fence_async_smem();
+        fence_before();
+        meet();
       }
-      fence_async_smem();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh.s_free[buf]);
-        mbar_arrive(&sh.p_full[buf]);
-      }
-#pragma unroll
-      for (int cb = 0; cb < kColsHalf / 8; ++cb)
-        if (cb < n16) {
-#pragma unroll
-          for (int x = cb * 4; x < cb * 4 + 4; ++x) add_halves(w16[x], l[2 * x], l[2 * x + 1]);
-        }
+      if (tid == 0) mbar_arrive(&sh.p_full);
     }
-    if (!dead) dead |= !mbar_wait_for(&sh.pv_done[(i - 1u) & 1u], ((i - 1u) >> 1) & 1u, &sh.dead);
-    if (any(dead)) {
-      sh.dead = 1;
-      return;
-    }
+
     // O, references and sums of the item's columns
+    if (!dead) dead = !wait_phase(&sh.pv_done, (i - 1u) & 1u, &sh.dead);
     fence_after();
 #pragma unroll
-    for (int cb = 0; cb < kColsHalf / 8; ++cb)
+    for (int cb = 0; cb < kBlocks; ++cb)
       if (cb < n16) {
         const float x = warp_sum8(&l[cb * 8], lane);
         if (lane < 8) sh.red[warp & 3][cb * 16 + wg * 8 + lane] = x;
       }
-    meet();
+    if (any(dead)) {
+      sh.dead = 1;
+      continue;
+    }
+    Part<D, kCols>* const part = reinterpret_cast<Part<D, kCols>*>(a.parts) + it.slot;
     if (tid < kCols) {
       const float sum = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
       sh.f[tid] = __fdividef(1.0f, sum);
       if (!it.whole) {
-        part->m[tid] = -nm_of[tid];
+        part->m[tid] = -sh.nm[tid];
         part->l[tid] = sum;
       }
     }
     meet();
-    __nv_bfloat16* const out0 = a.out + (((int64_t)it.off + it.b + it.i0) * a.q_heads + (int64_t)it.kvh * (a.q_heads / a.kv.heads)) * D + tok;
-    const int32_t* const at_of = sh.at[qb];
+    __nv_bfloat16* const out0 = a.out + (((int64_t)it.off + it.b + it.i0) * a.q_heads + (int64_t)it.kvh * share) * D + tok;
+#pragma unroll 1
     for (int cb = 0; cb < n16; ++cb) {
       const int j0 = cb * 16 + wg * 8;
       float o[8];
-      tmem_ld8(tmem + my_lanes + kTmemO + (uint32_t)j0, o);
+      tmem_ld8(my_lanes + Sh::kTmemO + (uint32_t)j0, o);
       tmem_wait_ld();
       if (tok < D) {
         if (!it.whole) {
@@ -691,165 +747,23 @@ __device__ __forceinline__ void weigh(const AttendArgs& a, AttendShared& sh, uns
         } else {
 #pragma unroll
           for (int y = 0; y < 8; ++y)
-            if (j0 + y < it.n) out0[(int64_t)at_of[j0 + y] * D] = __float2bfloat16_rn(o[y] * sh.f[j0 + y]);
+            if (j0 + y < it.n) out0[(int64_t)sh.at[j0 + y] * D] = __float2bfloat16_rn(o[y] * sh.f[j0 + y]);
         }
       }
     }
     fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh.o_free);
-      mbar_arrive(&sh.q_free[qb]);
-    }
-    item_done(sh, j);
-    meet();  // red and f are free again
   }
 }
 
-// One thread issues the products: S of the tiles,
-template <int D>
-__device__ __forceinline__ void multiply_keys(AttendShared& sh, unsigned char* s_q, uint32_t tmem) {
-  using Sm = AttendSmem<D>;
-  const uint64_t q_mat = smem_matrix(s_q, 0, 1024);
-  uint32_t i = 0;
-  bool ok = true;
-  for (uint32_t j = 0; ok && item_at(sh, j); ++j) {
-    const Item& it = sh.item[j % kItems];
-    const uint32_t idesc = kIdescF32 | kIdescM128 | kIdescBf16 | (uint32_t)((it.n + 15) / 16 * 2) << 17;
-    const uint32_t qb = j & 1u;
-    const int32_t tiles = it.k1 - it.k0;
-    mbar_arrive(&sh.item_free[j % kItems]);
-    ok = mbar_wait_for(&sh.q_full[qb], (j >> 1) & 1u, &sh.dead);
-    for (int32_t k = 0; ok && k < tiles; ++k, ++i) {
-      const uint32_t buf = i & 1u, par = (i >> 1) & 1u;
-      ok = mbar_wait_for(&sh.k_full[buf], par, &sh.dead) && (i < 2 || mbar_wait_for(&sh.s_free[buf], par ^ 1u, &sh.dead));
-      if (!ok) break;
-      fence_after();
-      const uint64_t bq = q_mat + (uint64_t)(qb * Sm::kQ >> 4);
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-        mma_tmem_a(tmem + kTmemS + buf * kCols, tmem + kTmemK + buf * 64u + (uint32_t)x * 8u,
-                   bq + (uint64_t)(((x / 4) * (kCols * 128) + (x % 4) * 32) >> 4), idesc, x > 0);
-      mma_commit(&sh.s_full[buf]);
-      if (k == tiles - 1) mma_commit(&sh.q_free[qb]);
-    }
-  }
-  if (!ok) {
-    sh.dead = 1;
-    // the products under way end before the tensor memory is given back
-    mma_commit(&sh.drained[0]);
-    (void)mbar_wait_for(&sh.drained[0], 0u, nullptr);
-  }
-}
-// and, in another warp, O += values x weights.
-template <int D>
-__device__ __forceinline__ void multiply_values(AttendShared& sh, unsigned char* s_v, unsigned char* s_p, uint32_t tmem) {
-  using Sm = AttendSmem<D>;
-  const uint64_t v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024), p_mat = smem_matrix(s_p, kTile * 128, 1024);
-  uint32_t i = 0;
-  bool ok = true;
-  for (uint32_t j = 0; ok && item_at(sh, j); ++j) {
-    const Item& it = sh.item[j % kItems];
-    const uint32_t idesc = kIdescF32 | kIdescM128 | kIdescTransposeBoth | (uint32_t)((it.n + 15) / 16 * 2) << 17;
-    const int32_t tiles = it.k1 - it.k0;
-    mbar_arrive(&sh.item_free[j % kItems]);
-    if (j > 0) ok = mbar_wait_for(&sh.o_free, (j - 1u) & 1u, &sh.dead);
-    for (int32_t k = 0; ok && k < tiles; ++k, ++i) {
-      const uint32_t buf = i & 1u, par = (i >> 1) & 1u;
-      ok = mbar_wait_for(&sh.v_full[buf], par, &sh.dead) && mbar_wait_for(&sh.p_full[buf], par, &sh.dead);
-      if (!ok) break;
-      fence_after();
-      const uint64_t av = v_mat + (uint64_t)(buf * Sm::kV >> 4), bp = p_mat + (uint64_t)(buf * Sm::kP >> 4);
-#pragma unroll
-      for (int x = 0; x < kTile / 16; ++x)
-        mma_smem_a(tmem + kTmemO, av + (uint64_t)(x * 2048 >> 4), bp + (uint64_t)(x * 2048 >> 4), idesc, k > 0 || x > 0);
-      mma_commit(&sh.pv_done[buf]);
-    }
-  }
-  if (!ok) {
-    sh.dead = 1;
-    mma_commit(&sh.drained[1]);
-    (void)mbar_wait_for(&sh.drained[1], 0u, nullptr);
-  }
-}
-
-// Queries and column arrays of the items, one item ahead of the products.
-template <int D>
-__device__ __forceinline__ void bring_queries(const AttendArgs& a, AttendShared& sh, unsigned char* s_q) {
-  const int lane = (int)(threadIdx.x & 31u);
-  const int32_t share = a.q_heads / a.kv.heads;
-  for (uint32_t j = 0; item_at(sh, j); ++j) {
-    const Item& it = sh.item[j % kItems];
-    const uint32_t qb = j & 1u;
-    if (j >= 2 && !mbar_wait_for(&sh.q_free[qb], ((j >> 1) - 1u) & 1u, &sh.dead)) {
-      sh.dead = 1;
-      return;
-    }
-    for (int x = lane; x < kCols; x += 32) {
-      const int32_t r = (it.g0 + x) / share;
-      sh.at[qb][x] = r * a.q_heads + it.g0 + x - r * share;
-      sh.nm[qb][x] = x < it.n ? INFINITY : kLift;
-      sh.last[qb][x] = x < it.n ? it.len + it.i0 + r : INT_MAX;
-    }
-    const __nv_bfloat16* const q0 = a.q + ((int64_t)it.off + it.b + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
-    const int32_t cols = (it.n + 15) / 16 * 16;
-    constexpr int kStep = 32 / (D / 8);  // columns a warp brings at once
-    const int ch = lane % (D / 8);
-    unsigned char* const dst = s_q + qb * AttendSmem<D>::kQ + (ch / 8) * (kCols * 128);
-#pragma unroll 4
-    for (int col = lane / (D / 8); col < cols; col += kStep) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (col < it.n) {
-        const int32_t r = (it.g0 + col) / share;
-        v = *reinterpret_cast<const uint4*>(q0 + r * a.q_stride + (it.g0 + col - r * share) * D + ch * 8);
-      }
-      *reinterpret_cast<uint4*>(dst + col * 128 + (((ch & 7) ^ (col & 7)) << 4)) = v;
-    }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_full[qb]);
-    item_done(sh, j);
-  }
-}
-
-// Plans the items, a ring ahead; a part that holds no tile of its item is marked at once.
-template <int D>
-__device__ __forceinline__ void plan_items(const AttendArgs& a, AttendShared& sh, const Line& line) {
-  const int lane = (int)(threadIdx.x & 31u);
-  Walk walk;
-  walk.begin(a, line, sh.session, sh.base);
-  bool more = true;
-  for (uint32_t j = 0; more; ++j) {
-    Item it;
-    while ((more = walk.next(a, it)) && it.k0 >= it.k1) {
-      Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
-      for (int x = lane; x < kCols; x += 32) {
-        part->m[x] = -INFINITY;
-        part->l[x] = 0.0f;
-      }
-    }
-    if (j >= kItems && !mbar_wait_for(&sh.item_free[j % kItems], ((j / kItems) - 1u) & 1u, &sh.dead)) {
-      sh.dead = 1;
-      return;
-    }
-    if (!more) it.k0 = it.k1 = 0;
-    if (lane == 0) {
-      sh.item[j % kItems] = it;
-      mbar_arrive(&sh.item_full[j % kItems]);
-    }
-    __syncwarp();
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendArgs a) {
-  using Sm = AttendSmem<D>;
+template <int D, int kCols>
+__global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_kernel(const AttendArgs a) {
+  using Sm = AttendSmem<D, kCols>;
+  using Sh = Shape<kCols>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* const s_q = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* const s_v = s_q + 2 * Sm::kQ;
-  unsigned char* const s_p = s_v + 2 * Sm::kV;
-  unsigned char* const s_c = s_p + 2 * Sm::kP;
-  __shared__ AttendShared sh;
+  unsigned char* const s_v = s_q + Sm::kQ;
+  unsigned char* const s_p = s_v + Sm::kV;
+  __shared__ AttendShared<kCols> sh;
 
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t cta = (int32_t)blockIdx.x;
@@ -894,54 +808,33 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const AttendA
     sh.session = b;
     sh.base = at;
   }
-  if (warp == 16) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 8) tmem_alloc(&sh.tmem, Sh::kTmemCols);
   if (tid == 0) {
-#pragma unroll
-    for (int e = 0; e < kItems; ++e) {
-      mbar_init(&sh.item_full[e], 1);
-      mbar_init(&sh.item_free[e], kItemReaders);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mbar_init(&sh.k_full[e], 4);   // a turning warp each
-      mbar_init(&sh.v_full[e], 4);
-      mbar_init(&sh.s_full[e], 1);   // the products themselves
-      mbar_init(&sh.pv_done[e], 1);
-      mbar_init(&sh.s_free[e], 8);   // a weighing warp each
-      mbar_init(&sh.p_full[e], 8);
-      mbar_init(&sh.q_full[e], 1);
-      mbar_init(&sh.q_free[e], 9);   // the item's last S product, and the weighing warps
-    }
-    mbar_init(&sh.o_free, 8);
-    mbar_init(&sh.drained[0], 1);
-    mbar_init(&sh.drained[1], 1);
+    mbar_init(&sh.k_full, kComputeThreads / 32);
+    mbar_init(&sh.s_full, 1);
+    mbar_init(&sh.p_full, 1);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.drained, 1);
     fence_barrier_init();
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh.tmem;
-  if (warp < 4) {
-    fewer_registers<kTurnRegs>();
-    turn_tokens<D, true>(a, sh, s_v, s_c, tmem);
-  } else if (warp < 8) {
-    fewer_registers<kTurnRegs>();
-    turn_tokens<D, false>(a, sh, s_v, s_c, tmem);
-  } else if (warp < 16) {
-    more_registers<kWeightRegs>();
-    weigh<D>(a, sh, s_p, tmem);
+  if (warp == 8) {
+    if (lane == 0) {
+      sh.walk.begin(a, line, sh.session, sh.base);
+      plan_item<D, kCols>(a, sh, 0);
+    }
+    __syncwarp();
+    multiply<D, kCols>(a, sh, s_q, s_v, s_p, tmem);
   } else {
-    fewer_registers<kRestRegs>();
-    if (warp == 19) plan_items<D>(a, sh, line);
-    else if (warp == 18) bring_queries<D>(a, sh, s_q);
-    else if (lane == 0 && warp == 16) multiply_keys<D>(sh, s_q, tmem);
-    else if (lane == 0) multiply_values<D>(sh, s_v, s_p, tmem);
+    attend_tiles<D, kCols>(a, sh, s_q, s_v, s_p, s_p + Sm::kP, tmem);
   }
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (tid == 0 && sh.dead != 0) atomicOr(a.error, 1u);
-  if (warp == 16) tmem_free(tmem, kTmemCols);
+  if (warp == 8) tmem_free(tmem, Sh::kTmemCols);
 }
 
 // ---- the joining of parts -----------------------------------------------------------------
@@ -949,7 +842,7 @@ constexpr int kJoinThreads = 256;
 
 // One warp per row and query head: a row of a refused session becomes zero, a row whose item was cut
 // is the parts' sum, a row that one CTA wrote is left.
-template <int D>
+template <int D, int kCols>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int64_t rows) {
   constexpr int kPer = D / 32;
   const int lane = (int)(threadIdx.x & 31u);
@@ -960,7 +853,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
       a.status[b] = SDCP_S_INTERNAL;
   const Line line(a.prefix[a.s.B], a.ctas);
   const int32_t share = a.q_heads / a.kv.heads;
-  const Part<D>* const parts = reinterpret_cast<const Part<D>*>(a.parts);
+  const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
   for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); at < rows * a.q_heads;
        at += (int64_t)gridDim.x * (kJoinThreads / 32)) {
     const int64_t row = quotient(at, a.q_heads);
@@ -987,7 +880,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
       m = warp_max(m);
       float sum = 0.0f;
       for (int32_t c = c_lo; c <= c_hi; ++c) {
-        const Part<D>& p = parts[c * 2 + (c == c_lo && line.first(c) < first ? 1 : 0)];
+        const Part<D, kCols>& p = parts[c * 2 + (c == c_lo && line.first(c) < first ? 1 : 0)];
         const float pm = p.m[j];
         if (pm == -INFINITY && p.l[j] == 0.0f) continue;  // nothing of the column in this part
         const float f = pm == m ? 1.0f : ex2(pm - m);
@@ -1014,30 +907,44 @@ struct AttendDevice {
   cudaError_t err = cudaSuccess;
 };
 AttendDevice g_attend_device[kMaxDevices];
+template <int D, int kCols> void set_shared(cudaError_t* e) {
+  if (*e == cudaSuccess)
+    *e = cudaFuncSetAttribute(attend_kernel<D, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AttendSmem<D, kCols>::kBytes);
+  if (*e == cudaSuccess) *e = cudaFuncSetAttribute(attend_kernel<D, kCols>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+}
 bool attend_ready() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   AttendDevice& d = g_attend_device[dev];
   std::call_once(d.once, [&] {
-    d.err = cudaFuncSetAttribute(attend_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AttendSmem<128>::kBytes);
-    if (d.err == cudaSuccess)
-      d.err = cudaFuncSetAttribute(attend_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AttendSmem<64>::kBytes);
-    if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(attend_kernel<128>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(attend_kernel<64>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    set_shared<128, 96>(&d.err);
+    set_shared<128, 32>(&d.err);
+    set_shared<64, 96>(&d.err);
+    set_shared<64, 32>(&d.err);
   });
   return d.err == cudaSuccess;
 }
 
-template <int D>
-cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st) {
+// Columns of an item: the small shape where a session has at most 32 on average.  Sessions with more
+// are cut into several items by either shape.
+int32_t columns_of(int32_t B, int64_t total, int32_t share) { return (total + B) * share <= (int64_t)32 * B ? 32 : 96; }
+
+template <int D, int kCols>
+cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
+  a.ctas = min(sms, kMaxSms) * Shape<kCols>::kCtas;
   attend_plan_kernel<<<(unsigned)a.s.B, kCheckThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(attend_kernel<D>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D>::kBytes, st, a);
+  e = launch_after(attend_kernel<D, kCols>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D, kCols>::kBytes, st, a);
   if (e != cudaSuccess) return e;
   const int64_t rows = a.s.total + a.s.B, warps = rows * a.q_heads;
   const int64_t blocks = min((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32), (int64_t)sms * 16);
-  return launch_after(attend_join_kernel<D>, (unsigned)blocks, kJoinThreads, 0, st, a, rows);
+  return launch_after(attend_join_kernel<D, kCols>, (unsigned)blocks, kJoinThreads, 0, st, a, rows);
+}
+
+template <int D>
+size_t parts_bytes(int32_t cols) {
+  return cols == 32 ? sizeof(Part<D, 32>) * kMaxSms * Shape<32>::kCtas * 2 : sizeof(Part<D, 96>) * kMaxSms * Shape<96>::kCtas * 2;
 }
 
 }  // namespace
@@ -1049,8 +956,9 @@ extern "C" size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, i
                                               int32_t kv_heads, int32_t head_dim) {
   if (B < 0 || total_drafts < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
+  const int32_t cols = columns_of(B, total_drafts, q_heads / kv_heads);
   return kHeader + round256((size_t)B * sizeof(SessionPlan)) + round256(((size_t)B * 2 + 1) * sizeof(int64_t)) +
-         (size_t)kMaxCtas * 2 * (head_dim == 128 ? sizeof(Part<128>) : sizeof(Part<64>));
+         (head_dim == 128 ? parts_bytes<128>(cols) : parts_bytes<64>(cols));
 }
 
 extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
@@ -1081,8 +989,10 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
                      static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), units,
                      reinterpret_cast<SessionPlan*>(plans), units + B,
                      reinterpret_cast<float*>(lines + round256(((size_t)B * 2 + 1) * sizeof(int64_t))),
-                     min(di.sms, kMaxCtas)};
+                     0, columns_of(B, total_drafts, q_heads / cache->kv_heads)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 128 ? launch_attend<128>(a, di.sms, st) : launch_attend<64>(a, di.sms, st);
+  cudaError_t e;
+  if (D == 128) e = a.cols == 32 ? launch_attend<128, 32>(a, di.sms, st) : launch_attend<128, 96>(a, di.sms, st);
+  else e = a.cols == 32 ? launch_attend<64, 32>(a, di.sms, st) : launch_attend<64, 96>(a, di.sms, st);
   return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
 }
