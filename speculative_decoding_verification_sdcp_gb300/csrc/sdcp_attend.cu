@@ -180,12 +180,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const
   }
   return false;
 }
-// A shared-memory matrix of 128-byte swizzled atoms (8 rows of 128 bytes).  lead: bytes between
-// atoms along the contiguous dimension (used where that is not the product's inner one); step:
-// bytes between atoms along the other.
-__device__ __forceinline__ uint64_t smem_matrix(const void* p, uint32_t lead, uint32_t step) {
+// A shared-memory matrix of swizzled atoms (8 rows of 128 or 64 bytes).  lead: bytes between atoms
+// along the contiguous dimension (used where that is not the product's inner one); step: bytes
+// between atoms along the other.
+constexpr uint64_t kSwizzle128 = (uint64_t)2 << 61, kSwizzle64 = (uint64_t)4 << 61;
+__device__ __forceinline__ uint64_t smem_matrix(const void* p, uint32_t lead, uint32_t step, uint64_t swizzle) {
   return (uint64_t)((smem_u32(p) & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(step >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
+         swizzle;
 }
 constexpr uint32_t kIdescF32 = 1u << 4, kIdescBf16 = 1u << 7 | 1u << 10, kIdescTransposeBoth = 1u << 15 | 1u << 16, kIdescM128 = 8u << 24;
 
@@ -285,7 +286,8 @@ template <int D, int kCols> struct AttendSmem {
   static constexpr int kAtoms = D / 64;                        // 128-byte atoms along the channels
   static constexpr int kQ = kAtoms * kCols * 128;              // queries: [atom][column][128 bytes]
   static constexpr int kV = kAtoms * kTile * 128;              // values: [atom][token][128 bytes]
-  static constexpr int kP = (kCols + 63) / 64 * kTile * 128;   // weights: [atom of 64 columns][token][128 bytes]
+  static constexpr bool kNarrow = kCols == 32;                 // weights: [token][64 bytes], swizzled in 64 bytes,
+  static constexpr int kP = kNarrow ? kTile * 64 : (kCols + 63) / 64 * kTile * 128;  // or [atom of 64 columns][token][128 bytes]
   static constexpr int kC = 2 * kTile * (D / 2 + 8);           // codes and scales of the next keys and values
   static constexpr size_t kBytes = (size_t)kQ + kV + kP + kC + 1024;  // and the alignment to 1024
 };
@@ -416,8 +418,10 @@ __device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols
                                          const unsigned char* s_p, uint32_t tmem) {
   using Sm = AttendSmem<D, kCols>;
   using Sh = Shape<kCols>;
-  const uint64_t q_mat = smem_matrix(s_q, 0, 1024), v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024),
-                 p_mat = smem_matrix(s_p, kTile * 128, 1024);
+  constexpr uint32_t kPRow = Sm::kNarrow ? 64 : 128;
+  const uint64_t q_mat = smem_matrix(s_q, 0, 1024, kSwizzle128),
+                 v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024, kSwizzle128),
+                 p_mat = smem_matrix(s_p, kTile * kPRow, 8 * kPRow, Sm::kNarrow ? kSwizzle64 : kSwizzle128);
   uint32_t i = 0;
   for (uint32_t j = 0;; ++j) {
     __syncthreads();  // item j is planned, and the previous one is done with
@@ -447,7 +451,7 @@ __device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols
         fence_after();
 #pragma unroll
         for (int x = 0; x < kTile / 16; ++x)
-          mma_smem_a(tmem + Sh::kTmemO, v_mat + (uint64_t)(x * 2048 >> 4), p_mat + (uint64_t)(x * 2048 >> 4), idesc | kIdescTransposeBoth,
+          mma_smem_a(tmem + Sh::kTmemO, v_mat + (uint64_t)(x * 2048 >> 4), p_mat + (uint64_t)(x * 16 * kPRow >> 4), idesc | kIdescTransposeBoth,
                      k > 0 || x > 0);
         mma_commit(&sh.pv_done);
       }
@@ -472,7 +476,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
   const uint32_t swizzled = (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);
   // values: channels (wg * kOwn + g) * 32 of the token; weights: block 2 cb + wg of eight columns
   const uint32_t v_at = smem_u32(s_v) + (D == 128 ? (uint32_t)(wg * kTile * 128) + swizzled : swizzled ^ ((uint32_t)wg << 6));
-  const uint32_t p_at = smem_u32(s_p) + (swizzled ^ ((uint32_t)wg << 4));
+  const uint32_t p_at =
+      smem_u32(s_p) + (Sm::kNarrow ? (uint32_t)(tok * 64) + ((uint32_t)(wg ^ ((tok >> 1) & 3)) << 4) : swizzled ^ ((uint32_t)wg << 4));
   const uint32_t s_at = my_lanes + Sh::kTmemS + (uint32_t)(wg * 8);
   auto meet = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
   auto any = [](bool p) {
@@ -917,10 +922,10 @@ bool attend_ready() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   AttendDevice& d = g_attend_device[dev];
   std::call_once(d.once, [&] {
-    set_shared<128, 96>(&d.err);
-    set_shared<128, 32>(&d.err);
-    set_shared<64, 96>(&d.err);
     set_shared<64, 32>(&d.err);
+    set_shared<64, 96>(&d.err);
+    set_shared<128, 32>(&d.err);
+    set_shared<128, 96>(&d.err);
   });
   return d.err == cudaSuccess;
 }
