@@ -1,14 +1,17 @@
 // sdcp_logits.cu - sdcp_adjust_logits: penalties for repeated tokens, biases and grammar masks
 // on the rows of a ragged batch.
 //
-// A CTA owns a slice of the vocabulary of one session and handles that slice of all the session's
-// rows: the history is the same for every row, so the slice's occurrence counts are built once, in
-// shared memory, and used M + 1 times.  Row i also counts the drafts x[0 .. i-1]; the few of them
-// that fall into the slice are kept as a list, which only tokens that are listed look at.
-//
 //   z = l;  seen: z = z > 0 ? z / r : z * r;  z -= f c;  c > 0: z -= p;  z += bias;  masked: -inf
 //
-// Everything else is a copy, in 16-byte blocks of memory.
+// A CTA owns a slice of the vocabulary of one session, for all its rows: the history is the same
+// for every row, so the slice's occurrence counts are built once, in shared memory.  Row i also
+// counts the drafts x[0 .. i-1]; the few that fall into the slice are kept as a list.
+//
+// It is bound by memory: every logit is read and written once (in place: only what changes).  So the
+// rows are first streamed with their masks alone, in 16-byte blocks, and the few tokens that a
+// penalty or a bias applies to are written again, from a list of them in rising order, after a
+// barrier: the second write meets lines that are still in L2.  With the arithmetic inside the
+// streaming loop (unrolled over a block's elements) the kernel starved for instructions.
 #include <climits>
 
 #include "sdcp_device.cuh"
@@ -51,46 +54,11 @@ struct SliceDraft {
   int32_t pos;
 };
 
-// What the slow path needs about one row.
-struct RowView {
-  const uint32_t* mask;  // the row's mask words, or null
-  int32_t i;             // drafts before this row
-};
-
 template <typename T> __device__ __forceinline__ T from_float(float x);
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-struct Slice {
-  const uint32_t* words;   // [slice] kInPrompt | outputs
-  const float* bias;       // [slice], or null
-  const uint32_t* touched; // a bit per 8 tokens: something may apply to one of them
-  const SliceDraft* drafts;
-  int32_t n_drafts;
-  float rep, freq, pres;
-};
-
-// The logit of token `at` (relative to the slice) of a row, `keep` = its mask bit.
-template <typename T>
-__device__ __forceinline__ T adjust_one(const Slice& s, int32_t at, int32_t i, bool keep, T l) {
-  if (!keep) return from_float<T>(__uint_as_float(0xFF800000u));
-  const uint32_t w = s.words[at];
-  uint32_t c = w & kCountMask;
-  for (int k = 0; k < s.n_drafts; ++k) c += (s.drafts[k].at == at && s.drafts[k].pos < i) ? 1u : 0u;
-  const bool seen = (w & kInPrompt) != 0u || c != 0u;
-  const float b = s.bias ? s.bias[at] : 0.0f;
-  if (!seen && b == 0.0f) return l;
-  float z = to_float(l);
-  if (seen) z = z > 0.0f ? __fdiv_rn(z, s.rep) : __fmul_rn(z, s.rep);
-  if (c != 0u) {
-    z = __fsub_rn(z, __fmul_rn(s.freq, (float)c));
-    z = __fsub_rn(z, s.pres);
-  }
-  z = __fadd_rn(z, b);
-  return from_float<T>(z);
-}
 
 // E mask bits from token t on (t + E - 1 < V), 1 = may be chosen.
 template <int E>
@@ -101,13 +69,35 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* mask, int64_t t) {
   return w & ((1u << E) - 1u);
 }
 
+// A block of E logits with -inf where its mask bit is clear.
+__device__ __forceinline__ uint4 masked_block(uint4 q, uint32_t keep, const float*) {
+  const uint32_t ninf = 0xFF800000u;
+  return make_uint4(keep & 1u ? q.x : ninf, keep & 2u ? q.y : ninf, keep & 4u ? q.z : ninf, keep & 8u ? q.w : ninf);
+}
+__device__ __forceinline__ uint32_t masked_pair(uint32_t w, uint32_t keep) {
+  const uint32_t lo = keep & 1u ? w & 0xFFFFu : 0xFF80u, hi = keep & 2u ? w & 0xFFFF0000u : 0xFF800000u;
+  return lo | hi;
+}
+__device__ __forceinline__ uint4 masked_block(uint4 q, uint32_t keep, const __nv_bfloat16*) {
+  return make_uint4(masked_pair(q.x, keep), masked_pair(q.y, keep >> 2), masked_pair(q.z, keep >> 4), masked_pair(q.w, keep >> 6));
+}
+
+// Shared memory of a CTA, for a slice of n tokens: words [n] (kInPrompt | outputs), marks [n / 32] (a
+// bit a token that something applies to), listed [n] (those tokens, rising), bias [n] where there are any.
+__host__ __device__ constexpr size_t adjust_smem(int32_t slice, bool biased) {
+  return (size_t)slice * 4 + (size_t)slice / 8 + (size_t)slice * 2 + (biased ? (size_t)slice * 4 : 0);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a) {
   constexpr int E = Elem<T>::kPerVec;
+  constexpr uint32_t kAll = (1u << E) - 1u;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ SliceDraft s_drafts[SDCP_MAX_M];
   __shared__ int32_t s_ndrafts;
-  const int tid = (int)threadIdx.x;
+  __shared__ int32_t s_mask[SDCP_MAX_M + 1];  // the rows' masks, -1: none
+  __shared__ int32_t s_sum[kAdjThreads / 32];
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.n_slices);
   const int32_t part = (int32_t)(blockIdx.x % (uint32_t)a.n_slices);
   const int64_t v0 = (int64_t)part * a.slice;
@@ -115,6 +105,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
 
   // the session: offsets, controls, masks and biases, checked by every CTA of it
   const int32_t lo = a.m_offsets[b], hi = a.m_offsets[b + 1];
+  const sdcp_logit_controls ctl = a.controls[b];
   if (lo < 0 || hi < lo || (int64_t)hi > a.total) {
     if (part == 0 && tid == 0) a.status[b] = SDCP_S_BAD_PARAMS;
     return;
@@ -122,145 +113,163 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
   const int32_t M = hi - lo;
   const int32_t rows = M + a.extra;
   const int64_t row0 = (int64_t)lo + (int64_t)b * a.extra;
-  const sdcp_logit_controls ctl = a.controls[b];
-  bool bad = !(ctl.repetition > 0.0f && ctl.repetition < INFINITY) || !isfinite(ctl.frequency) ||
-             !isfinite(ctl.presence) || (int64_t)ctl.history_len > a.history_stride ||
-             ctl.prompt_len > ctl.history_len || (int64_t)ctl.bias_offset + ctl.bias_count > a.n_bias;
-  if (M <= SDCP_MAX_M && !bad) {
-    if (a.mask_rows != nullptr)
-      for (int i = tid; i < rows; i += kAdjThreads) {
-        const int32_t r = a.mask_rows[row0 + i];
-        bad |= r < -1 || (int64_t)r >= a.n_masks;
+  const T* const in = static_cast<const T*>(a.logits) + row0 * a.V + v0;
+  T* const out = static_cast<T*>(a.out) + row0 * a.V + v0;
+  bool bad = M > SDCP_MAX_M || !(ctl.repetition > 0.0f && ctl.repetition < INFINITY) || !isfinite(ctl.frequency) ||
+             !isfinite(ctl.presence) || (int64_t)ctl.history_len > a.history_stride || ctl.prompt_len > ctl.history_len ||
+             (int64_t)ctl.bias_offset + ctl.bias_count > a.n_bias;
+
+  if (!bad) {
+    uint32_t* const words = reinterpret_cast<uint32_t*>(smem);
+    uint32_t* const marks = words + a.slice;
+    uint16_t* const listed = reinterpret_cast<uint16_t*>(marks + a.slice / 32);
+    float* const bias = reinterpret_cast<float*>(listed + a.slice);
+    const bool has_bias = ctl.bias_count != 0u;
+    for (int k = tid; k < a.slice / 4; k += kAdjThreads) reinterpret_cast<uint4*>(words)[k] = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = tid; k < a.slice / 32; k += kAdjThreads) marks[k] = 0u;
+    if (has_bias)
+      for (int k = tid; k < a.slice / 4; k += kAdjThreads) reinterpret_cast<uint4*>(bias)[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_ndrafts = 0;
+    for (int i = tid; i < rows; i += kAdjThreads) {
+      int32_t r = a.mask_rows ? a.mask_rows[row0 + i] : -1;
+      if (r < -1 || (int64_t)r >= a.n_masks) {
+        bad = true;
+        r = -1;
       }
+      s_mask[i] = r;
+    }
+    __syncthreads();
+
+    // the slice's counts, biases and drafts (their loads are on the way while the rows stream)
+    const int32_t* const hist = a.history + (int64_t)b * a.history_stride;
+    for (uint32_t k = tid; k < ctl.history_len; k += kAdjThreads) {
+      const uint32_t at = (uint32_t)((int64_t)hist[k] - v0);
+      if (at < (uint32_t)n) {
+        if (k < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
+        else atomicAdd(&words[at], 1u);
+        atomicOr(&marks[at >> 5], 1u << (at & 31u));
+      }
+    }
     for (uint32_t k = tid; k < ctl.bias_count; k += kAdjThreads) {
       const int32_t t = a.bias_tokens[ctl.bias_offset + k];
       const int32_t before = k ? a.bias_tokens[ctl.bias_offset + k - 1] : -1;
       bad |= t <= before || (int64_t)t >= a.V;
-    }
-  }
-
-  uint32_t* words = reinterpret_cast<uint32_t*>(smem);
-  uint32_t* touched = words + a.slice;
-  float* bias = reinterpret_cast<float*>(touched + a.slice / 256);
-  const bool has_bias = ctl.bias_count != 0u;
-  for (int k = tid; k < a.slice; k += kAdjThreads) {
-    words[k] = 0u;
-    if (has_bias) bias[k] = 0.0f;
-  }
-  for (int k = tid; k < a.slice / 256; k += kAdjThreads) touched[k] = 0u;
-  if (tid == 0) s_ndrafts = 0;
-  const int32_t st = M > SDCP_MAX_M ? SDCP_S_LIMIT : __syncthreads_or(bad) ? SDCP_S_BAD_PARAMS : SDCP_S_OK;
-  if (part == 0 && tid == 0) a.status[b] = st;
-
-  const T* in = static_cast<const T*>(a.logits) + row0 * a.V + v0;
-  T* out = static_cast<T*>(a.out) + row0 * a.V + v0;
-  if (st != SDCP_S_OK) {
-    const T nan = from_float<T>(__uint_as_float(0x7FC00000u));
-    for (int i = 0; i < rows; ++i)
-      for (int k = tid; k < n; k += kAdjThreads) out[(int64_t)i * a.V + k] = nan;
-    return;
-  }
-
-  // the slice's counts, biases and drafts
-  const int32_t* hist = a.history + (int64_t)b * a.history_stride;
-  for (uint32_t k = tid; k < ctl.history_len; k += kAdjThreads) {
-    const uint32_t at = (uint32_t)((int64_t)hist[k] - v0);
-    if (at < (uint32_t)n) {
-      if (k < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
-      else atomicAdd(&words[at], 1u);
-      atomicOr(&touched[at >> 8], 1u << ((at >> 3) & 31u));
-    }
-  }
-  for (uint32_t k = tid; k < ctl.bias_count; k += kAdjThreads) {
-    const uint32_t at = (uint32_t)((int64_t)a.bias_tokens[ctl.bias_offset + k] - v0);
-    if (at < (uint32_t)n) {
-      bias[at] = a.bias_values[ctl.bias_offset + k];
-      atomicOr(&touched[at >> 8], 1u << ((at >> 3) & 31u));
-    }
-  }
-  for (int k = tid; k < M; k += kAdjThreads) {
-    const uint32_t at = (uint32_t)((int64_t)a.tokens[lo + k] - v0);
-    if (at < (uint32_t)n) {
-      s_drafts[atomicAdd(&s_ndrafts, 1)] = SliceDraft{(int32_t)at, k};
-      atomicOr(&touched[at >> 8], 1u << ((at >> 3) & 31u));
-    }
-  }
-  __syncthreads();
-
-  const Slice s{words, has_bias ? bias : nullptr, touched, s_drafts, s_ndrafts, ctl.repetition, ctl.frequency, ctl.presence};
-  const bool in_place = a.logits == a.out;
-
-  // The slice of a row is cut at 16-byte boundaries of memory: block k covers the tokens from
-  // k E - lead on, the first and the last may be partial.  Rows whose two addresses differ modulo
-  // 16 go element by element.
-  const int32_t slots = (n + E - 1) / E + 1;
-  int32_t i = 0, k = tid;
-  while (k >= slots) { k -= slots; ++i; }
-  while (i < rows) {
-    uint4 q[kAdjUnroll];
-    int32_t ui[kAdjUnroll], ut[kAdjUnroll];  // row, first token (relative to the slice)
-    uint32_t keep[kAdjUnroll];               // mask bits of a whole block
-    int kind[kAdjUnroll];                    // 0: nothing to do, 1: a whole block, 2: element by element
-#pragma unroll
-    for (int u = 0; u < kAdjUnroll; ++u) {
-      kind[u] = 0;
-      ui[u] = i;
-      if (i < rows) {
-        const T* pr = in + (int64_t)i * a.V;
-        const T* po = out + (int64_t)i * a.V;
-        const int32_t lead = (int32_t)(((uintptr_t)pr & 15u) / sizeof(T));
-        const int32_t t = k * E - lead;
-        ut[u] = t;
-        if (t < n) {
-          const bool whole = t >= 0 && t + E <= n && (((uintptr_t)pr ^ (uintptr_t)po) & 15u) == 0;
-          kind[u] = whole ? 1 : 2;
-          if (whole) {
-            const int32_t mr = a.mask_rows ? a.mask_rows[row0 + i] : -1;
-            keep[u] = mr < 0 ? (1u << E) - 1u : mask_bits<E>(a.masks + (int64_t)mr * a.mask_stride, v0 + t);
-            const uint32_t t1 = touched[t >> 8] >> ((t >> 3) & 31);
-            const int32_t e = t + E - 1;
-            const uint32_t any = (t1 | (touched[e >> 8] >> ((e >> 3) & 31))) & 1u;
-            keep[u] |= any << 31;
-            if (in_place && any == 0u && keep[u] == (1u << E) - 1u) kind[u] = 0;
-            else q[u] = *reinterpret_cast<const uint4*>(pr + t);
-          }
-        }
-        k += kAdjThreads;
-        while (k >= slots) { k -= slots; ++i; }
+      const uint32_t at = (uint32_t)((int64_t)t - v0);
+      if (at < (uint32_t)n) {
+        bias[at] = a.bias_values[ctl.bias_offset + k];
+        atomicOr(&marks[at >> 5], 1u << (at & 31u));
       }
     }
+    for (int k = tid; k < M; k += kAdjThreads) {
+      const uint32_t at = (uint32_t)((int64_t)a.tokens[lo + k] - v0);
+      if (at < (uint32_t)n) {
+        s_drafts[atomicAdd(&s_ndrafts, 1)] = SliceDraft{(int32_t)at, k};
+        atomicOr(&marks[at >> 5], 1u << (at & 31u));
+      }
+    }
+
+    // The rows and their masks.  The slice of a row is cut at 16-byte boundaries of memory: block k
+    // covers the tokens from k E - lead on, the first and the last may be partial.  Rows whose two
+    // addresses differ modulo 16 go element by element.
+    const bool in_place = a.logits == a.out;
+    const int32_t slots = (n + E - 1) / E + 1;
+    int32_t i = 0, k = tid;
+    while (k >= slots) { k -= slots; ++i; }
+    while (i < rows) {
+      uint4 q[kAdjUnroll];
+      T* to[kAdjUnroll];           // null: nothing to write
+      uint32_t keep[kAdjUnroll];
 #pragma unroll
-    for (int u = 0; u < kAdjUnroll; ++u) {
-      const T* pr = in + (int64_t)ui[u] * a.V;
-      T* po = out + (int64_t)ui[u] * a.V;
-      if (kind[u] == 1) {
-        T* e = reinterpret_cast<T*>(&q[u]);
-        if (keep[u] != (1u << E) - 1u) {
-          if (keep[u] >> 31) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) e[j] = adjust_one<T>(s, ut[u] + j, ui[u], (keep[u] >> j) & 1u, e[j]);
+      for (int u = 0; u < kAdjUnroll; ++u) {
+        to[u] = nullptr;
+        if (i < rows) {
+          const T* const pr = in + (int64_t)i * a.V;
+          T* const po = out + (int64_t)i * a.V;
+          const int32_t t = k * E - (int32_t)(((uintptr_t)pr & 15u) / sizeof(T));
+          const int32_t mr = s_mask[i];
+          const uint32_t* const mask = a.masks + (int64_t)mr * a.mask_stride;
+          if (t >= 0 && t + E <= n && (((uintptr_t)pr ^ (uintptr_t)po) & 15u) == 0) {
+            keep[u] = mr < 0 ? kAll : mask_bits<E>(mask, v0 + t);
+            if (!in_place || keep[u] != kAll) {
+              to[u] = po + t;
+              q[u] = *reinterpret_cast<const uint4*>(pr + t);
+            }
           } else {
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-              if (!((keep[u] >> j) & 1u)) e[j] = from_float<T>(__uint_as_float(0xFF800000u));
+#pragma unroll 1
+            for (int32_t e = max(t, 0); e < min(t + E, n); ++e)
+              po[e] = mr < 0 || mask_bits<1>(mask, v0 + e) != 0u ? pr[e] : from_float<T>(__uint_as_float(0xFF800000u));
           }
+          k += kAdjThreads;
+          while (k >= slots) { k -= slots; ++i; }
         }
-        *reinterpret_cast<uint4*>(po + ut[u]) = q[u];
-      } else if (kind[u] == 2) {
-        const int32_t mr = a.mask_rows ? a.mask_rows[row0 + ui[u]] : -1;
-        const uint32_t* mask = mr < 0 ? nullptr : a.masks + (int64_t)mr * a.mask_stride;
-        for (int32_t t = max(ut[u], 0); t < min(ut[u] + E, n); ++t) {
-          const bool keep1 = mask == nullptr || mask_bits<1>(mask, v0 + t) != 0u;
-          po[t] = adjust_one<T>(s, t, ui[u], keep1, pr[t]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAdjUnroll; ++u)
+        if (to[u] != nullptr)
+          *reinterpret_cast<uint4*>(to[u]) = keep[u] == kAll ? q[u] : masked_block(q[u], keep[u], static_cast<const T*>(nullptr));
+    }
+    bad = __syncthreads_or(bad) != 0;
+
+    if (!bad) {
+      // the marked tokens, rising: a stretch of the marks per thread, and their number before it
+      const int per = (a.slice / 32 + kAdjThreads - 1) / kAdjThreads, w0 = min(tid * per, a.slice / 32), w1 = min(w0 + per, a.slice / 32);
+      int32_t mine = 0;
+      for (int w = w0; w < w1; ++w) mine += __popc(marks[w]);
+      int32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      int32_t at = incl - mine, total = 0;
+#pragma unroll
+      for (int w = 0; w < kAdjThreads / 32; ++w) {
+        if (w < warp) at += s_sum[w];
+        total += s_sum[w];
+      }
+      for (int w = w0; w < w1; ++w)
+        for (uint32_t m = marks[w]; m != 0u; m &= m - 1u) listed[at++] = (uint16_t)(w * 32 + __ffs((int)m) - 1);
+      __syncthreads();
+
+      // their logits, row after row
+      const int32_t nd = s_ndrafts;
+      const float rep = ctl.repetition, freq = ctl.frequency, pres = ctl.presence;
+      for (int32_t r = 0; r < rows; ++r) {
+        const T* const pr = in + (int64_t)r * a.V;
+        T* const po = out + (int64_t)r * a.V;
+        const int32_t mr = s_mask[r];
+        const uint32_t* const mask = a.masks + (int64_t)mr * a.mask_stride;
+#pragma unroll 1
+        for (int32_t x = tid; x < total; x += kAdjThreads) {
+          const int32_t t = listed[x];
+          if (mr >= 0 && mask_bits<1>(mask, v0 + t) == 0u) continue;
+          const uint32_t w = words[t];
+          uint32_t c = w & kCountMask;
+          for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
+          const bool seen = (w & kInPrompt) != 0u || c != 0u;
+          const float bt = has_bias ? bias[t] : 0.0f;
+          if (!seen && bt == 0.0f) continue;
+          float z = to_float(pr[t]);
+          if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+          if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
+          po[t] = from_float<T>(__fadd_rn(z, bt));
         }
       }
     }
+  }
+  if (part == 0 && tid == 0) a.status[b] = M > SDCP_MAX_M ? SDCP_S_LIMIT : bad ? SDCP_S_BAD_PARAMS : SDCP_S_OK;
+  if (bad) {
+    const T nan = from_float<T>(__uint_as_float(0x7FC00000u));
+    for (int r = 0; r < rows; ++r)
+      for (int k = tid; k < n; k += kAdjThreads) out[(int64_t)r * a.V + k] = nan;
   }
 }
 
 template <typename T>
 cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
-  const size_t smem = (size_t)a.slice * 4 + (size_t)a.slice / 256 * 4 + (a.n_bias > 0 ? (size_t)a.slice * 4 : 0);
+  const size_t smem = adjust_smem(a.slice, a.n_bias > 0);
   adjust_kernel<T><<<(unsigned)a.B * (unsigned)a.n_slices, kAdjThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
