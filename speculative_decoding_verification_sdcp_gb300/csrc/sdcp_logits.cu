@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ SliceDraft s_drafts[SDCP_MAX_M];
   __shared__ int32_t s_ndrafts;
-  __shared__ int32_t s_mask[SDCP_MAX_M + 1];  // the rows' masks, -1: none
+  __shared__ const uint32_t* s_mask[SDCP_MAX_M + 1];  // the rows' masks, null: none
   __shared__ int32_t s_sum[kAdjThreads / 32];
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.n_slices);
@@ -136,14 +136,14 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
         bad = true;
         r = -1;
       }
-      s_mask[i] = r;
+      s_mask[i] = r < 0 ? nullptr : a.masks + (int64_t)r * a.mask_stride;
     }
     __syncthreads();
 
     // the slice's counts, biases and drafts (their loads are on the way while the rows stream)
     const int32_t* const hist = a.history + (int64_t)b * a.history_stride;
     for (uint32_t k = tid; k < ctl.history_len; k += kAdjThreads) {
-      const uint32_t at = (uint32_t)((int64_t)hist[k] - v0);
+      const uint32_t at = (uint32_t)hist[k] - (uint32_t)v0;  // beyond the slice: >= n
       if (at < (uint32_t)n) {
         if (k < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
         else atomicAdd(&words[at], 1u);
@@ -169,44 +169,55 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
     }
 
     // The rows and their masks.  The slice of a row is cut at 16-byte boundaries of memory: block k
-    // covers the tokens from k E - lead on, the first and the last may be partial.  Rows whose two
-    // addresses differ modulo 16 go element by element.
+    // covers the tokens k E - lead .. k E - lead + E - 1 of the row, the first and the last may be
+    // partial.  A thread keeps its blocks and goes down the rows, four at a time.
     const bool in_place = a.logits == a.out;
-    const int32_t slots = (n + E - 1) / E + 1;
-    int32_t i = 0, k = tid;
-    while (k >= slots) { k -= slots; ++i; }
-    while (i < rows) {
-      uint4 q[kAdjUnroll];
-      T* to[kAdjUnroll];           // null: nothing to write
-      uint32_t keep[kAdjUnroll];
+    const bool alike = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
+    const int32_t lead0 = (int32_t)(((uintptr_t)in & 15u) / sizeof(T)), step = (int32_t)(a.V & (E - 1));
+    const int32_t blocks = alike ? (n + E - 1) / E + 1 : 0;
+    for (int32_t k = tid; k < blocks; k += kAdjThreads) {
+      const T* pr = in + k * E;
+      int32_t lead = lead0;
+      for (int32_t i = 0; i < rows; i += kAdjUnroll) {
+        uint4 q[kAdjUnroll];
+        T* to[kAdjUnroll];  // null: nothing to write
+        uint32_t keep[kAdjUnroll];
 #pragma unroll
-      for (int u = 0; u < kAdjUnroll; ++u) {
-        to[u] = nullptr;
-        if (i < rows) {
-          const T* const pr = in + (int64_t)i * a.V;
-          T* const po = out + (int64_t)i * a.V;
-          const int32_t t = k * E - (int32_t)(((uintptr_t)pr & 15u) / sizeof(T));
-          const int32_t mr = s_mask[i];
-          const uint32_t* const mask = a.masks + (int64_t)mr * a.mask_stride;
-          if (t >= 0 && t + E <= n && (((uintptr_t)pr ^ (uintptr_t)po) & 15u) == 0) {
-            keep[u] = mr < 0 ? kAll : mask_bits<E>(mask, v0 + t);
+        for (int u = 0; u < kAdjUnroll; ++u) {
+          const int32_t t = k * E - lead;
+          const T* const from = pr - lead;
+          to[u] = nullptr;
+          if (i + u < rows && t >= 0 && t + E <= n) {
+            const uint32_t* const mask = s_mask[i + u];
+            keep[u] = mask == nullptr ? kAll : mask_bits<E>(mask, v0 + t);
             if (!in_place || keep[u] != kAll) {
-              to[u] = po + t;
-              q[u] = *reinterpret_cast<const uint4*>(pr + t);
+              to[u] = out + (from - in);
+              q[u] = *reinterpret_cast<const uint4*>(from);
             }
-          } else {
-#pragma unroll 1
-            for (int32_t e = max(t, 0); e < min(t + E, n); ++e)
-              po[e] = mr < 0 || mask_bits<1>(mask, v0 + e) != 0u ? pr[e] : from_float<T>(__uint_as_float(0xFF800000u));
           }
-          k += kAdjThreads;
-          while (k >= slots) { k -= slots; ++i; }
+          pr += a.V;
+          lead = (lead + step) & (E - 1);
         }
-      }
 #pragma unroll
-      for (int u = 0; u < kAdjUnroll; ++u)
-        if (to[u] != nullptr)
-          *reinterpret_cast<uint4*>(to[u]) = keep[u] == kAll ? q[u] : masked_block(q[u], keep[u], static_cast<const T*>(nullptr));
+        for (int u = 0; u < kAdjUnroll; ++u)
+          if (to[u] != nullptr)
+            *reinterpret_cast<uint4*>(to[u]) = keep[u] == kAll ? q[u] : masked_block(q[u], keep[u], static_cast<const T*>(nullptr));
+      }
+    }
+    // what the blocks left: the ends of the rows, or all of them where the two addresses differ modulo 16
+    const int32_t ends = alike ? 2 * E : n;
+    for (int32_t x = tid; x < rows * ends; x += kAdjThreads) {
+      const int32_t i = x / ends, e = x - i * ends;
+      int32_t t = e;
+      if (alike) {
+        const int32_t lead = (int32_t)((lead0 + (int64_t)i * step) & (E - 1));
+        const int32_t head = (E - lead) & (E - 1), tail = head + (max(n - head, 0) / E) * E;  // [head, tail) is in blocks
+        t = e < E ? e : tail + e - E;
+        if ((e < E ? t >= head : t < head) || t >= n) continue;
+      }
+      const uint32_t* const mask = s_mask[i];
+      const bool keep = mask == nullptr || mask_bits<1>(mask, v0 + t) != 0u;
+      if (!in_place || !keep) out[(int64_t)i * a.V + t] = keep ? in[(int64_t)i * a.V + t] : from_float<T>(__uint_as_float(0xFF800000u));
     }
     bad = __syncthreads_or(bad) != 0;
 
@@ -233,29 +244,25 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
         for (uint32_t m = marks[w]; m != 0u; m &= m - 1u) listed[at++] = (uint16_t)(w * 32 + __ffs((int)m) - 1);
       __syncthreads();
 
-      // their logits, row after row
+      // their logits, in every row
       const int32_t nd = s_ndrafts;
       const float rep = ctl.repetition, freq = ctl.frequency, pres = ctl.presence;
-      for (int32_t r = 0; r < rows; ++r) {
-        const T* const pr = in + (int64_t)r * a.V;
-        T* const po = out + (int64_t)r * a.V;
-        const int32_t mr = s_mask[r];
-        const uint32_t* const mask = a.masks + (int64_t)mr * a.mask_stride;
 #pragma unroll 1
-        for (int32_t x = tid; x < total; x += kAdjThreads) {
-          const int32_t t = listed[x];
-          if (mr >= 0 && mask_bits<1>(mask, v0 + t) == 0u) continue;
-          const uint32_t w = words[t];
-          uint32_t c = w & kCountMask;
-          for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
-          const bool seen = (w & kInPrompt) != 0u || c != 0u;
-          const float bt = has_bias ? bias[t] : 0.0f;
-          if (!seen && bt == 0.0f) continue;
-          float z = to_float(pr[t]);
-          if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-          if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
-          po[t] = from_float<T>(__fadd_rn(z, bt));
-        }
+      for (int32_t x = tid; x < rows * total; x += kAdjThreads) {
+        const int32_t r = x / total, t = listed[x - r * total];
+        const uint32_t* const mask = s_mask[r];
+        if (mask != nullptr && mask_bits<1>(mask, v0 + t) == 0u) continue;
+        const uint32_t w = words[t];
+        uint32_t c = w & kCountMask;
+        for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
+        const bool seen = (w & kInPrompt) != 0u || c != 0u;
+        const float bt = has_bias ? bias[t] : 0.0f;
+        if (!seen && bt == 0.0f) continue;
+        const int64_t at_row = (int64_t)r * a.V + t;
+        float z = to_float(in[at_row]);
+        if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+        if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
+        out[at_row] = from_float<T>(__fadd_rn(z, bt));
       }
     }
   }
