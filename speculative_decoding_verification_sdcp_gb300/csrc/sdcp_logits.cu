@@ -20,7 +20,8 @@ namespace sdcp {
 namespace {
 
 constexpr int kAdjThreads = 256;
-constexpr int kAdjUnroll = 4;             // blocks a thread has in flight
+constexpr int kAdjUnroll = 8;             // blocks a thread has in flight
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kInPrompt = 1u << 31;  // of a slice's word: the token is in the prompt
 constexpr uint32_t kCountMask = ~kInPrompt;
 
@@ -130,78 +131,94 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
     if (has_bias)
       for (int k = tid; k < a.slice / 4; k += kAdjThreads) reinterpret_cast<uint4*>(bias)[k] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) s_ndrafts = 0;
-    for (int i = tid; i < rows; i += kAdjThreads) {
-      int32_t r = a.mask_rows ? a.mask_rows[row0 + i] : -1;
+    // what the slice is told apart by: all asked for at once, before the barrier
+    const int32_t* const hist = a.history + (int64_t)b * a.history_stride;
+    constexpr int kEarly = 4;
+    int32_t early[kEarly];
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u) early[u] = (uint32_t)(tid + u * kAdjThreads) < ctl.history_len ? hist[tid + u * kAdjThreads] : -1;
+    const int32_t draft = tid < M ? a.tokens[lo + tid] : -1;
+    if (tid < rows) {
+      int32_t r = a.mask_rows ? a.mask_rows[row0 + tid] : -1;
       if (r < -1 || (int64_t)r >= a.n_masks) {
         bad = true;
         r = -1;
       }
-      s_mask[i] = r < 0 ? nullptr : a.masks + (int64_t)r * a.mask_stride;
+      s_mask[tid] = r < 0 ? nullptr : a.masks + (int64_t)r * a.mask_stride;
     }
     __syncthreads();
 
-    // the slice's counts, biases and drafts (their loads are on the way while the rows stream)
-    const int32_t* const hist = a.history + (int64_t)b * a.history_stride;
-    for (uint32_t k = tid; k < ctl.history_len; k += kAdjThreads) {
-      const uint32_t at = (uint32_t)hist[k] - (uint32_t)v0;  // beyond the slice: >= n
+    // the slice's counts, biases and drafts
+    auto count = [&](uint32_t k, int32_t token) {
+      const uint32_t at = (uint32_t)token - (uint32_t)v0;  // beyond the slice: >= n
       if (at < (uint32_t)n) {
         if (k < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
         else atomicAdd(&words[at], 1u);
         atomicOr(&marks[at >> 5], 1u << (at & 31u));
       }
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u) count((uint32_t)(tid + u * kAdjThreads), early[u]);
+#pragma unroll 4
+    for (uint32_t k = tid + kEarly * kAdjThreads; k < ctl.history_len; k += kAdjThreads) count(k, hist[k]);
     for (uint32_t k = tid; k < ctl.bias_count; k += kAdjThreads) {
       const int32_t t = a.bias_tokens[ctl.bias_offset + k];
       const int32_t before = k ? a.bias_tokens[ctl.bias_offset + k - 1] : -1;
       bad |= t <= before || (int64_t)t >= a.V;
-      const uint32_t at = (uint32_t)((int64_t)t - v0);
+      const uint32_t at = (uint32_t)t - (uint32_t)v0;
       if (at < (uint32_t)n) {
         bias[at] = a.bias_values[ctl.bias_offset + k];
         atomicOr(&marks[at >> 5], 1u << (at & 31u));
       }
     }
-    for (int k = tid; k < M; k += kAdjThreads) {
-      const uint32_t at = (uint32_t)((int64_t)a.tokens[lo + k] - v0);
+    if (tid < M) {
+      const uint32_t at = (uint32_t)draft - (uint32_t)v0;
       if (at < (uint32_t)n) {
-        s_drafts[atomicAdd(&s_ndrafts, 1)] = SliceDraft{(int32_t)at, k};
+        s_drafts[atomicAdd(&s_ndrafts, 1)] = SliceDraft{(int32_t)at, tid};
         atomicOr(&marks[at >> 5], 1u << (at & 31u));
       }
     }
 
     // The rows and their masks.  The slice of a row is cut at 16-byte boundaries of memory: block k
     // covers the tokens k E - lead .. k E - lead + E - 1 of the row, the first and the last may be
-    // partial.  A thread keeps its blocks and goes down the rows, four at a time.
+    // partial.  A thread goes down the rows with a block, then with its next one.
     const bool in_place = a.logits == a.out;
     const bool alike = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
     const int32_t lead0 = (int32_t)(((uintptr_t)in & 15u) / sizeof(T)), step = (int32_t)(a.V & (E - 1));
     const int32_t blocks = alike ? (n + E - 1) / E + 1 : 0;
-    for (int32_t k = tid; k < blocks; k += kAdjThreads) {
-      const T* pr = in + k * E;
-      int32_t lead = lead0;
-      for (int32_t i = 0; i < rows; i += kAdjUnroll) {
+    {
+      int32_t k = tid, i = 0, lead = lead0;
+      uint32_t at = (uint32_t)k * E;  // of the block's first logit from `in`, plus lead (at most 65 rows of 2^24)
+      while (rows > 0 && k < blocks) {  // (a session without drafts has no draft rows)
         uint4 q[kAdjUnroll];
-        T* to[kAdjUnroll];  // null: nothing to write
-        uint32_t keep[kAdjUnroll];
+        uint32_t to[kAdjUnroll], keep[kAdjUnroll];
 #pragma unroll
         for (int u = 0; u < kAdjUnroll; ++u) {
           const int32_t t = k * E - lead;
-          const T* const from = pr - lead;
-          to[u] = nullptr;
-          if (i + u < rows && t >= 0 && t + E <= n) {
-            const uint32_t* const mask = s_mask[i + u];
-            keep[u] = mask == nullptr ? kAll : mask_bits<E>(mask, v0 + t);
-            if (!in_place || keep[u] != kAll) {
-              to[u] = out + (from - in);
-              q[u] = *reinterpret_cast<const uint4*>(from);
+          to[u] = kNowhere;
+          if (k < blocks) {
+            if (t >= 0 && t + E <= n) {
+              const uint32_t* const mask = s_mask[i];
+              keep[u] = mask == nullptr ? kAll : mask_bits<E>(mask, v0 + t);
+              if (!in_place || keep[u] != kAll) {
+                to[u] = at - (uint32_t)lead;
+                q[u] = *reinterpret_cast<const uint4*>(in + to[u]);
+              }
+            }
+            at += (uint32_t)a.V;
+            lead = (lead + step) & (E - 1);
+            if (++i == rows) {
+              i = 0;
+              k += kAdjThreads;
+              at = (uint32_t)k * E;
+              lead = lead0;
             }
           }
-          pr += a.V;
-          lead = (lead + step) & (E - 1);
         }
 #pragma unroll
         for (int u = 0; u < kAdjUnroll; ++u)
-          if (to[u] != nullptr)
-            *reinterpret_cast<uint4*>(to[u]) = keep[u] == kAll ? q[u] : masked_block(q[u], keep[u], static_cast<const T*>(nullptr));
+          if (to[u] != kNowhere)
+            *reinterpret_cast<uint4*>(out + to[u]) = keep[u] == kAll ? q[u] : masked_block(q[u], keep[u], static_cast<const T*>(nullptr));
       }
     }
     // what the blocks left: the ends of the rows, or all of them where the two addresses differ modulo 16
