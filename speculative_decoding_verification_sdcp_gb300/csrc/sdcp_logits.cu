@@ -20,7 +20,8 @@ namespace sdcp {
 namespace {
 
 constexpr int kAdjThreads = 256;
-constexpr int kAdjUnroll = 8;             // blocks a thread has in flight
+constexpr int kAdjUnroll = 4;             // blocks a thread has in flight
+constexpr int kAdjCtas = 5;               // CTAs of an SM
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kInPrompt = 1u << 31;  // of a slice's word: the token is in the prompt
 constexpr uint32_t kCountMask = ~kInPrompt;
@@ -90,7 +91,7 @@ __host__ __device__ constexpr size_t adjust_smem(int32_t slice, bool biased) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const AdjustArgs a) {
   constexpr int E = Elem<T>::kPerVec;
   constexpr uint32_t kAll = (1u << E) - 1u;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -264,22 +265,28 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs a)
       // their logits, in every row
       const int32_t nd = s_ndrafts;
       const float rep = ctl.repetition, freq = ctl.frequency, pres = ctl.presence;
+      int32_t side = 1;  // threads of a token, a row each
+      while (side < 32 && side < rows && total * side < kAdjThreads) side *= 2;
+      const int32_t first = tid & (side - 1);
 #pragma unroll 1
-      for (int32_t x = tid; x < rows * total; x += kAdjThreads) {
-        const int32_t r = x / total, t = listed[x - r * total];
-        const uint32_t* const mask = s_mask[r];
-        if (mask != nullptr && mask_bits<1>(mask, v0 + t) == 0u) continue;
+      for (int32_t x = tid / side; x < total; x += kAdjThreads / side) {
+        const int32_t t = listed[x];
         const uint32_t w = words[t];
-        uint32_t c = w & kCountMask;
-        for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
-        const bool seen = (w & kInPrompt) != 0u || c != 0u;
         const float bt = has_bias ? bias[t] : 0.0f;
-        if (!seen && bt == 0.0f) continue;
-        const int64_t at_row = (int64_t)r * a.V + t;
-        float z = to_float(in[at_row]);
-        if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-        if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
-        out[at_row] = from_float<T>(__fadd_rn(z, bt));
+        const T* pr = in + (int64_t)first * a.V + t;
+        T* po = out + (int64_t)first * a.V + t;
+#pragma unroll 2
+        for (int32_t r = first; r < rows; r += side, pr += side * a.V, po += side * a.V) {
+          const uint32_t* const mask = s_mask[r];
+          uint32_t c = w & kCountMask;
+          for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
+          const bool seen = (w & kInPrompt) != 0u || c != 0u;
+          if ((!seen && bt == 0.0f) || (mask != nullptr && mask_bits<1>(mask, v0 + t) == 0u)) continue;
+          float z = to_float(*pr);
+          if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+          if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
+          *po = from_float<T>(__fadd_rn(z, bt));
+        }
       }
     }
   }
@@ -296,6 +303,16 @@ cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
   const size_t smem = adjust_smem(a.slice, a.n_bias > 0);
   adjust_kernel<T><<<(unsigned)a.B * (unsigned)a.n_slices, kAdjThreads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+// Tokens of a slice: 4096 while a session has fewer than eight rows on average (what a CTA does
+// besides streaming is then spread over more tokens: 5 rows of 152064, 601 us against 630 with
+// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 138 us
+// against 149), and down to 512 where that leaves SMs without a CTA.
+int32_t adjust_slice(int64_t V, int32_t B, int64_t rows, int sms) {
+  int32_t slice = rows < (int64_t)8 * B ? 4096 : 2048;
+  while (slice > 512 && (V + slice - 1) / slice * B < (int64_t)2 * sms) slice /= 2;
+  return slice;
 }
 
 }  // namespace
@@ -323,7 +340,9 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
   if (mask_rows && n_masks > 0 && (!masks || mask_stride < (V + 31) / 32)) return SDCP_E_INVALID;
   const size_t esz = dtype == SDCP_BF16 ? 2 : 4;
   if (((uintptr_t)logits % esz) != 0 || ((uintptr_t)out % esz) != 0) return SDCP_E_ALIGN;
-  const int32_t slice = 4096;
+  DeviceInfo di;
+  if (!device_info(&di)) return SDCP_E_DEVICE;
+  const int32_t slice = adjust_slice(V, B, total_drafts + (rows == SDCP_ROWS_TARGET ? B : 0), di.sms);
   const int64_t n_slices = (V + slice - 1) / slice;
   if (n_slices * B > (int64_t)INT32_MAX) return SDCP_E_TOO_LARGE;
   const AdjustArgs a{logits, out, V, B, rows == SDCP_ROWS_TARGET ? 1 : 0, m_offsets, total_drafts, draft_tokens,

@@ -290,9 +290,30 @@ def controls_tensor(controls: np.ndarray, device) -> torch.Tensor:
 
 def _is(t, dtype, what):
     """The library reads raw memory: a tensor of another type or with gaps is refused here."""
-    if t is not None and (t.dtype != dtype or not t.is_contiguous()):
+    if t is not None and (t.dtype is not dtype or not t.is_contiguous()):
         raise TypeError("%s must be a contiguous %s tensor" % (what, dtype))
     return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, what, device, stream, *args):
+    """One call of the library on a device: on the given stream handle, or the device's current
+    stream.  (A serving step makes several calls of a few microseconds, so the device is only
+    switched where it is not the current one.)"""
+    here = torch.cuda.current_device()
+    index = here if device.index is None else device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    if index == here:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc, what)
 
 
 def sdcp_adjust_logits(logits, out, m_offsets, total_drafts, draft_tokens, controls_dev, history, status,
@@ -318,15 +339,11 @@ def sdcp_adjust_logits(logits, out, m_offsets, total_drafts, draft_tokens, contr
         raise ValueError("m_offsets, controls, history and draft tokens must cover the %d sessions" % B)
     if bias_tokens is not None and (bias_values is None or bias_values.numel() != bias_tokens.numel()):
         raise ValueError("bias_tokens and bias_values must have the same length")
-    s = _stream_handle(logits.device) if stream is None else ctypes.c_void_p(stream)
-    with _on(logits):
-        rc = lib.sdcp_adjust_logits(_ptr(logits), _ptr(out), code, V, B, int(rows), _ptr(m_offsets), int(total_drafts),
-                                    _ptr(draft_tokens), _ptr(controls_dev), _ptr(history),
-                                    0 if history is None else history.shape[1], _ptr(bias_tokens), _ptr(bias_values),
-                                    0 if bias_tokens is None else bias_tokens.numel(), _ptr(masks),
-                                    0 if masks is None else masks.shape[1], 0 if masks is None else masks.shape[0],
-                                    _ptr(mask_rows), _ptr(status), s)
-    _check(rc, "sdcp_adjust_logits")
+    _call(lib.sdcp_adjust_logits, "sdcp_adjust_logits", logits.device, stream, logits.data_ptr(), out.data_ptr(), code, V, B, int(rows),
+          m_offsets.data_ptr(), int(total_drafts), _addr(draft_tokens), controls_dev.data_ptr(), _addr(history),
+          0 if history is None else history.shape[1], _addr(bias_tokens), _addr(bias_values),
+          0 if bias_tokens is None else bias_tokens.numel(), _addr(masks), 0 if masks is None else masks.shape[1],
+          0 if masks is None else masks.shape[0], _addr(mask_rows), status.data_ptr())
 
 
 class KvCache:
@@ -389,12 +406,9 @@ def sdcp_append_kv(cache, page_table, m_offsets, total_drafts, kv_len, k, v, sta
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    s = _stream_handle(k.device) if stream is None else ctypes.c_void_p(stream)
-    with _on(k):
-        rc = lib.sdcp_append_kv(ctypes.byref(desc), B, _ptr(m_offsets), int(total_drafts), _ptr(kv_len),
-                                code, _ptr(k), ks, _ptr(v), vs, None if rotary is None else ctypes.byref(rotary.desc),
-                                _ptr(q), qs, n_q, _ptr(q_out), _ptr(status), s)
-    _check(rc, "sdcp_append_kv")
+    _call(lib.sdcp_append_kv, "sdcp_append_kv", k.device, stream, ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
+          kv_len.data_ptr(), code, k.data_ptr(), ks, v.data_ptr(), vs, None if rotary is None else ctypes.byref(rotary.desc),
+          _addr(q), qs, n_q, _addr(q_out), status.data_ptr())
 
 
 def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, status, stream=None):
@@ -411,11 +425,8 @@ def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, stat
     if offsets.numel() < B + 1 or start.numel() < B:
         raise ValueError("offsets and start must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    s = _stream_handle(status.device) if stream is None else ctypes.c_void_p(stream)
-    with _on(status):
-        rc = lib.sdcp_read_kv(ctypes.byref(desc), B, _ptr(offsets), int(n_tokens), _ptr(start),
-                              dtype_code(outs[0]), _ptr(k_out), _ptr(v_out), _ptr(status), s)
-    _check(rc, "sdcp_read_kv")
+    _call(lib.sdcp_read_kv, "sdcp_read_kv", status.device, stream, ctypes.byref(desc), B, offsets.data_ptr(), int(n_tokens),
+          start.data_ptr(), dtype_code(outs[0]), _addr(k_out), _addr(v_out), status.data_ptr())
 
 
 def sdcp_attend_workspace_bytes(B: int, total_drafts: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -446,12 +457,9 @@ def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, s
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    s = _stream_handle(q.device) if stream is None else ctypes.c_void_p(stream)
-    with _on(q):
-        rc = lib.sdcp_attend_kv(ctypes.byref(desc), B, _ptr(m_offsets), int(total_drafts), _ptr(kv_len),
-                                _ptr(q), qs, q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), int(window),
-                                _ptr(out), _ptr(status), _ptr(workspace), workspace.numel(), s)
-    _check(rc, "sdcp_attend_kv")
+    _call(lib.sdcp_attend_kv, "sdcp_attend_kv", q.device, stream, ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
+          kv_len.data_ptr(), q.data_ptr(), qs, q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), int(window),
+          out.data_ptr(), status.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def sdcp_split_sessions(m_offsets: np.ndarray, params: np.ndarray | None, n_parts: int) -> np.ndarray:
