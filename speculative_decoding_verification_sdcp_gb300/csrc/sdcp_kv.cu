@@ -34,8 +34,13 @@ cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* stat
 
 // ---- append ---------------------------------------------------------------------------
 
-constexpr int kAppendThreads = 256;
-constexpr int kChan = 4;  // channels of a lane
+// Bound by memory for long rounds and by its chain of loads for short ones (offsets, session, page,
+// angles).  A warp has a row: it finds the row's session, position, page and angles once, behind its
+// first loads, and goes over the heads, eight channels a lane (16 bytes of bfloat16, one word of
+// codes), a few heads' loads in flight.  Short rounds share a row's heads among several warps.
+constexpr int kAppendThreads = 128;
+constexpr int kAppendCtas = 5;  // of an SM
+constexpr int kChan = 8;
 
 struct AppendArgs {
   KvView kv;
@@ -50,123 +55,17 @@ struct AppendArgs {
   const int32_t* status;
 };
 
-__device__ __forceinline__ void load4(const float* p, float (&x)[kChan]) {
-  const float4 w = *reinterpret_cast<const float4*>(p);
-  x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+__device__ __forceinline__ void load8(const float* p, float (&x)[kChan]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[kChan]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[kChan]) {
+  uint32_t b[8];
+  Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(p), b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(b[j]);
 }
-__device__ __forceinline__ void store4(float* p, const float (&x)[kChan]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[kChan]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ float elem(const float* p) { return *p; }
-__device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-// One warp handles 32 / (D / 4) heads at a time, four channels a lane.
-template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
-  constexpr int kLanes = D / kChan;           // lanes of a head
-  constexpr int kHeads = 32 / kLanes;         // heads of a warp
-  const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
-  const int64_t row = blockIdx.x;
-  wait_for_previous();
-  const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
-  const int64_t i = row - a.s.offsets[b] - b;
-  if (a.status[b] != SDCP_S_OK || i < 0 || i > (int64_t)a.s.offsets[b + 1] - a.s.offsets[b]) return;
-  const int32_t pos = a.s.start[b] + (int32_t)i;
-
-  // this lane's channels, and the cosines and signed sines they turn by
-  const int c0 = (lane % kLanes) * kChan;
-  float cs[kChan], sn[kChan];
-  bool turns[kChan];
-  int other[kChan];  // the channel each turns with
-#pragma unroll
-  for (int j = 0; j < kChan; ++j) {
-    const int c = c0 + j, half = a.rot / 2;
-    turns[j] = a.table != nullptr && c < a.rot;
-    cs[j] = 1.0f;
-    sn[j] = 0.0f;
-    other[j] = c;
-    if (turns[j]) {
-      const bool second = a.interleaved ? (c & 1) != 0 : c >= half;
-      const int pair = a.interleaved ? c >> 1 : second ? c - half : c;
-      other[j] = a.interleaved ? c ^ 1 : second ? c - half : c + half;
-      const float* t = a.table + (int64_t)pos * a.rot;
-      cs[j] = t[pair];
-      sn[j] = second ? t[half + pair] : -t[half + pair];
-    }
-  }
-
-  const int32_t page = a.kv.page_table[(int64_t)b * a.kv.max_pages + (pos >> a.kv.log_page)];
-  const int32_t slot = pos & (a.kv.page_tokens() - 1);
-  uint8_t* pg = a.kv.pages + (int64_t)page * a.kv.page;
-  const int32_t heads = 2 * a.kv.heads + a.q_heads;
-  for (int32_t h = ((int32_t)blockIdx.y * (kAppendThreads / 32) + warp) * kHeads + lane / kLanes; h - lane / kLanes < heads;
-       h += (int32_t)gridDim.y * (kAppendThreads / 32) * kHeads) {
-    const bool live = h < heads;
-    const bool is_k = h < a.kv.heads, is_v = !is_k && h < 2 * a.kv.heads;
-    const int32_t head = is_k ? h : is_v ? h - a.kv.heads : h - 2 * a.kv.heads;
-    const T* src = is_k ? static_cast<const T*>(a.k) + row * a.k_stride
-                        : is_v ? static_cast<const T*>(a.v) + row * a.v_stride : static_cast<const T*>(a.q) + row * a.q_stride;
-    src += (int64_t)head * D;
-    float x[kChan] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) {
-      load4(src + c0, x);
-      if (!is_v) {
-        float y[kChan];
-#pragma unroll
-        for (int j = 0; j < kChan; ++j) y[j] = turns[j] ? elem(src + other[j]) : 0.0f;
-        // x1 cos - x2 sin and x2 cos + x1 sin, each product and sum rounded by itself
-#pragma unroll
-        for (int j = 0; j < kChan; ++j)
-          if (turns[j]) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
-      }
-    }
-    if (live && !is_k && !is_v) store4(static_cast<T*>(a.q_out) + (row * a.q_heads + head) * D + c0, x);
-    // quantise: the largest magnitude over the group's eight lanes (fmaxf leaves a NaN out)
-    float most = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    most = isnan(most) ? 0.0f : most;
-#pragma unroll
-    for (int o = 1; o < kKvGroup / kChan; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    const uint32_t sb = scale_byte(most);
-    const float s = scale_value(sb);
-    uint32_t w = 0u;
-    const int base = (c0 & 4) ? 8 : 0;  // channels 4..7 of a word sit eight bits up
-#pragma unroll
-    for (int j = 0; j < kChan; ++j) {
-      const float n = fminf(fmaxf(rintf(__fdiv_rn(x[j], s)), -7.0f), 7.0f);
-      const uint32_t code = isnan(x[j]) ? 8u : (uint32_t)((int32_t)n + 8);
-      w |= code << (base + 4 * (j / 2) + 16 * (j % 2));
-    }
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-    if (live && (is_k || is_v)) {
-      uint8_t* blk = pg + ((int64_t)head * 2 + (is_v ? 1 : 0)) * a.kv.block;
-      const int g = c0 / kKvGroup;
-      if ((c0 & 4) == 0) *reinterpret_cast<uint32_t*>(blk + code_at(g, slot, a.kv.log_page) + (c0 % kKvGroup) / 8 * 4) = w;
-      if ((c0 % kKvGroup) == 0) blk[scale_at<D>(g, slot, a.kv.log_page)] = (uint8_t)sb;
-    }
-  }
-}
-
-// ---- read -----------------------------------------------------------------------------
-
-constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 32;  // rows of a CTA
-
-struct ReadArgs {
-  KvView kv;
-  KvSessions s;
-  void *k_out, *v_out;
-  const int32_t* status;
-};
-
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -180,6 +79,182 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ float elem(const float* p) { return *p; }
+__device__ __forceinline__ float elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// Eight channels as they are in memory.
+template <typename T> struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j) v[j] = reinterpret_cast<const uint4*>(p)[j];
+  }
+  __device__ __forceinline__ void values(float (&x)[kChan]) const { load8(reinterpret_cast<const T*>(v), x); }
+};
+
+// How a lane's channels turn: with their neighbours, with eight channels half a rotation away, or (a
+// half that is no multiple of eight, or a table off its boundary) one by one.
+enum { kStay, kNeighbours, kHalves, kOneByOne };
+template <int kKind> struct Turn {
+  float cs[kChan], sn[kChan];  // cosines, and sines with their signs
+  int c0, rot;
+  bool on;  // some of the lane's channels turn
+  __device__ __forceinline__ Turn(const AppendArgs& a, int c) : c0(c), rot(a.rot), on(kKind != kStay && c < a.rot) {}
+  __device__ __forceinline__ void angles(const AppendArgs& a, int64_t pos) {
+    if (!on) return;
+    const float* const row = a.table + pos * rot;
+    const int half = rot / 2;
+    if (kKind == kHalves) {
+      const int pair = c0 >= half ? c0 - half : c0;
+      load8(row + pair, cs);
+      load8(row + half + pair, sn);
+      if (c0 < half)
+#pragma unroll
+        for (int j = 0; j < kChan; ++j) sn[j] = -sn[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChan; ++j) {
+        const int c = c0 + j;
+        const bool in = c < rot, second = a.interleaved ? (c & 1) != 0 : c >= half;
+        const int pair = a.interleaved ? c >> 1 : second ? c - half : c;
+        cs[j] = in ? row[pair] : 1.0f;
+        const float s = in ? row[half + pair] : 0.0f;
+        sn[j] = second ? s : -s;
+      }
+    }
+  }
+  // x1 cos - x2 sin and x2 cos + x1 sin, each product and sum rounded by itself; x: the lane's
+  // channels of the head at src
+  template <typename T> __device__ __forceinline__ void turn(const T* src, float (&x)[kChan]) const {
+    if (!on) return;
+    const int half = rot / 2;
+    float y[kChan];
+    if (kKind == kNeighbours) {
+#pragma unroll
+      for (int j = 0; j < kChan; ++j) y[j] = x[j ^ 1];
+    } else if (kKind == kHalves) {
+      load8(src + (c0 < half ? c0 + half : c0 - half), y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChan; ++j) {
+        const int c = c0 + j;
+        y[j] = c < rot ? elem(src + (c < half ? c + half : c - half)) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kChan; ++j)
+      if (kKind == kHalves || c0 + j < rot) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
+  }
+};
+
+template <typename T, int D, int kKind>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendArgs a) {
+  constexpr int kLanes = D / kChan;               // lanes of a head
+  constexpr int kHeads = 32 / kLanes;             // heads of a warp at once
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // and times that in flight
+  const int lane = (int)(threadIdx.x & 31u);
+  const int c0 = (lane % kLanes) * kChan, own = lane / kLanes;
+  const int step = (int)gridDim.y * kHeads, h_first = (int)blockIdx.y * kHeads;
+  const int64_t row = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  if (row >= a.s.total + a.s.B) return;
+  wait_for_previous();
+
+  // keys and values: head h below the cached heads is a key's, else a value's
+  const int kv2 = 2 * a.kv.heads;
+  const T* const k_row = static_cast<const T*>(a.k) + row * a.k_stride;
+  const T* const v_row = static_cast<const T*>(a.v) + row * a.v_stride - (int64_t)a.kv.heads * D;
+  Raw<T> raw[kBatch];
+  auto load_kv = [&](int hs) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = hs + u * step + own;
+      if (h < kv2) raw[u].load((h < a.kv.heads ? k_row : v_row) + h * D + c0);
+    }
+  };
+  load_kv(h_first);
+
+  const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
+  const int32_t off = a.s.offsets[b];
+  const int64_t i = row - off - b;
+  if (a.status[b] != SDCP_S_OK || i < 0 || i > (int64_t)a.s.offsets[b + 1] - off) return;
+  const int32_t pos = a.s.start[b] + (int32_t)i;
+  const int32_t page = a.kv.page_table[(int64_t)b * a.kv.max_pages + (pos >> a.kv.log_page)];
+  Turn<kKind> t(a, c0);
+  t.angles(a, pos);
+
+  const int g = c0 / kKvGroup;
+  const int32_t slot = pos & (a.kv.page_tokens() - 1);
+  uint8_t* const pg = a.kv.pages + (int64_t)page * a.kv.page;
+  const int32_t code = code_at(g, slot, a.kv.log_page) + (c0 % kKvGroup) / kChan * 4, scale = scale_at<D>(g, slot, a.kv.log_page);
+  for (int hs = h_first; hs < kv2; hs += kBatch * step) {
+    if (hs != h_first) load_kv(hs);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (hs + u * step >= kv2) break;
+      const int h = hs + u * step + own;
+      const bool live = h < kv2, is_k = h < a.kv.heads;
+      float x[kChan];
+      raw[u].values(x);
+      if (is_k) t.turn(k_row + h * D, x);
+      // the largest magnitude over the group's four lanes (fmaxf leaves a NaN out)
+      float most = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kChan; ++j) most = fmaxf(most, fabsf(x[j]));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      const uint32_t sb = scale_byte(most);
+      const float s = scale_value(sb);
+      uint32_t w = 0u;
+#pragma unroll
+      for (int j = 0; j < kChan; ++j) {
+        const float n = fminf(fmaxf(rintf(__fdiv_rn(x[j], s)), -7.0f), 7.0f);
+        const uint32_t c = isnan(x[j]) ? 8u : (uint32_t)((int32_t)n + 8);
+        w |= c << (4 * (j / 2) + 16 * (j % 2));
+      }
+      if (live) {
+        uint8_t* const blk = pg + ((int64_t)(is_k ? h : h - a.kv.heads) * 2 + (is_k ? 0 : 1)) * a.kv.block;
+        *reinterpret_cast<uint32_t*>(blk + code) = w;
+        if ((c0 % kKvGroup) == 0) blk[scale] = (uint8_t)sb;
+      }
+    }
+  }
+  // queries
+  const T* const q_row = static_cast<const T*>(a.q) + row * a.q_stride;
+  T* const q_to = static_cast<T*>(a.q_out) + row * a.q_heads * D + c0;
+  for (int h = h_first + own; h < a.q_heads; h += kBatch * step) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (h + u * step < a.q_heads) raw[u].load(q_row + (int64_t)(h + u * step) * D + c0);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (h + u * step < a.q_heads) {
+        float x[kChan];
+        raw[u].values(x);
+        t.turn(q_row + (int64_t)(h + u * step) * D, x);
+        store8(q_to + (int64_t)(h + u * step) * D, x);
+      }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_append(const AppendArgs& a, dim3 grid, cudaStream_t st) {
+  if (a.table == nullptr) return launch_after(append_kernel<T, D, kStay>, grid, kAppendThreads, 0, st, a);
+  if (a.interleaved) return launch_after(append_kernel<T, D, kNeighbours>, grid, kAppendThreads, 0, st, a);
+  if (a.rot % (2 * kChan) == 0 && ((uintptr_t)a.table & 15u) == 0) return launch_after(append_kernel<T, D, kHalves>, grid, kAppendThreads, 0, st, a);
+  return launch_after(append_kernel<T, D, kOneByOne>, grid, kAppendThreads, 0, st, a);
+}
+
+// ---- read -----------------------------------------------------------------------------
+
+constexpr int kReadThreads = 256;
+constexpr int kReadTokens = 32;  // rows of a CTA, one per lane of its first warp
+
+struct ReadArgs {
+  KvView kv;
+  KvSessions s;
+  void *k_out, *v_out;
+  const int32_t* status;
+};
 
 // A warp reads eight tokens of one head: the four words of a group of each, then the next group.
 template <typename T, int D>
@@ -190,12 +265,13 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
   const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
   const int64_t row0 = (int64_t)blockIdx.x * kReadTokens;
   wait_for_previous();
-  for (int r = warp; r < kReadTokens; r += kReadThreads / 32) {
-    const int64_t row = row0 + r;
+  if (warp == 0) {  // the first row's session by a search, the others' from there on
+    int32_t b = find_session(a.s.offsets, a.s.B, row0, false);
+    const int64_t row = row0 + lane;
     int64_t at = -1;
     int32_t slot = 0;
     if (row < a.s.total) {
-      const int32_t b = find_session(a.s.offsets, a.s.B, row, false);
+      while (b + 1 < a.s.B && a.s.offsets[b + 1] <= row) ++b;
       const int64_t i = row - a.s.offsets[b];
       if (a.status[b] == SDCP_S_OK && i >= 0 && row < a.s.offsets[b + 1]) {
         const int32_t pos = a.s.start[b] + (int32_t)i;
@@ -203,14 +279,12 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs a) {
         slot = pos & (a.kv.page_tokens() - 1);
       }
     }
-    if (lane == 0) {
-      s_page[r] = at;
-      s_slot[r] = slot;
-    }
+    s_page[lane] = at;
+    s_slot[lane] = slot;
   }
   __syncthreads();
   const int word = lane & 3;
-  for (int u = warp; u < kReadTokens / 8 * a.kv.heads * 2; u += kReadThreads / 32) {
+  for (int u = (int)blockIdx.y * (kReadThreads / 32) + warp; u < kReadTokens / 8 * a.kv.heads * 2; u += (int)gridDim.y * (kReadThreads / 32)) {
     const int r = (u & 3) * 8 + (lane >> 2);
     const int which = (u >> 2) & 1, head = u >> 3;
     T* dst = static_cast<T*>(which ? a.v_out : a.k_out);
@@ -288,19 +362,14 @@ extern "C" int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   const AppendArgs a{kv, s, k, v, q, k_stride, v_stride, q_stride, q ? q_heads : 0, q_out,
                      rotary ? rotary->table : nullptr, rotary ? rotary->rot_dim : 0,
                      rotary && rotary->layout == SDCP_ROTARY_INTERLEAVED ? 1 : 0, status};
-  // heads of a row over several CTAs where there are few rows
-  const int64_t rows = total_drafts + B;
-  const int64_t per_cta = (int64_t)(kAppendThreads / 32) * (128 / D);
-  const int64_t most = (2 * (int64_t)cache->kv_heads + a.q_heads + per_cta - 1) / per_cta;
-  const int64_t y = min(most, (2 * (int64_t)di.sms + rows - 1) / rows);
-  const dim3 grid((unsigned)rows, (unsigned)max(y, (int64_t)1));
+  // a row's heads over several warps where there are few rows
+  const int64_t rows = total_drafts + B, per_warp = (int64_t)32 / (D / kChan);
+  const int64_t most = (max(2 * (int64_t)cache->kv_heads, (int64_t)a.q_heads) + per_warp - 1) / per_warp;
+  const int64_t y = max((int64_t)1, min(most, 24 * (int64_t)di.sms / rows));
+  const dim3 grid((unsigned)((rows + kAppendThreads / 32 - 1) / (kAppendThreads / 32)), (unsigned)y);
   cudaError_t e;
-  if (dtype == SDCP_BF16)
-    e = D == 128 ? launch_after(append_kernel<__nv_bfloat16, 128>, grid, kAppendThreads, 0, st, a)
-                 : launch_after(append_kernel<__nv_bfloat16, 64>, grid, kAppendThreads, 0, st, a);
-  else
-    e = D == 128 ? launch_after(append_kernel<float, 128>, grid, kAppendThreads, 0, st, a)
-                 : launch_after(append_kernel<float, 64>, grid, kAppendThreads, 0, st, a);
+  if (dtype == SDCP_BF16) e = D == 128 ? launch_append<__nv_bfloat16, 128>(a, grid, st) : launch_append<__nv_bfloat16, 64>(a, grid, st);
+  else e = D == 128 ? launch_append<float, 128>(a, grid, st) : launch_append<float, 64>(a, grid, st);
   return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
 }
 
@@ -316,12 +385,16 @@ extern "C" int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t
   if (B == 0) return SDCP_OK;
   if (!offsets || !start || !status || (n_tokens > 0 && !k_out && !v_out)) return SDCP_E_INVALID;
   if (!aligned16(k_out) || !aligned16(v_out)) return SDCP_E_ALIGN;
+  DeviceInfo di;
+  if (!device_info(&di)) return SDCP_E_DEVICE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const KvSessions s{B, offsets, n_tokens, 0, start, -1, INT32_MAX};
   if (launch_kv_check(kv, s, status, st) != cudaSuccess) return SDCP_E_LAUNCH;
   if (n_tokens == 0) return SDCP_OK;
   const ReadArgs a{kv, s, k_out, v_out, status};
-  const dim3 grid((unsigned)((n_tokens + kReadTokens - 1) / kReadTokens));
+  // heads over several CTAs where there are few tokens
+  const int64_t chunks = (n_tokens + kReadTokens - 1) / kReadTokens;
+  const dim3 grid((unsigned)chunks, (unsigned)max((int64_t)1, min((int64_t)cache->kv_heads, 8 * (int64_t)di.sms / chunks)));
   cudaError_t e;
   if (dtype == SDCP_BF16)
     e = cache->head_dim == 128 ? launch_after(read_kernel<__nv_bfloat16, 128>, grid, kReadThreads, 0, st, a)
