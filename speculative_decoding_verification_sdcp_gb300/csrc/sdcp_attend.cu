@@ -69,6 +69,15 @@ struct SessionPlan {
 };
 constexpr int32_t kItemUnits = 2;  // what an item's start and end cost, in tiles
 
+// The item that a CTA begins and another one goes on with: its parts are the CTA's second (or, where
+// it began with it, first) and the first of the CTAs after it, up to `last`.  n = 0: none.
+struct Cut {
+  int32_t n, first_slot, last;
+  int32_t row_head;  // place of column 0 among the heads of the output row of column 0
+  int64_t row;       // and that row
+  int32_t g0, pad;
+};
+
 struct AttendArgs {
   KvView kv;
   KvSessions s;
@@ -81,8 +90,8 @@ struct AttendArgs {
   uint32_t* error;   // non-zero: a bounded wait gave up
   int64_t* units;    // [B] units of a session: kv heads x chunks x tiles; 0 for a refused one
   SessionPlan* plans;  // [B]
-  int64_t* prefix;   // [B+1]
   float* parts;      // [ctas * 2] of Part
+  Cut* cuts;         // [ctas]
   int32_t ctas;
   int32_t cols;      // columns an item has at most
 };
@@ -324,7 +333,7 @@ struct Walk {
     chunk = (int32_t)(item - (int64_t)kvh * pl.chunks);
   }
   // the next item; false at the end of the CTA's part
-  __device__ __forceinline__ bool next(const AttendArgs& a, Item& it) {
+  __device__ __forceinline__ bool next(const AttendArgs& a, const Line& line, Item& it) {
     if (t >= t_end) return false;
     if (kvh == a.kv.heads) {  // the next session that has work
       do ++b;
@@ -348,6 +357,8 @@ struct Walk {
     it.k1 = min(max(unit0 + units - kItemUnits, 0), real);
     it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
     it.whole = units == pl.tiles;
+    if (!it.whole && unit0 == 0)  // the CTA's last item, and others go on with it
+      a.cuts[blockIdx.x] = Cut{it.n, it.slot, line.cta_of(t + pl.tiles - 1), kvh * share + it.g0, (int64_t)off + b + it.i0, it.g0, 0};
     t += units;
     unit0 = 0;
     if (++chunk == pl.chunks) {
@@ -395,11 +406,11 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
 // ---- the products -------------------------------------------------------------------------
 // The next item that has tiles; a part that holds no tile of its item is marked at once.  One thread.
 template <int D, int kCols>
-__device__ __forceinline__ void plan_item(const AttendArgs& a, AttendShared<kCols>& sh, uint32_t j) {
+__device__ __forceinline__ void plan_item(const AttendArgs& a, AttendShared<kCols>& sh, const Line& line, uint32_t j) {
   Item it;
   bool more;
   Walk walk = sh.walk;
-  while ((more = walk.next(a, it)) && it.k0 >= it.k1) {
+  while ((more = walk.next(a, line, it)) && it.k0 >= it.k1) {
     Part<D, kCols>* const part = reinterpret_cast<Part<D, kCols>*>(a.parts) + it.slot;
     for (int x = 0; x < kCols; ++x) {
       part->m[x] = -INFINITY;
@@ -414,7 +425,7 @@ __device__ __forceinline__ void plan_item(const AttendArgs& a, AttendShared<kCol
 // The ninth warp: S of a tile when its keys are in tensor memory, O when its weights are in shared
 // memory (the values are there before the weights).  One thread.
 template <int D, int kCols>
-__device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols>& sh, const unsigned char* s_q, const unsigned char* s_v,
+__device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols>& sh, const Line& line, const unsigned char* s_q, const unsigned char* s_v,
                                          const unsigned char* s_p, uint32_t tmem) {
   using Sm = AttendSmem<D, kCols>;
   using Sh = Shape<kCols>;
@@ -437,7 +448,7 @@ __device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols
     if (tiles <= 0) return;
     const uint32_t idesc = kIdescF32 | kIdescM128 | (uint32_t)((sh.item[j & 1u].n + 15) / 16 * 2) << 17;
     if ((threadIdx.x & 31u) == 0) {
-      plan_item<D, kCols>(a, sh, j + 1);
+      plan_item<D, kCols>(a, sh, line, j + 1);
       for (int32_t k = 0; k < tiles; ++k, ++i) {
         const uint32_t par = i & 1u;
         if (!wait_phase(&sh.k_full, par, &sh.dead)) { sh.dead = 1; break; }
@@ -796,14 +807,7 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
   }
   const long long start = before + incl - mine;
   const Line line(all, a.ctas);
-  if (cta == 0) {
-    long long at = start;
-    for (int32_t b = b0; b < b1; ++b) {
-      a.prefix[b] = at;
-      at += a.units[b];
-    }
-    if (tid == 0) a.prefix[a.s.B] = all;
-  }
+  if (tid == 0) a.cuts[cta].n = 0;
   if (cta >= line.ctas || all == 0) return;
   const int64_t here = line.first(cta);
   if (here >= start && here < start + mine) {
@@ -829,10 +833,10 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
   if (warp == 8) {
     if (lane == 0) {
       sh.walk.begin(a, line, sh.session, sh.base);
-      plan_item<D, kCols>(a, sh, 0);
+      plan_item<D, kCols>(a, sh, line, 0);
     }
     __syncwarp();
-    multiply<D, kCols>(a, sh, s_q, s_v, s_p, tmem);
+    multiply<D, kCols>(a, sh, line, s_q, s_v, s_p, tmem);
   } else {
     attend_tiles<D, kCols>(a, sh, s_q, s_v, s_p, s_p + Sm::kP, tmem);
   }
@@ -845,60 +849,61 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
 // ---- the joining of parts -----------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// One warp per row and query head: a row of a refused session becomes zero, a row whose item was cut
-// is the parts' sum, a row that one CTA wrote is left.
+// One warp per CTA and column: where the CTA's last item goes on in others, the column is the sum of
+// its parts, in the line's order.  The same warps go over the rows: a refused session's become zero.
 template <int D, int kCols>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int64_t rows) {
   constexpr int kPer = D / 32;
   const int lane = (int)(threadIdx.x & 31u);
+  const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), ids = (int64_t)gridDim.x * (kJoinThreads / 32);
   wait_for_previous();
   const bool failed = *a.error != 0u;
   if (failed)
     for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
       a.status[b] = SDCP_S_INTERNAL;
-  const Line line(a.prefix[a.s.B], a.ctas);
-  const int32_t share = a.q_heads / a.kv.heads;
-  const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
-  for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); at < rows * a.q_heads;
-       at += (int64_t)gridDim.x * (kJoinThreads / 32)) {
-    const int64_t row = quotient(at, a.q_heads);
-    const int32_t h = (int32_t)(at - row * a.q_heads);
-    const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
-    const int32_t off = a.s.offsets[b], last = a.s.offsets[b + 1] - off;
-    const int64_t i = row - off - b;
-    __nv_bfloat16* out = a.out + at * D + lane * kPer;
-    float o[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
-    if (!failed && a.units[b] > 0 && i >= 0 && i <= last) {
-      const SessionPlan pl = a.plans[b];
-      const int32_t kvh = h / share;
-      const int64_t col = i * share + (h - kvh * share);
-      const int64_t part = quotient(col, pl.w);
-      const int64_t first = a.prefix[b] + ((int64_t)kvh * pl.chunks + part) * pl.tiles;
-      const int32_t j = (int32_t)(col - part * pl.w);
-      const int32_t c_lo = line.cta_of(first), c_hi = line.cta_of(first + pl.tiles - 1);
-      if (c_lo == c_hi) continue;
+  const int64_t cta = id / kCols;
+  const int j = (int)(id - cta * kCols);
+  if (cta < a.ctas && !failed) {
+    const Cut cut = a.cuts[cta];
+    if (j < cut.n) {
+      const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
+      auto part = [&](int32_t c) -> const Part<D, kCols>& { return parts[c == (int32_t)cta ? cut.first_slot : 2 * c]; };
       float m = -INFINITY;
-      for (int32_t c = c_lo + lane; c <= c_hi; c += 32)
-        m = fmaxf(m, parts[c * 2 + (c == c_lo && line.first(c) < first ? 1 : 0)].m[j]);
+      for (int32_t c = (int32_t)cta + lane; c <= cut.last; c += 32) m = fmaxf(m, part(c).m[j]);
       m = warp_max(m);
-      float sum = 0.0f;
-      for (int32_t c = c_lo; c <= c_hi; ++c) {
-        const Part<D, kCols>& p = parts[c * 2 + (c == c_lo && line.first(c) < first ? 1 : 0)];
-        const float pm = p.m[j];
-        if (pm == -INFINITY && p.l[j] == 0.0f) continue;  // nothing of the column in this part
-        const float f = pm == m ? 1.0f : ex2(pm - m);
-        sum += p.l[j] * f;
+      float sum = 0.0f, o[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) o[k] += p.o[j][lane * kPer + k] * f;
+      for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
+      for (int32_t c0 = (int32_t)cta; c0 <= cut.last; c0 += 32) {
+        // a lane's part: its factor, 0 where it holds nothing of the column (its O may not be written)
+        const int32_t n = min(32, cut.last - c0 + 1);
+        float f = 0.0f;
+        if (lane < n) {
+          const float pm = part(c0 + lane).m[j], pl = part(c0 + lane).l[j];
+          if (pm != -INFINITY || pl != 0.0f) f = pm == m ? 1.0f : ex2(pm - m);
+          if (f != 0.0f) sum += pl * f;
+        }
+#pragma unroll 8
+        for (int32_t x = 0; x < n; ++x) {
+          const float fx = __shfl_sync(0xFFFFFFFFu, f, x);
+          const float* const po = part(c0 + x).o[j] + lane;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) o[k] += (fx != 0.0f ? po[32 * k] : 0.0f) * fx;
+        }
       }
+      sum = warp_reduce(sum, [](float x, float y) { return x + y; });
+      const int32_t share = a.q_heads / a.kv.heads, r = (cut.g0 + j) / share;
+      __nv_bfloat16* const out = a.out + ((cut.row + r) * a.q_heads + cut.row_head - cut.g0 + (cut.g0 + j - r * share)) * D;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) o[k] = __fdividef(o[k], sum);
+      for (int k = 0; k < kPer; ++k) out[lane + 32 * k] = __float2bfloat16_rn(__fdividef(o[k], sum));
     }
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(o[0], o[1]);
-    *reinterpret_cast<__nv_bfloat162*>(out) = v0;
-    if (kPer == 4) *reinterpret_cast<__nv_bfloat162*>(out + 2) = __floats2bfloat162_rn(o[kPer - 2], o[kPer - 1]);
+  }
+  for (int64_t row = id; row < rows; row += ids) {
+    const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
+    const int64_t i = row - a.s.offsets[b] - b;
+    if (!failed && a.units[b] > 0 && i >= 0 && i <= (int64_t)a.s.offsets[b + 1] - a.s.offsets[b]) continue;
+    for (int64_t x = lane; x < (int64_t)a.q_heads * D / 8; x += 32)
+      reinterpret_cast<uint4*>(a.out + row * a.q_heads * D)[x] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -942,9 +947,8 @@ cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_after(attend_kernel<D, kCols>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D, kCols>::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  const int64_t rows = a.s.total + a.s.B, warps = rows * a.q_heads;
-  const int64_t blocks = min((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32), (int64_t)sms * 16);
-  return launch_after(attend_join_kernel<D, kCols>, (unsigned)blocks, kJoinThreads, 0, st, a, rows);
+  const int64_t warps = (int64_t)a.ctas * kCols;
+  return launch_after(attend_join_kernel<D, kCols>, (unsigned)(warps / (kJoinThreads / 32)), kJoinThreads, 0, st, a, a.s.total + a.s.B);
 }
 
 template <int D>
@@ -962,8 +966,8 @@ extern "C" size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, i
   if (B < 0 || total_drafts < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   const int32_t cols = columns_of(B, total_drafts, q_heads / kv_heads);
-  return kHeader + round256((size_t)B * sizeof(SessionPlan)) + round256(((size_t)B * 2 + 1) * sizeof(int64_t)) +
-         (head_dim == 128 ? parts_bytes<128>(cols) : parts_bytes<64>(cols));
+  return kHeader + round256((size_t)B * sizeof(SessionPlan)) + round256((size_t)B * sizeof(int64_t)) +
+         round256(kMaxSms * 3 * sizeof(Cut)) + (head_dim == 128 ? parts_bytes<128>(cols) : parts_bytes<64>(cols));
 }
 
 extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
@@ -988,12 +992,12 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   char* w = static_cast<char*>(workspace);
   char* const plans = w + kHeader;
   char* const lines = plans + round256((size_t)B * sizeof(SessionPlan));
-  int64_t* const units = reinterpret_cast<int64_t*>(lines);
+  char* const cuts = lines + round256((size_t)B * sizeof(int64_t));
+  char* const parts = cuts + round256(kMaxSms * 3 * sizeof(Cut));
   const KvSessions s{B, m_offsets, total_drafts, 1, kv_len, window, INT32_MAX};
   const AttendArgs a{kv, s, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
-                     static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), units,
-                     reinterpret_cast<SessionPlan*>(plans), units + B,
-                     reinterpret_cast<float*>(lines + round256(((size_t)B * 2 + 1) * sizeof(int64_t))),
+                     static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), reinterpret_cast<int64_t*>(lines),
+                     reinterpret_cast<SessionPlan*>(plans), reinterpret_cast<float*>(parts), reinterpret_cast<Cut*>(cuts),
                      0, columns_of(B, total_drafts, q_heads / cache->kv_heads)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
