@@ -94,6 +94,7 @@ struct AttendArgs {
   Cut* cuts;         // [ctas]
   int32_t ctas;
   int32_t cols;      // columns an item has at most
+  int32_t dim;       // channels of a head
 };
 
 template <int D, int kCols> struct Part {
@@ -179,15 +180,30 @@ __device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t a, uint64_t b, u
                "l"(b), "r"(idesc), "r"((uint32_t)add)
                : "memory");
 }
-// Bounded wait for a phase: polls without reading a clock or sleeping (waits here are a few hundred
-// cycles, a tile's step); false after kPolls, some seconds, or when another role has given up.
-constexpr uint32_t kPolls = 1u << 26;
+// Bounded wait for a phase.  Waits here are a few hundred cycles, a tile's step, so it polls a while
+// without reading a clock; false after kWaitNs, or when another warp has given up.
+__device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p, q; .reg .u32 n;\n"
+      "mov.u32 n, 0;\n"
+      "POLL:\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "@p bra DONE;\n"
+      "add.u32 n, n, 1;\n"
+      "setp.lt.u32 q, n, 4096;\n"
+      "@q bra POLL;\n"
+      "DONE:\n"
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile int* dead) {
-  for (uint32_t n = 0; n < kPolls; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((n & 255u) == 255u && dead != nullptr && *dead) return false;
-  }
-  return false;
+  if (poll_phase(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!poll_phase(bar, parity))
+    if ((dead != nullptr && *dead) || global_ns() - t0 > kWaitNs) return false;
+  return true;
 }
 // A shared-memory matrix of swizzled atoms (8 rows of 128 or 64 bytes).  lead: bytes between atoms
 // along the contiguous dimension (used where that is not the product's inner one); step: bytes
@@ -390,6 +406,12 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
   let_next_start();
   const int32_t b = (int32_t)blockIdx.x;
   const int32_t st = kv_session_status(a.kv, a.s, b);
+  if (st != SDCP_S_OK) {  // its rows become zero (what another session has of them is written later)
+    const int64_t lo = min(max((int64_t)a.s.offsets[b], (int64_t)0), a.s.total), hi = min(max((int64_t)a.s.offsets[b + 1], lo), a.s.total);
+    const int64_t row = (int64_t)a.q_heads * a.dim / 8;
+    uint4* const out = reinterpret_cast<uint4*>(a.out);
+    for (int64_t x = (lo + b) * row + threadIdx.x; x < (hi + b + 1) * row; x += kCheckThreads) out[x] = make_uint4(0u, 0u, 0u, 0u);
+  }
   if (threadIdx.x == 0) {
     a.status[b] = st;
     int64_t units = 0;
@@ -503,7 +525,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
   const int sb_shift = D == 128 ? wg * 16 : (tok & 1) * 16 + wg * 8;  // of the thread's own scales (tiles start at even tokens)
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at + kCodes), "r"(0u) : "memory");
-  uint32_t slot = 0;
+  // scales from the thread's codes: past the block's codes (D / 2 bytes a token), less the thread's own start
+  const int64_t scale_off = (int64_t)(D / 2 << a.kv.log_page) - ((wg * kOwn) << (a.kv.log_page + 4));
   uint32_t i = 0;  // tiles so far
   bool dead = false;  // a wait gave up: the eight warps agree on it at a vote, all nine at an item's start
   for (uint32_t j = 0;; ++j) {
@@ -519,28 +542,32 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     // numbers, whose weight is zero)
     const uint32_t lowest = it.lowest, end = it.end;
     uint32_t pos = it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok, ahead = pos;
-    const uint8_t* const head = a.kv.pages + (int64_t)it.kvh * 2 * a.kv.block;
+    const uint8_t* const head = a.kv.pages + (int64_t)it.kvh * 2 * a.kv.block + ((uint32_t)(wg * kOwn) << (a.kv.log_page + 4));
     const int32_t* const table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
-    const uint8_t* blk = nullptr;  // of the next token, as `ahead`; null: nothing to read
+    const uint32_t page_bytes = (uint32_t)a.kv.page, slot_mask = (1u << a.kv.log_page) - 1u;
+    const uint8_t *code_src = nullptr, *scale_src = nullptr;  // of the next token's keys
+    bool some = false;                                        // there is something to read
     int32_t left = tiles, page = 0;
     auto find_page = [&] {
       page = -1;
       if (left > 0 && ahead >= lowest && ahead < end) page = table[ahead >> a.kv.log_page];
     };
-    auto aim = [&] {  // at the token whose page is known
-      blk = page >= 0 ? head + (int64_t)page * a.kv.page : nullptr;
-      slot = ahead & ((1u << a.kv.log_page) - 1u);
+    auto aim = [&] {  // at the token `ahead`, whose page is known
+      const uint32_t slot = ahead & slot_mask;
+      some = page >= 0;
+      const uint8_t* const at = head + (uint64_t)(uint32_t)page * page_bytes;
+      code_src = at + (uint64_t)slot * 16u;
+      // four scale bytes of a token, or two each of a pair of tokens
+      scale_src = at + scale_off + (D == 128 ? slot * 4u : (slot & ~1u) * 2u);
       ahead += kTile;
       --left;
     };
     auto fetch = [&](int which) {
-      if (blk != nullptr) {
-        const uint8_t* const b0 = which ? blk + a.kv.block : blk;
-        const uint8_t* const c0 = b0 + ((((uint32_t)(wg * kOwn) << a.kv.log_page) + slot) << 4);
-        copy_async16(c_at + (uint32_t)which * kCodes, c0);
-        if (kOwn == 2) copy_async16(c_at + (uint32_t)which * kCodes + kComputeThreads * 16, c0 + (16u << a.kv.log_page));
-        // four scale bytes of a token, or two each of a pair of tokens
-        copy_async4(sb_at + (uint32_t)which * kCodes, b0 + (D / 2 << a.kv.log_page) + ((slot * (D / kKvGroup)) & ~3u));
+      if (some) {
+        const uint32_t o = which ? (uint32_t)a.kv.block : 0u;
+        copy_async16(c_at + (uint32_t)which * kCodes, code_src + o);
+        if (kOwn == 2) copy_async16(c_at + (uint32_t)which * kCodes + kComputeThreads * 16, code_src + o + (16u << a.kv.log_page));
+        copy_async4(sb_at + (uint32_t)which * kCodes, scale_src + o);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -649,15 +676,17 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         for (int y = 0; y < 4; ++y) add_halves(w[y], l[cb * 8 + 2 * y], l[cb * 8 + 2 * y + 1]);
       };
       auto weights = [&](auto with_mask) {
-        float x[2][8];
-        tmem_ld8(s_at, x[0]);
-        tmem_wait_ld();
+        // S of the next block is on its way, where there are registers for it
+        constexpr int kAhead = kBlocks <= 2 ? 1 : 0;
+        float x[kAhead + 1][8];
+        if (kAhead) tmem_ld8(s_at, x[0]);
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb)
           if (cb < n16) {
-            if (cb + 1 < kBlocks && cb + 1 < n16) tmem_ld8(s_at + (uint32_t)(cb + 1) * 16u, x[(cb + 1) & 1]);
-            block(cb, x[cb & 1], with_mask);
+            if (!kAhead) tmem_ld8(s_at + (uint32_t)cb * 16u, x[0]);
             tmem_wait_ld();
+            if (kAhead && cb + 1 < kBlocks && cb + 1 < n16) tmem_ld8(s_at + (uint32_t)(cb + 1) * 16u, x[(cb + 1) & kAhead]);
+            block(cb, x[cb & kAhead], with_mask);
           }
       };
       if (!first) {  // no reference yet on the first one
@@ -850,31 +879,28 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
 constexpr int kJoinThreads = 256;
 
 // One warp per CTA and column: where the CTA's last item goes on in others, the column is the sum of
-// its parts, in the line's order.  The same warps go over the rows: a refused session's become zero.
+// its parts, in the line's order.
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
   constexpr int kPer = D / 32;
   const int lane = (int)(threadIdx.x & 31u);
-  const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), ids = (int64_t)gridDim.x * (kJoinThreads / 32);
+  const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)), cta = id / kCols, j = id - cta * kCols;
   wait_for_previous();
   const bool failed = *a.error != 0u;
   if (failed)
     for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
       a.status[b] = SDCP_S_INTERNAL;
-  const int64_t cta = id / kCols;
-  const int j = (int)(id - cta * kCols);
-  if (cta < a.ctas && !failed) {
-    const Cut cut = a.cuts[cta];
-    if (j < cut.n) {
+  const Cut cut = a.cuts[cta];
+  if (!failed && j < cut.n) {
       const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
-      auto part = [&](int32_t c) -> const Part<D, kCols>& { return parts[c == (int32_t)cta ? cut.first_slot : 2 * c]; };
+      auto part = [&](int32_t c) -> const Part<D, kCols>& { return parts[c == cta ? cut.first_slot : 2 * c]; };
       float m = -INFINITY;
-      for (int32_t c = (int32_t)cta + lane; c <= cut.last; c += 32) m = fmaxf(m, part(c).m[j]);
+      for (int32_t c = cta + lane; c <= cut.last; c += 32) m = fmaxf(m, part(c).m[j]);
       m = warp_max(m);
       float sum = 0.0f, o[kPer];
 #pragma unroll
       for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
-      for (int32_t c0 = (int32_t)cta; c0 <= cut.last; c0 += 32) {
+      for (int32_t c0 = cta; c0 <= cut.last; c0 += 32) {
         // a lane's part: its factor, 0 where it holds nothing of the column (its O may not be written)
         const int32_t n = min(32, cut.last - c0 + 1);
         float f = 0.0f;
@@ -896,14 +922,6 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
       __nv_bfloat16* const out = a.out + ((cut.row + r) * a.q_heads + cut.row_head - cut.g0 + (cut.g0 + j - r * share)) * D;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) out[lane + 32 * k] = __float2bfloat16_rn(__fdividef(o[k], sum));
-    }
-  }
-  for (int64_t row = id; row < rows; row += ids) {
-    const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
-    const int64_t i = row - a.s.offsets[b] - b;
-    if (!failed && a.units[b] > 0 && i >= 0 && i <= (int64_t)a.s.offsets[b + 1] - a.s.offsets[b]) continue;
-    for (int64_t x = lane; x < (int64_t)a.q_heads * D / 8; x += 32)
-      reinterpret_cast<uint4*>(a.out + row * a.q_heads * D)[x] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -948,7 +966,7 @@ cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
   e = launch_after(attend_kernel<D, kCols>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D, kCols>::kBytes, st, a);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.ctas * kCols;
-  return launch_after(attend_join_kernel<D, kCols>, (unsigned)(warps / (kJoinThreads / 32)), kJoinThreads, 0, st, a, a.s.total + a.s.B);
+  return launch_after(attend_join_kernel<D, kCols>, (unsigned)(warps / (kJoinThreads / 32)), kJoinThreads, 0, st, a);
 }
 
 template <int D>
@@ -998,7 +1016,7 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   const AttendArgs a{kv, s, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
                      static_cast<__nv_bfloat16*>(out), status, reinterpret_cast<uint32_t*>(w), reinterpret_cast<int64_t*>(lines),
                      reinterpret_cast<SessionPlan*>(plans), reinterpret_cast<float*>(parts), reinterpret_cast<Cut*>(cuts),
-                     0, columns_of(B, total_drafts, q_heads / cache->kv_heads)};
+                     0, columns_of(B, total_drafts, q_heads / cache->kv_heads), D};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (D == 128) e = a.cols == 32 ? launch_attend<128, 32>(a, di.sms, st) : launch_attend<128, 96>(a, di.sms, st);
