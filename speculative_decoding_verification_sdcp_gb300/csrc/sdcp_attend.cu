@@ -285,26 +285,33 @@ __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
 // Byte g of w in both halves of a word.
 __device__ __forceinline__ uint32_t twice(uint32_t w, int g) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * g); }
 
-// (a & b) | c in one instruction, which the two constants would keep the compiler from.
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+// (a & kMask) | c in one instruction; c is a constant that the compiler is kept from loading anew at
+// each use (kept(), once).
+template <uint32_t kMask> __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t c) {
   uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "n"(kMask), "r"(c));
   return d;
+}
+__device__ __forceinline__ uint32_t kept(uint32_t x) {
+  uint32_t y;
+  asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // A word of eight codes as pairs of numbers n s.  bfloat16: the four bits in the low end of
-// 128 + 8 + n; the pairs of a word lie four bits apart.
-__device__ __forceinline__ void word_bf16(uint32_t w, uint32_t s, uint32_t c, uint32_t* r) {
+// 128 + 8 + n (one: 128 twice); the pairs of a word lie four bits apart.
+__device__ __forceinline__ void word_bf16(uint32_t w, uint32_t one, uint32_t s, uint32_t c, uint32_t* r) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = fma_bf16x2(and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u), s, c);
+  for (int j = 0; j < 4; ++j) r[j] = fma_bf16x2(and_or<0x000F000Fu>(w >> (4 * j), one), s, c);
 }
-// binary16: 1024 + 8 + n in the low four bits, or 1024 + 16 (8 + n) in the next four, with s / 16.
-__device__ __forceinline__ void word_f16(uint32_t w, uint32_t s, uint32_t c, uint32_t s16, uint32_t c16, uint32_t* r) {
+// binary16: 1024 + 8 + n in the low four bits, or 1024 + 16 (8 + n) in the next four, with s / 16
+// (one: 1024 twice).
+__device__ __forceinline__ void word_f16(uint32_t w, uint32_t one, uint32_t s, uint32_t c, uint32_t s16, uint32_t c16, uint32_t* r) {
   const uint32_t h = w >> 8;
-  r[0] = fma_f16x2(and_or(w, 0x000F000Fu, 0x64006400u), s, c);
-  r[1] = fma_f16x2(and_or(w, 0x00F000F0u, 0x64006400u), s16, c16);
-  r[2] = fma_f16x2(and_or(h, 0x000F000Fu, 0x64006400u), s, c);
-  r[3] = fma_f16x2(and_or(h, 0x00F000F0u, 0x64006400u), s16, c16);
+  r[0] = fma_f16x2(and_or<0x000F000Fu>(w, one), s, c);
+  r[1] = fma_f16x2(and_or<0x00F000F0u>(w, one), s16, c16);
+  r[2] = fma_f16x2(and_or<0x000F000Fu>(h, one), s, c);
+  r[3] = fma_f16x2(and_or<0x00F000F0u>(h, one), s16, c16);
 }
 
 template <int D, int kCols> struct AttendSmem {
@@ -501,9 +508,10 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
   using Sh = Shape<kCols>;
   constexpr int kOwn = D / kKvGroup / 2;  // channel groups of a thread
   constexpr int kBlocks = Sh::kHalf / 8;
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wg = tid >> 7, tok = tid & 127;
-  const uint32_t my_lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes of tensor memory, in bits 16 up
+  const int tid = (int)kept(threadIdx.x), lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int wg = warp >> 2, tok = tid & 127;
+  const uint32_t my_lanes = __shfl_sync(0xFFFFFFFFu, tmem + ((uint32_t)(warp & 3) << 21), 0);  // 32 lanes of tensor memory, in bits 16 up
+  const uint32_t one_k = kept(0x43004300u), one_v = kept(0x64006400u);
   const uint32_t win = a.s.window > 0 ? (uint32_t)a.s.window : 0x80000000u;
   const int32_t share = a.q_heads / a.kv.heads;
   const uint32_t swizzled = (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);
@@ -614,10 +622,10 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
         const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
         uint32_t r[16];
-        word_bf16(c.x, s, m, r);
-        word_bf16(c.y, s, m, r + 4);
-        word_bf16(c.z, s, m, r + 8);
-        word_bf16(c.w, s, m, r + 12);
+        word_bf16(c.x, one_k, s, m, r);
+        word_bf16(c.y, one_k, s, m, r + 4);
+        word_bf16(c.z, one_k, s, m, r + 8);
+        word_bf16(c.w, one_k, s, m, r + 12);
         tmem_st16(my_lanes + (uint32_t)((wg * kOwn + g) * 16), r);
       }
       tmem_wait_st();
@@ -641,7 +649,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t r[4];
-          word_f16(w[x], s, m, s16, m16, r);
+          word_f16(w[x], one_v, s, m, s16, m16, r);
           st_shared16(v_at ^ (uint32_t)((g * 4 + x) << 4), r[0], r[1], r[2], r[3]);
         }
       }
@@ -689,16 +697,19 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
             block(cb, x[cb & kAhead], with_mask);
           }
       };
-      if (!first) {  // no reference yet on the first one
-        if (masked) weights(std::true_type{});
-        else weights(std::false_type{});
-      }
-      fence_async_smem();
-      fence_before();
-      if (any(top > kTop || first || dead)) {
+      bool again = false, gone = false;
+      while (true) {
+        if (!first || again) {  // no reference yet on the first one
+          if (masked) weights(std::true_type{});
+          else weights(std::false_type{});
+        }
+        fence_async_smem();
+        fence_before();
+        if (!any(!again && (top > kTop || first || dead))) break;
         // slow path: the tile's weights out of the sums, its columns' maxima, new references, O and
         // the sums rescaled, and the weights again
-        if (any(dead)) break;
+        if ((gone = any(dead))) break;
+        again = true;
         fence_after();
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb)
@@ -730,28 +741,26 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
           sh.f[tid] = f;
         }
         meet();
+        if (!first) {
 #pragma unroll
-        for (int cb = 0; cb < kBlocks; ++cb)
-          if (cb < n16) {
-            const int j0 = cb * 16 + wg * 8;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) l[cb * 8 + y] *= sh.f[j0 + y];
-            if (!first) {
+          for (int cb = 0; cb < kBlocks; ++cb)
+            if (cb < n16) {
+              const int j0 = cb * 16 + wg * 8;
               float o[8];
               const uint32_t o_at = my_lanes + Sh::kTmemO + (uint32_t)j0;
               tmem_ld8(o_at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 8; ++y) o[y] *= sh.f[j0 + y];
+              for (int y = 0; y < 8; ++y) {
+                l[cb * 8 + y] *= sh.f[j0 + y];
+                o[y] *= sh.f[j0 + y];
+              }
               tmem_st8(o_at, o);
             }
-          }
-        weights(std::true_type{});
-        tmem_wait_st();
-        fence_async_smem();
-        fence_before();
-        meet();
+          tmem_wait_st();
+        }
       }
+      if (gone) break;
       if (tid == 0) mbar_arrive(&sh.p_full);
     }
 
