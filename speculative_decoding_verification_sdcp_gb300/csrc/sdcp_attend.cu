@@ -242,25 +242,25 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Sums of eight values over a warp: each exchange halves the values a lane carries, and lanes
-// 0..7 end with the sum of value `lane`.
-__device__ __forceinline__ float warp_sum8(const float* x, int lane) {
+// Eight values folded over a warp: each exchange halves the values a lane carries, and lanes 0..7 end
+// with value `lane` of all lanes.
+template <typename F>
+__device__ __forceinline__ float warp_fold8(const float* x, int lane, F op) {
   float y[4], z[2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float keep = (lane & 4) ? x[k + 4] : x[k], give = (lane & 4) ? x[k] : x[k + 4];
-    y[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+    y[k] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 4));
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float keep = (lane & 2) ? y[k + 2] : y[k], give = (lane & 2) ? y[k] : y[k + 2];
-    z[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+    z[k] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 2));
   }
   const float keep = (lane & 1) ? z[1] : z[0], give = (lane & 1) ? z[0] : z[1];
-  float s = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
-  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
-  return s;
+  float s = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 1));
+  s = op(s, __shfl_xor_sync(0xFFFFFFFFu, s, 8));
+  return op(s, __shfl_xor_sync(0xFFFFFFFFu, s, 16));
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -278,6 +278,9 @@ __device__ __forceinline__ uint32_t ld_shared4(uint32_t at) {
 }
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async16_or_zero(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -477,7 +480,6 @@ __device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols
     if (tiles <= 0) return;
     const uint32_t idesc = kIdescF32 | kIdescM128 | (uint32_t)((sh.item[j & 1u].n + 15) / 16 * 2) << 17;
     if ((threadIdx.x & 31u) == 0) {
-      plan_item<D, kCols>(a, sh, line, j + 1);
       for (int32_t k = 0; k < tiles; ++k, ++i) {
         const uint32_t par = i & 1u;
         if (!wait_phase(&sh.k_full, par, &sh.dead)) { sh.dead = 1; break; }
@@ -487,6 +489,7 @@ __device__ __forceinline__ void multiply(const AttendArgs& a, AttendShared<kCols
           mma_tmem_a(tmem + Sh::kTmemS, tmem + (uint32_t)x * 8u, q_mat + (uint64_t)(((x / 4) * (kCols * 128) + (x % 4) * 32) >> 4),
                      idesc | kIdescBf16, x > 0);
         mma_commit(&sh.s_full);
+        if (k == 0) plan_item<D, kCols>(a, sh, line, j + 1);
         if (!wait_phase(&sh.p_full, par, &sh.dead)) { sh.dead = 1; break; }
         fence_after();
 #pragma unroll
@@ -545,6 +548,27 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     if (tiles <= 0) return;
     const int32_t n16 = (it.n + 15) / 16;  // blocks of 16 columns; a group of threads has eight of each
 
+    // queries of the columns, zero past them (the oldest group of copies: they are there with the first
+    // keys), and the columns' state
+    {
+      const __nv_bfloat16* const q0 = a.q + ((int64_t)it.off + it.b + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
+      const int ch = tid % (D / 8);
+      const uint32_t dst = smem_u32(s_q) + (uint32_t)(ch / 8) * (kCols * 128);
+#pragma unroll 2
+      for (int col = tid / (D / 8); col < n16 * 16; col += kComputeThreads / (D / 8)) {
+        const int32_t c = min(col, it.n - 1) + it.g0, r = c / share;
+        copy_async16_or_zero(dst + (uint32_t)col * 128u + (uint32_t)(((ch & 7) ^ (col & 7)) << 4), q0 + r * a.q_stride + (c - r * share) * D + ch * 8,
+                             col < it.n);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    if (tid < kCols) {
+      const int32_t r = (it.g0 + tid) / share;
+      sh.at[tid] = r * a.q_heads + it.g0 + tid - r * share;
+      sh.nm[tid] = tid < it.n ? INFINITY : kLift;
+      sh.last[tid] = tid < it.n ? it.len + it.i0 + r : INT_MAX;
+    }
+
     // a tile ahead: the page of the next token, and the copy of the thread's share of its codes to
     // the thread's own places in shared memory (a token that is not read keeps old codes: finite
     // numbers, whose weight is zero)
@@ -585,27 +609,6 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     fetch(0);
     fetch(1);
 
-    // queries of the columns, zero past them, and the columns' state
-    if (tid < kCols) {
-      const int32_t r = (it.g0 + tid) / share;
-      sh.at[tid] = r * a.q_heads + it.g0 + tid - r * share;
-      sh.nm[tid] = tid < it.n ? INFINITY : kLift;
-      sh.last[tid] = tid < it.n ? it.len + it.i0 + r : INT_MAX;
-    }
-    {
-      const __nv_bfloat16* const q0 = a.q + ((int64_t)it.off + it.b + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
-      const int ch = tid % (D / 8);
-      unsigned char* const dst = s_q + (ch / 8) * (kCols * 128);
-      for (int col = tid / (D / 8); col < n16 * 16; col += kComputeThreads / (D / 8)) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (col < it.n) {
-          const int32_t r = (it.g0 + col) / share;
-          v = *reinterpret_cast<const uint4*>(q0 + r * a.q_stride + (it.g0 + col - r * share) * D + ch * 8);
-        }
-        *reinterpret_cast<uint4*>(dst + col * 128 + (((ch & 7) ^ (col & 7)) << 4)) = v;
-      }
-      fence_async_smem();  // seen by the first S product through the keys' barrier
-    }
     const uint32_t low_last = (uint32_t)(it.len + it.i0), high_last = end - 1u;  // of the columns
     float l[Sh::kHalf];
 #pragma unroll
@@ -629,6 +632,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         tmem_st16(my_lanes + (uint32_t)((wg * kOwn + g) * 16), r);
       }
       tmem_wait_st();
+      if (first) fence_async_smem();  // the queries
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full);
@@ -725,9 +729,10 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
                 const uint32_t w = pack_f16x2(hidden ? 0.0f : ex2(fmaf(x[y], a.c, sh.nm[j0 + y])), 0.0f);
                 l[cb * 8 + y] -= __half2float(__ushort_as_half((unsigned short)w));
               }
-              const float m = warp_max(hidden ? -INFINITY : x[y] * a.c);
-              if (lane == 0) sh.red[warp & 3][j0 + y] = m;
+              x[y] = hidden ? -INFINITY : x[y] * a.c;
             }
+            const float m = warp_fold8(x, lane, [](float p, float q) { return fmaxf(p, q); });  // NaN left out
+            if (lane < 8) sh.red[warp & 3][j0 + lane] = m;
           }
         meet();
         if (tid < kCols) {
@@ -770,7 +775,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
 #pragma unroll
     for (int cb = 0; cb < kBlocks; ++cb)
       if (cb < n16) {
-        const float x = warp_sum8(&l[cb * 8], lane);
+        const float x = warp_fold8(&l[cb * 8], lane, [](float p, float q) { return p + q; });
         if (lane < 8) sh.red[warp & 3][cb * 16 + wg * 8 + lane] = x;
       }
     if (any(dead)) {
@@ -788,7 +793,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     }
     meet();
     __nv_bfloat16* const out0 = a.out + (((int64_t)it.off + it.b + it.i0) * a.q_heads + (int64_t)it.kvh * share) * D + tok;
-#pragma unroll 1
+#pragma unroll 2
     for (int cb = 0; cb < n16; ++cb) {
       const int j0 = cb * 16 + wg * 8;
       float o[8];
