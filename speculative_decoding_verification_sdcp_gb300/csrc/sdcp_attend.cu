@@ -67,7 +67,7 @@ constexpr float kTop = 15.0f;     // and 2^kTop at most
 struct SessionPlan {
   int32_t w, chunks, tiles;
 };
-constexpr int32_t kItemUnits = 2;  // what an item's start and end cost, in tiles
+constexpr int32_t kItemUnits = 4;  // what an item's start and end cost, in tiles (2: 198 us, 4: 188, 8: 194, 72 columns)
 
 // The item that a CTA begins and another one goes on with: its parts are the CTA's second (or, where
 // it began with it, first) and the first of the CTAs after it, up to `last`.  n = 0: none.
@@ -536,8 +536,6 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
   const int sb_shift = D == 128 ? wg * 16 : (tok & 1) * 16 + wg * 8;  // of the thread's own scales (tiles start at even tokens)
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at + kCodes), "r"(0u) : "memory");
-  // scales from the thread's codes: past the block's codes (D / 2 bytes a token), less the thread's own start
-  const int64_t scale_off = (int64_t)(D / 2 << a.kv.log_page) - ((wg * kOwn) << (a.kv.log_page + 4));
   uint32_t i = 0;  // tiles so far
   bool dead = false;  // a wait gave up: the eight warps agree on it at a vote, all nine at an item's start
   for (uint32_t j = 0;; ++j) {
@@ -573,41 +571,26 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     // the thread's own places in shared memory (a token that is not read keeps old codes: finite
     // numbers, whose weight is zero)
     const uint32_t lowest = it.lowest, end = it.end;
-    uint32_t pos = it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok, ahead = pos;
-    const uint8_t* const head = a.kv.pages + (int64_t)it.kvh * 2 * a.kv.block + ((uint32_t)(wg * kOwn) << (a.kv.log_page + 4));
+    uint32_t pos = it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok;
+    const uint32_t in_page = (uint32_t)it.kvh * 2u * (uint32_t)a.kv.block;  // the head's keys
     const int32_t* const table = a.kv.page_table + (int64_t)it.b * a.kv.max_pages;
-    const uint32_t page_bytes = (uint32_t)a.kv.page, slot_mask = (1u << a.kv.log_page) - 1u;
-    const uint8_t *code_src = nullptr, *scale_src = nullptr;  // of the next token's keys
-    bool some = false;                                        // there is something to read
-    int32_t left = tiles, page = 0;
-    auto find_page = [&] {
-      page = -1;
-      if (left > 0 && ahead >= lowest && ahead < end) page = table[ahead >> a.kv.log_page];
-    };
-    auto aim = [&] {  // at the token `ahead`, whose page is known
-      const uint32_t slot = ahead & slot_mask;
-      some = page >= 0;
-      const uint8_t* const at = head + (uint64_t)(uint32_t)page * page_bytes;
-      code_src = at + (uint64_t)slot * 16u;
-      // four scale bytes of a token, or two each of a pair of tokens
-      scale_src = at + scale_off + (D == 128 ? slot * 4u : (slot & ~1u) * 2u);
-      ahead += kTile;
-      --left;
-    };
-    auto fetch = [&](int which) {
-      if (some) {
-        const uint32_t o = which ? (uint32_t)a.kv.block : 0u;
-        copy_async16(c_at + (uint32_t)which * kCodes, code_src + o);
-        if (kOwn == 2) copy_async16(c_at + (uint32_t)which * kCodes + kComputeThreads * 16, code_src + o + (16u << a.kv.log_page));
-        copy_async4(sb_at + (uint32_t)which * kCodes, scale_src + o);
+    auto page_of = [&](uint32_t p, bool some) { return some && p >= lowest && p < end ? table[p >> a.kv.log_page] : -1; };
+    auto fetch = [&](int which, uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read)
+      if (page >= 0) {
+        const uint32_t slot = p & ((1u << a.kv.log_page) - 1u);
+        const uint8_t* const blk = a.kv.pages + (uint64_t)(uint32_t)page * (uint32_t)a.kv.page + (in_page + (which ? (uint32_t)a.kv.block : 0u));
+        const uint32_t o = (((uint32_t)(wg * kOwn) << a.kv.log_page) + slot) * 16u;
+        copy_async16(c_at + (uint32_t)which * kCodes, blk + o);
+        if (kOwn == 2) copy_async16(c_at + (uint32_t)which * kCodes + kComputeThreads * 16, blk + (o + (16u << a.kv.log_page)));
+        // four scale bytes of a token, or two each of a pair of tokens
+        copy_async4(sb_at + (uint32_t)which * kCodes, blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    find_page();
-    aim();
-    find_page();
-    fetch(0);
-    fetch(1);
+    int32_t page = page_of(pos, true);
+    fetch(0, pos, page);
+    fetch(1, pos, page);
+    page = page_of(pos + kTile, tiles > 1);
 
     const uint32_t low_last = (uint32_t)(it.len + it.i0), high_last = end - 1u;  // of the columns
     float l[Sh::kHalf];
@@ -636,9 +619,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.k_full);
-      aim();
-      find_page();
-      fetch(0);
+      fetch(0, pos + kTile, page);
       // values to shared memory, once the O product has read the ones before
       if (i > 0) dead |= !wait_phase(&sh.pv_done, (i - 1u) & 1u, &sh.dead);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -657,7 +638,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
           st_shared16(v_at ^ (uint32_t)((g * 4 + x) << 4), r[0], r[1], r[2], r[3]);
         }
       }
-      fetch(1);
+      fetch(1, pos + kTile, page);
+      page = page_of(pos + 2 * kTile, k + 2 < tiles);
 
       // weights of this group's columns with the references at hand; into the sums
       const uint32_t lo = pos - (uint32_t)tok;
