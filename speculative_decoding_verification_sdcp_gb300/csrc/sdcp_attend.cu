@@ -621,7 +621,6 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
       if (lane == 0) mbar_arrive(&sh.k_full);
       fetch(0, pos + kTile, page);
       // values to shared memory, once the O product has read the ones before
-      if (i > 0) dead |= !wait_phase(&sh.pv_done, (i - 1u) & 1u, &sh.dead);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       sb = ld_shared4(sb_at + kCodes) >> sb_shift;
 #pragma unroll
@@ -630,13 +629,14 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         const uint32_t s = twice(sb, g) << 7;
         const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
         const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        uint32_t r[16];
+        word_f16(c.x, one_v, s, m, s16, m16, r);
+        word_f16(c.y, one_v, s, m, s16, m16, r + 4);
+        word_f16(c.z, one_v, s, m, s16, m16, r + 8);
+        word_f16(c.w, one_v, s, m, s16, m16, r + 12);
+        if (g == 0 && i > 0) dead |= !wait_phase(&sh.pv_done, (i - 1u) & 1u, &sh.dead);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t r[4];
-          word_f16(w[x], one_v, s, m, s16, m16, r);
-          st_shared16(v_at ^ (uint32_t)((g * 4 + x) << 4), r[0], r[1], r[2], r[3]);
-        }
+        for (int x = 0; x < 4; ++x) st_shared16(v_at ^ (uint32_t)((g * 4 + x) << 4), r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
       }
       fetch(1, pos + kTile, page);
       page = page_of(pos + 2 * kTile, k + 2 < tiles);
@@ -670,17 +670,13 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         for (int y = 0; y < 4; ++y) add_halves(w[y], l[cb * 8 + 2 * y], l[cb * 8 + 2 * y + 1]);
       };
       auto weights = [&](auto with_mask) {
-        // S of the next block is on its way, where there are registers for it
-        constexpr int kAhead = kBlocks <= 2 ? 1 : 0;
-        float x[kAhead + 1][8];
-        if (kAhead) tmem_ld8(s_at, x[0]);
 #pragma unroll
         for (int cb = 0; cb < kBlocks; ++cb)
           if (cb < n16) {
-            if (!kAhead) tmem_ld8(s_at + (uint32_t)cb * 16u, x[0]);
+            float x[8];
+            tmem_ld8(s_at + (uint32_t)cb * 16u, x);
             tmem_wait_ld();
-            if (kAhead && cb + 1 < kBlocks && cb + 1 < n16) tmem_ld8(s_at + (uint32_t)(cb + 1) * 16u, x[(cb + 1) & kAhead]);
-            block(cb, x[cb & kAhead], with_mask);
+            block(cb, x, with_mask);
           }
       };
       bool again = false, gone = false;
