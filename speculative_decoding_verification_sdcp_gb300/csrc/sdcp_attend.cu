@@ -199,7 +199,7 @@ __device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile int* dead) {
-  if (poll_phase(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity) || poll_phase(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   while (!poll_phase(bar, parity))
     if ((dead != nullptr && *dead) || global_ns() - t0 > kWaitNs) return false;
@@ -693,25 +693,37 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         if ((gone = any(dead))) break;
         again = true;
         fence_after();
-#pragma unroll
-        for (int cb = 0; cb < kBlocks; ++cb)
-          if (cb < n16) {
+        if (first) {  // (rolled: run once an item, its instructions are fetched anew each time)
+#pragma unroll 1
+          for (int cb = 0; cb < n16; ++cb) {
             const int j0 = cb * 16 + wg * 8;
             float x[8];
             tmem_ld8(s_at + (uint32_t)cb * 16u, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const bool hidden = masked && (uint32_t)sh.last[j0 + y] - pos >= win;
-              if (!first) {
-                const uint32_t w = pack_f16x2(hidden ? 0.0f : ex2(fmaf(x[y], a.c, sh.nm[j0 + y])), 0.0f);
-                l[cb * 8 + y] -= __half2float(__ushort_as_half((unsigned short)w));
-              }
-              x[y] = hidden ? -INFINITY : x[y] * a.c;
-            }
+            for (int y = 0; y < 8; ++y) x[y] = (uint32_t)sh.last[j0 + y] - pos >= win ? -INFINITY : x[y] * a.c;
             const float m = warp_fold8(x, lane, [](float p, float q) { return fmaxf(p, q); });  // NaN left out
             if (lane < 8) sh.red[warp & 3][j0 + lane] = m;
           }
+        } else {
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb)
+            if (cb < n16) {
+              const int j0 = cb * 16 + wg * 8;
+              float x[8];
+              tmem_ld8(s_at + (uint32_t)cb * 16u, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const bool hidden = masked && (uint32_t)sh.last[j0 + y] - pos >= win;
+                const uint32_t w = pack_f16x2(hidden ? 0.0f : ex2(fmaf(x[y], a.c, sh.nm[j0 + y])), 0.0f);
+                l[cb * 8 + y] -= __half2float(__ushort_as_half((unsigned short)w));
+                x[y] = hidden ? -INFINITY : x[y] * a.c;
+              }
+              const float m = warp_fold8(x, lane, [](float p, float q) { return fmaxf(p, q); });
+              if (lane < 8) sh.red[warp & 3][j0 + lane] = m;
+            }
+        }
         meet();
         if (tid < kCols) {
           float f = 1.0f;
@@ -771,7 +783,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
     }
     meet();
     __nv_bfloat16* const out0 = a.out + (((int64_t)it.off + it.b + it.i0) * a.q_heads + (int64_t)it.kvh * share) * D + tok;
-#pragma unroll 2
+#pragma unroll 1
     for (int cb = 0; cb < n16; ++cb) {
       const int j0 = cb * 16 + wg * 8;
       float o[8];
@@ -873,15 +885,16 @@ constexpr int kJoinThreads = 256;
 // One warp per CTA and column: where the CTA's last item goes on in others, the column is the sum of
 // its parts, in the line's order.
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int32_t cols) {
   constexpr int kPer = D / 32;
   const int lane = (int)(threadIdx.x & 31u);
-  const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)), cta = id / kCols, j = id - cta * kCols;
+  const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)), cta = id / cols, j = id - cta * cols;
   wait_for_previous();
   const bool failed = *a.error != 0u;
   if (failed)
     for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
       a.status[b] = SDCP_S_INTERNAL;
+  if (cta >= a.ctas) return;
   const Cut cut = a.cuts[cta];
   if (!failed && j < cut.n) {
       const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
@@ -957,8 +970,9 @@ cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_after(attend_kernel<D, kCols>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D, kCols>::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  const int64_t warps = (int64_t)a.ctas * kCols;
-  return launch_after(attend_join_kernel<D, kCols>, (unsigned)(warps / (kJoinThreads / 32)), kJoinThreads, 0, st, a);
+  const int32_t cols = (int32_t)min((int64_t)kCols, (a.s.total + a.s.B) * (a.q_heads / a.kv.heads));  // no item has more
+  const int32_t warps = a.ctas * cols, per = kJoinThreads / 32;
+  return launch_after(attend_join_kernel<D, kCols>, (unsigned)((warps + per - 1) / per), kJoinThreads, 0, st, a, cols);
 }
 
 template <int D>

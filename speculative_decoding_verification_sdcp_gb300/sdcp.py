@@ -295,8 +295,19 @@ def _is(t, dtype, what):
     return t
 
 
+def _ints(what, a, b, c):
+    """_is for the three index tensors of a call, together."""
+    if not (a.dtype is b.dtype is c.dtype is torch.int32 and a.is_contiguous() and b.is_contiguous() and c.is_contiguous()):
+        raise TypeError("%s must be contiguous torch.int32 tensors" % what)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+# the handle of a device's current stream, without the object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(fn, what, device, stream, *args):
@@ -306,7 +317,7 @@ def _call(fn, what, device, stream, *args):
     here = torch.cuda.current_device()
     index = here if device.index is None else device.index
     if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
+        stream = _raw_stream(index)
     if index == here:
         rc = fn(*args, stream)
     else:
@@ -323,27 +334,38 @@ def sdcp_adjust_logits(logits, out, m_offsets, total_drafts, draft_tokens, contr
     may be logits).  controls_dev: CONTROLS_DTYPE records as a uint8 tensor; history: int32
     [B, stride] or None; bias_tokens / bias_values: int32 / float32 [n]; masks: int32 [n_masks,
     words], one bit a token; mask_rows: int32 [rows], -1 = none; status: int32 [B], written."""
-    V = logits.shape[1]
-    B = status.shape[0]
+    n_logits, V = logits.shape
+    B, total = status.shape[0], int(total_drafts)
     code = dtype_code(logits)
-    n_rows = int(total_drafts) + (B if rows == ROWS_TARGET else 0)
-    if not logits.is_contiguous() or not out.is_contiguous() or out.dtype != logits.dtype or out.shape != logits.shape:
+    n_rows = total + (B if rows == ROWS_TARGET else 0)
+    if out is not logits and (out.dtype is not logits.dtype or out.shape != logits.shape or not out.is_contiguous()) or not logits.is_contiguous():
         raise TypeError("logits and out must be contiguous tensors of one shape and type")
-    if logits.shape[0] < n_rows or (mask_rows is not None and mask_rows.numel() < n_rows):
+    _ints("m_offsets, status and mask_rows", m_offsets, status, status if mask_rows is None else mask_rows)
+    if n_logits < n_rows or (mask_rows is not None and mask_rows.numel() < n_rows):
         raise ValueError("the batch has %d rows" % n_rows)
-    _is(m_offsets, torch.int32, "m_offsets"), _is(draft_tokens, torch.int32, "draft_tokens"), _is(status, torch.int32, "status")
-    _is(history, torch.int32, "history"), _is(bias_tokens, torch.int32, "bias_tokens"), _is(bias_values, torch.float32, "bias_values")
-    _is(masks, torch.int32, "masks"), _is(mask_rows, torch.int32, "mask_rows"), _is(controls_dev, torch.uint8, "controls_dev")
-    if (m_offsets.numel() < B + 1 or controls_dev.numel() < B * 32 or (history is not None and history.shape[0] < B)
-            or (draft_tokens is not None and draft_tokens.numel() < int(total_drafts))):
-        raise ValueError("m_offsets, controls, history and draft tokens must cover the %d sessions" % B)
-    if bias_tokens is not None and (bias_values is None or bias_values.numel() != bias_tokens.numel()):
-        raise ValueError("bias_tokens and bias_values must have the same length")
+    if controls_dev.dtype is not torch.uint8 or not controls_dev.is_contiguous():
+        raise TypeError("controls_dev must be a contiguous torch.uint8 tensor")
+    if m_offsets.numel() < B + 1 or controls_dev.numel() < B * 32:
+        raise ValueError("m_offsets and controls must cover the %d sessions" % B)
+    if draft_tokens is not None and _is(draft_tokens, torch.int32, "draft_tokens").numel() < total:
+        raise ValueError("draft_tokens must hold the %d drafts" % total)
+    stride = n_bias = n_masks = words = 0
+    if history is not None:
+        if _is(history, torch.int32, "history").shape[0] < B:
+            raise ValueError("history must have a row for each of the %d sessions" % B)
+        stride = history.shape[1]
+    if bias_tokens is not None:
+        n_bias = _is(bias_tokens, torch.int32, "bias_tokens").numel()
+        if bias_values is None or _is(bias_values, torch.float32, "bias_values").numel() != n_bias:
+            raise ValueError("bias_tokens and bias_values must have the same length")
+    if masks is not None:
+        n_masks, words = _is(masks, torch.int32, "masks").shape
     _call(lib.sdcp_adjust_logits, "sdcp_adjust_logits", logits.device, stream, logits.data_ptr(), out.data_ptr(), code, V, B, int(rows),
-          m_offsets.data_ptr(), int(total_drafts), _addr(draft_tokens), controls_dev.data_ptr(), _addr(history),
-          0 if history is None else history.shape[1], _addr(bias_tokens), _addr(bias_values),
-          0 if bias_tokens is None else bias_tokens.numel(), _addr(masks), 0 if masks is None else masks.shape[1],
-          0 if masks is None else masks.shape[0], _addr(mask_rows), status.data_ptr())
+          m_offsets.data_ptr(), total, _addr(draft_tokens), controls_dev.data_ptr(), _addr(history), stride, _addr(bias_tokens),
+          _addr(bias_values), n_bias, _addr(masks), words, n_masks, _addr(mask_rows), status.data_ptr())
+
+
+_DESC_SIZE = ctypes.sizeof(KvCacheDesc)
 
 
 class KvCache:
@@ -365,10 +387,10 @@ class KvCache:
 
     def desc(self, page_table, B):
         """The description of the cache with a batch's page table (int32 [B, max_pages])."""
-        if _is(page_table, torch.int32, "page_table").shape[0] < B:
+        n, most = _is(page_table, torch.int32, "page_table").shape
+        if n < B:
             raise ValueError("page_table must have a row for each of the %d sessions" % B)
-        return KvCacheDesc(ctypes.sizeof(KvCacheDesc), self.n_pages, self.page_tokens, self.kv_heads, self.head_dim,
-                           page_table.shape[1], page_table.data_ptr(), self.pages.data_ptr())
+        return KvCacheDesc(_DESC_SIZE, self.n_pages, self.page_tokens, self.kv_heads, self.head_dim, most, page_table.data_ptr(), self.pages.data_ptr())
 
 
 class Rotary:
@@ -402,7 +424,7 @@ def sdcp_append_kv(cache, page_table, m_offsets, total_drafts, kv_len, k, v, sta
     qs = 0 if q is None else _heads(q, rows, n_q, cache.head_dim, "q")
     if q is not None and (not q_out.is_contiguous() or q_out.shape[0] < rows or q_out.shape[1:] != q.shape[1:]):
         raise ValueError("q_out must be contiguous and have q's shape")
-    _is(m_offsets, torch.int32, "m_offsets"), _is(kv_len, torch.int32, "kv_len"), _is(status, torch.int32, "status")
+    _ints("m_offsets, kv_len and status", m_offsets, kv_len, status)
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
@@ -415,18 +437,22 @@ def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, stat
     """Cached tokens as values: tokens start[b] .. of session b into rows offsets[b] ..
     offsets[b+1] - 1 of k_out and v_out [n_tokens, kv_heads, head_dim] (either may be None)."""
     B = status.shape[0]
-    outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs or any(t.dtype != outs[0].dtype for t in outs):
-        raise TypeError("k_out and v_out must have one type, and one of them must be given")
-    for t in outs:
-        if not t.is_contiguous() or t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1:] != (cache.kv_heads, cache.head_dim):
-            raise ValueError("outputs must be contiguous [n_tokens, kv_heads, head_dim] tensors")
-    _is(offsets, torch.int32, "offsets"), _is(start, torch.int32, "start"), _is(status, torch.int32, "status")
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise TypeError("k_out or v_out must be given")
+    code, heads = dtype_code(some), (cache.kv_heads, cache.head_dim)
+    for t in (k_out, v_out):
+        if t is not None:
+            if t.dtype is not some.dtype:
+                raise TypeError("k_out and v_out must have one type")
+            if not t.is_contiguous() or t.shape[0] < n_tokens or t.shape[1:] != heads:
+                raise ValueError("outputs must be contiguous [n_tokens, kv_heads, head_dim] tensors")
+    _ints("offsets, start and status", offsets, start, status)
     if offsets.numel() < B + 1 or start.numel() < B:
         raise ValueError("offsets and start must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
     _call(lib.sdcp_read_kv, "sdcp_read_kv", status.device, stream, ctypes.byref(desc), B, offsets.data_ptr(), int(n_tokens),
-          start.data_ptr(), dtype_code(outs[0]), _addr(k_out), _addr(v_out), status.data_ptr())
+          start.data_ptr(), code, _addr(k_out), _addr(v_out), status.data_ptr())
 
 
 def sdcp_attend_workspace_bytes(B: int, total_drafts: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -453,7 +479,7 @@ def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, s
     qs = _heads(q, rows, q.shape[1], cache.head_dim, "q")
     if not out.is_contiguous() or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
         raise ValueError("out must be contiguous and have q's shape")
-    _is(m_offsets, torch.int32, "m_offsets"), _is(kv_len, torch.int32, "kv_len"), _is(status, torch.int32, "status")
+    _ints("m_offsets, kv_len and status", m_offsets, kv_len, status)
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
