@@ -48,6 +48,7 @@ struct AdjustArgs {
   int32_t* status;
   int32_t slice;    // tokens of a CTA, a power of two
   int32_t n_slices; // of a session
+  int32_t by_part;  // CTAs in the order of the slices, not of the sessions
 };
 
 // One listed draft of the slice: its token (relative to the slice) and its position.
@@ -100,8 +101,8 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
   __shared__ const uint32_t* s_mask[SDCP_MAX_M + 1];  // the rows' masks, null: none
   __shared__ int32_t s_sum[kAdjThreads / 32];
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t b = (int32_t)(blockIdx.x / (uint32_t)a.n_slices);
-  const int32_t part = (int32_t)(blockIdx.x % (uint32_t)a.n_slices);
+  const uint32_t per = (uint32_t)(a.by_part ? a.B : a.n_slices), major = blockIdx.x / per, minor = blockIdx.x % per;
+  const int32_t b = (int32_t)(a.by_part ? minor : major), part = (int32_t)(a.by_part ? major : minor);
   const int64_t v0 = (int64_t)part * a.slice;
   const int32_t n = (int32_t)min((int64_t)a.slice, a.V - v0);
 
@@ -134,10 +135,13 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
     if (tid == 0) s_ndrafts = 0;
     // what the slice is told apart by: all asked for at once, before the barrier
     const int32_t* const hist = a.history + (int64_t)b * a.history_stride;
-    constexpr int kEarly = 4;
-    int32_t early[kEarly];
+    constexpr int kBatch = 8;  // tokens of the history that a thread has in flight
+    int32_t token[kBatch];
+    auto load_history = [&](uint32_t k0) {
 #pragma unroll
-    for (int u = 0; u < kEarly; ++u) early[u] = (uint32_t)(tid + u * kAdjThreads) < ctl.history_len ? hist[tid + u * kAdjThreads] : -1;
+      for (int u = 0; u < kBatch; ++u) token[u] = k0 + u * kAdjThreads < ctl.history_len ? hist[k0 + u * kAdjThreads] : -1;
+    };
+    load_history((uint32_t)tid);
     const int32_t draft = tid < M ? a.tokens[lo + tid] : -1;
     if (tid < rows) {
       int32_t r = a.mask_rows ? a.mask_rows[row0 + tid] : -1;
@@ -150,18 +154,18 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
     __syncthreads();
 
     // the slice's counts, biases and drafts
-    auto count = [&](uint32_t k, int32_t token) {
-      const uint32_t at = (uint32_t)token - (uint32_t)v0;  // beyond the slice: >= n
-      if (at < (uint32_t)n) {
-        if (k < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
-        else atomicAdd(&words[at], 1u);
-        atomicOr(&marks[at >> 5], 1u << (at & 31u));
-      }
-    };
+    for (uint32_t k0 = (uint32_t)tid; k0 < ctl.history_len; k0 += kBatch * kAdjThreads) {
+      if (k0 != (uint32_t)tid) load_history(k0);
 #pragma unroll
-    for (int u = 0; u < kEarly; ++u) count((uint32_t)(tid + u * kAdjThreads), early[u]);
-#pragma unroll 4
-    for (uint32_t k = tid + kEarly * kAdjThreads; k < ctl.history_len; k += kAdjThreads) count(k, hist[k]);
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t at = (uint32_t)token[u] - (uint32_t)v0;  // beyond the slice: >= n
+        if (at < (uint32_t)n) {
+          if (k0 + u * kAdjThreads < ctl.prompt_len) atomicOr(&words[at], kInPrompt);
+          else atomicAdd(&words[at], 1u);
+          atomicOr(&marks[at >> 5], 1u << (at & 31u));
+        }
+      }
+    }
     for (uint32_t k = tid; k < ctl.bias_count; k += kAdjThreads) {
       const int32_t t = a.bias_tokens[ctl.bias_offset + k];
       const int32_t before = k ? a.bias_tokens[ctl.bias_offset + k - 1] : -1;
@@ -307,8 +311,8 @@ cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
 
 // Tokens of a slice: 4096 while a session has fewer than eight rows on average (what a CTA does
 // besides streaming is then spread over more tokens: 5 rows of 152064, 601 us against 630 with
-// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 138 us
-// against 149), and down to 512 where that leaves SMs without a CTA.
+// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 110 us
+// against 143), and down to 512 where that leaves SMs without a CTA.
 int32_t adjust_slice(int64_t V, int32_t B, int64_t rows, int sms) {
   int32_t slice = rows < (int64_t)8 * B ? 4096 : 2048;
   while (slice > 512 && (V + slice - 1) / slice * B < (int64_t)2 * sms) slice /= 2;
@@ -347,7 +351,10 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
   if (n_slices * B > (int64_t)INT32_MAX) return SDCP_E_TOO_LARGE;
   const AdjustArgs a{logits, out, V, B, rows == SDCP_ROWS_TARGET ? 1 : 0, m_offsets, total_drafts, draft_tokens,
                      controls, history, history_stride, bias_tokens, bias_values, n_bias, masks, mask_stride,
-                     n_masks, mask_rows, status, slice, (int32_t)n_slices};
+                     n_masks, mask_rows, status, slice, (int32_t)n_slices,
+                     // the slices of frequent tokens (low ids) take longest: first, where the grid is a few waves
+                     // (3 waves: 99 us against 110; 51 waves, whose rows are better read one after another: 655 against 610)
+                     n_slices * B < (int64_t)8 * kAdjCtas * di.sms ? 1 : 0};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == SDCP_BF16 ? launch_adjust<__nv_bfloat16>(a, s) : launch_adjust<float>(a, s);
   return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
