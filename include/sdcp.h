@@ -534,7 +534,8 @@ size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_he
  * workspace     device scratch of sdcp_attend_workspace_bytes bytes, 256-byte aligned, no
  *               initialisation needed.
  * M_b has no upper limit here.  A query row holding NaN or infinities gives NaN in its own
- * output row alone.  Deterministic.
+ * output row alone.  Deterministic.  SDCP_S_INTERNAL for every session: the call gave up a
+ * bounded wait on the GPU, and no output of it is valid.
  */
 int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
                    int64_t total_drafts, const int32_t* kv_len, const void* q, int64_t q_stride,

@@ -31,8 +31,15 @@
 // follow the same steps of a tile (turn half of the keys' channels each, then half of the values',
 // then weigh half of the columns each), and a ninth issues S as soon as the keys are there, behind
 // which the values are turned, and O behind the next tile's keys.  Loads are one tile ahead.  Roles
-// in warps of their own (keys, values, weights; one CTA an SM, two tiles deep) were slower (201 us
-// against X on attend_long): five streams of instructions on a scheduler starve one another.
+// in warps of their own (keys, values, weights; one CTA an SM, two tiles deep) were slower (203 us
+// for the 20 columns below against 182 when the same eight warps did everything): several kinds of
+// instruction streams on a scheduler starve one another.
+//
+// Measured (128 channels, 8 cached heads): 4 contexts of about 105000 tokens, 5 rows, 32 heads: 165 us,
+// 454 MB of cache at 2.8 TB/s; 64 contexts of 500 .. 8200, 9 rows, 64 heads: 182 us, 46 % of the
+// instruction issue going to the turning, a quarter of the tensor cores' cycles used.  The time of a
+// tile hardly depends on its columns up to 32 (16 contexts of 30000: 166 us at 4 and at 16 columns,
+// 182 at 32), so what a tile costs is its turning, its waits and its votes.
 //
 // Work: the tiles of all (session, cached head, block of columns) items in one line, cut evenly
 // over the CTAs, whatever the lengths.  A CTA's first and last items may be parts; their O, m and sum
@@ -67,7 +74,9 @@ constexpr float kTop = 15.0f;     // and 2^kTop at most
 struct SessionPlan {
   int32_t w, chunks, tiles;
 };
-constexpr int32_t kItemUnits = 4;  // what an item's start and end cost, in tiles (2: 198 us, 4: 188, 8: 194, 72 columns)
+// What an item's start and end cost, in tiles (512 items of 72 columns, 4 .. 64 tiles: 189 us with 2,
+// 184 with 4, 189 with 8; with 104 long items any does).
+constexpr int32_t kItemUnits = 4;
 
 // The item that a CTA begins and another one goes on with: its parts are the CTA's second (or, where
 // it began with it, first) and the first of the CTAs after it, up to `last`.  n = 0: none.
@@ -959,7 +968,10 @@ bool attend_ready() {
 }
 
 // Columns of an item: the small shape where a session has at most 32 on average.  Sessions with more
-// are cut into several items by either shape.
+// are cut into several items by either shape.  16 contexts of 30000 tokens, 8 cached heads of 128
+// channels, small shape against large: 166 and 199 us at 4 columns, 182 and 215 at 32, but 336 and 230
+// at 36 (two small items read the cache twice) and 494 and 281 at 96.  64 channels: 157 and 178 at 32,
+// 288 and 193 at 36.
 int32_t columns_of(int32_t B, int64_t total, int32_t share) { return (total + B) * share <= (int64_t)32 * B ? 32 : 96; }
 
 template <int D, int kCols>

@@ -11,7 +11,12 @@
 // rows are first streamed with their masks alone, in 16-byte blocks, and the few tokens that a
 // penalty or a bias applies to are written again, from a list of them in rising order, after a
 // barrier: the second write meets lines that are still in L2.  With the arithmetic inside the
-// streaming loop (unrolled over a block's elements) the kernel starved for instructions.
+// streaming loop (unrolled over a block's elements) the kernel starved for instructions (3058 us for
+// the large call below).
+//
+// Measured: 1024 sessions, 5 rows of 152064 bfloat16, histories of up to 2048 tokens: 607 us, 3.1 GB
+// at 5.2 TB/s.  96 sessions, 1 .. 16 draft rows of 50257: 100 us, 170 MB; there the histories are as
+// much work as the rows, and the slices of frequent tokens take longest.
 #include <climits>
 
 #include "sdcp_device.cuh"
