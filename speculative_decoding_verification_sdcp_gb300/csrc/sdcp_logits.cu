@@ -15,8 +15,8 @@
 // the large call below).
 //
 // Measured: 1024 sessions, 5 rows of 152064 bfloat16, histories of up to 2048 tokens: 607 us, 3.1 GB
-// at 5.2 TB/s.  96 sessions, 1 .. 16 draft rows of 50257: 100 us, 170 MB; there the histories are as
-// much work as the rows, and the slices of frequent tokens take longest.
+// at 5.2 TB/s.  96 sessions, 1 .. 16 draft rows of 50257, histories of up to 16384: 77 us, 170 MB; there
+// the listed tokens are as much work as the rows, and the slices of frequent ones take longest.
 #include <climits>
 
 #include "sdcp_device.cuh"
@@ -27,6 +27,7 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kAdjUnroll = 4;             // blocks a thread has in flight
 constexpr int kAdjCtas = 5;               // CTAs of an SM
+constexpr int kAhead = 2;                 // rows of a listed token in flight (8.5 rows: 77 us with 2 or 4, 81 with 8, 99 one by one)
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kInPrompt = 1u << 31;  // of a slice's word: the token is in the prompt
 constexpr uint32_t kCountMask = ~kInPrompt;
@@ -282,19 +283,39 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
         const int32_t t = listed[x];
         const uint32_t w = words[t];
         const float bt = has_bias ? bias[t] : 0.0f;
+        uint64_t drafted = 0;  // the places where the token is a draft
+        for (int d = 0; d < nd; ++d)
+          if (s_drafts[d].at == t) drafted |= 1ull << s_drafts[d].pos;
         const T* pr = in + (int64_t)first * a.V + t;
         T* po = out + (int64_t)first * a.V + t;
-#pragma unroll 2
-        for (int32_t r = first; r < rows; r += side, pr += side * a.V, po += side * a.V) {
-          const uint32_t* const mask = s_mask[r];
-          uint32_t c = w & kCountMask;
-          for (int d = 0; d < nd; ++d) c += s_drafts[d].at == t && s_drafts[d].pos < r ? 1u : 0u;
-          const bool seen = (w & kInPrompt) != 0u || c != 0u;
-          if ((!seen && bt == 0.0f) || (mask != nullptr && mask_bits<1>(mask, v0 + t) == 0u)) continue;
-          float z = to_float(*pr);
-          if (seen) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-          if (c != 0u) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)c)), pres);
-          *po = from_float<T>(__fadd_rn(z, bt));
+        // kAhead rows at a time: their mask words together, then their logits together
+#pragma unroll 1
+        for (int32_t r0 = first; r0 < rows; r0 += kAhead * side, pr += kAhead * side * a.V, po += kAhead * side * a.V) {
+          uint32_t bits[kAhead], c[kAhead];
+          float z[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int32_t r = r0 + u * side;
+            const uint32_t* const mask = r < rows ? s_mask[r] : nullptr;
+            bits[u] = r < rows ? ~0u : 0u;
+            if (mask != nullptr) bits[u] = mask[(v0 + t) >> 5];
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int32_t r = r0 + u * side;
+            c[u] = (w & kCountMask) + (uint32_t)__popcll(r < 64 ? drafted & ((1ull << r) - 1ull) : drafted);
+            bits[u] = (bits[u] >> ((uint32_t)(v0 + t) & 31u)) & 1u;
+            if ((w & kInPrompt) == 0u && c[u] == 0u && bt == 0.0f) bits[u] = 0u;
+            if (bits[u] != 0u) z[u] = to_float(pr[(int64_t)u * side * a.V]);
+          }
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (bits[u] != 0u) {
+              float y = z[u];
+              if ((w & kInPrompt) != 0u || c[u] != 0u) y = y > 0.0f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+              if (c[u] != 0u) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)c[u])), pres);
+              po[(int64_t)u * side * a.V] = from_float<T>(__fadd_rn(y, bt));
+            }
         }
       }
     }
@@ -316,8 +337,8 @@ cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
 
 // Tokens of a slice: 4096 while a session has fewer than eight rows on average (what a CTA does
 // besides streaming is then spread over more tokens: 5 rows of 152064, 601 us against 630 with
-// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 110 us
-// against 143), and down to 512 where that leaves SMs without a CTA.
+// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 77 us
+// against 94 with 4096, 109 with 1024), and down to 512 where that leaves SMs without a CTA.
 int32_t adjust_slice(int64_t V, int32_t B, int64_t rows, int sms) {
   int32_t slice = rows < (int64_t)8 * B ? 4096 : 2048;
   while (slice > 512 && (V + slice - 1) / slice * B < (int64_t)2 * sms) slice /= 2;
@@ -358,7 +379,7 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
                      controls, history, history_stride, bias_tokens, bias_values, n_bias, masks, mask_stride,
                      n_masks, mask_rows, status, slice, (int32_t)n_slices,
                      // the slices of frequent tokens (low ids) take longest: first, where the grid is a few waves
-                     // (3 waves: 99 us against 110; 51 waves, whose rows are better read one after another: 655 against 610)
+                     // (3 waves, before the listed tokens' rows were loaded together: 99 us against 110; 51 waves, whose rows are better read one after another: 655 against 610)
                      n_slices * B < (int64_t)8 * kAdjCtas * di.sms ? 1 : 0};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == SDCP_BF16 ? launch_adjust<__nv_bfloat16>(a, s) : launch_adjust<float>(a, s);
