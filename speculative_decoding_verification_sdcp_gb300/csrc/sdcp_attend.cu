@@ -35,14 +35,14 @@
 // for the 20 columns below against 182 when the same eight warps did everything): several kinds of
 // instruction streams on a scheduler starve one another.
 //
-// Measured (128 channels, 8 cached heads): 4 contexts of about 105000 tokens, 5 rows, 32 heads: 165 us,
-// 454 MB of cache at 2.8 TB/s; 64 contexts of 500 .. 8200, 9 rows, 64 heads: 182 us, 46 % of the
-// instruction issue going to the turning, a quarter of the tensor cores' cycles used.  The time of a
+// Measured (128 channels, 8 cached heads): 4 contexts of about 105000 tokens, 5 rows, 32 heads: 166 us,
+// 454 MB of cache at 2.7 TB/s; 64 contexts of 500 .. 8200, 9 rows, 64 heads: 183 us, 60 % of the issue
+// slots and a quarter of the tensor cores' cycles used.  The time of a
 // tile hardly depends on its columns up to 32 (16 contexts of 30000: 166 us at 4 and at 16 columns,
 // 182 at 32), so what a tile costs is its turning, its waits and its votes.
 //
-// Work: the tiles of all (session, cached head, block of columns) items in one line, cut evenly
-// over the CTAs, whatever the lengths.  A CTA's first and last items may be parts; their O, m and sum
+// Work: the tiles of all (session, cached head, block of columns) items in one line, a tile as
+// long as its columns make it, cut evenly over the CTAs, whatever the lengths.  A CTA's first and last items may be parts; their O, m and sum
 // go to the workspace, and a second kernel joins them in the order of the line.
 #include <climits>
 #include <math.h>
@@ -72,11 +72,15 @@ constexpr float kTop = 15.0f;     // and 2^kTop at most
 // How a session's work is cut: kv heads x `chunks` items of at most `w` columns, `tiles` units each:
 // the most tiles any chunk needs (its own may be fewer), after kItemUnits for the item itself.
 struct SessionPlan {
-  int32_t w, chunks, tiles;
+  int32_t w, chunks, tiles, cost;  // cost: of a unit, on the line
 };
 // What an item's start and end cost, in tiles (512 items of 72 columns, 4 .. 64 tiles: 189 us with 2,
-// 184 with 4, 189 with 8; with 104 long items any does).
-constexpr int32_t kItemUnits = 4;
+// 183 with 3, 185 with 4, 189 with 8; with 32 long items any does).
+constexpr int32_t kItemUnits = 3;
+// What a tile of w columns costs on the line: kTileCost + w / 16 (16 contexts of 30000 tokens, 16 to 96
+// columns: 200 to 281 us with 128 channels, 160 to 250 with 64).  Sessions of 14 .. 119 columns over a
+// window of 1000: 93 us, 101 with one cost for all.
+constexpr int32_t kTileCost = 8;
 
 // The item that a CTA begins and another one goes on with: its parts are the CTA's second (or, where
 // it began with it, first) and the first of the CTAs after it, up to `last`.  n = 0: none.
@@ -97,7 +101,7 @@ struct AttendArgs {
   __nv_bfloat16* out;
   int32_t* status;
   uint32_t* error;   // non-zero: a bounded wait gave up
-  int64_t* units;    // [B] units of a session: kv heads x chunks x tiles; 0 for a refused one
+  int64_t* units;    // [B] length of a session on the line: kv heads x chunks x tiles x cost; 0 for a refused one
   SessionPlan* plans;  // [B]
   float* parts;      // [ctas * 2] of Part
   Cut* cuts;         // [ctas]
@@ -122,6 +126,7 @@ __device__ __forceinline__ SessionPlan session_plan(int32_t len, int32_t rows, i
   int64_t span = (int64_t)len + rows;
   if (window > 0) span = min(span, (int64_t)window - 1 + (p.w + share - 2) / share + 1 + 31);
   p.tiles = (int32_t)((span + kTile - 1) / kTile) + kItemUnits;
+  p.cost = kTileCost + p.w / 16;
   return p;
 }
 // a / b where both are rarely beyond 32 bits
@@ -129,13 +134,13 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The line of tiles over the CTAs: CTA k has [first(k), first(k + 1)).
+// The line over the CTAs: CTA k has the units that begin in [first(k), first(k + 1)).
 struct Line {
   int64_t total, each, more;
   int32_t ctas;
   __device__ __forceinline__ Line(int64_t t, int32_t most) {
     total = t;
-    ctas = (int32_t)min((int64_t)most, max(t, (int64_t)1));
+    ctas = (int32_t)min((int64_t)most, max(quotient(t, kTileCost + 1), (int64_t)1));
     each = quotient(t, ctas);
     more = t - each * ctas;
   }
@@ -358,12 +363,22 @@ struct Walk {
     len = a.s.start[b];
   }
   __device__ __forceinline__ void begin(const AttendArgs& a, const Line& line, int32_t session, int64_t base) {
-    t = t_first = line.first((int32_t)blockIdx.x);
     t_end = line.first((int32_t)blockIdx.x + 1);
     b = session;
     load(a);
-    const int64_t item = quotient(t - base, pl.tiles);
-    unit0 = (int32_t)(t - base - item * pl.tiles);
+    int64_t unit = quotient(line.first((int32_t)blockIdx.x) - base + pl.cost - 1, pl.cost);
+    if (unit * pl.cost >= a.units[b]) {  // the CTA begins with the next session, if there is one
+      base += a.units[b];
+      unit = 0;
+      if (base < t_end) {
+        do ++b;
+        while (a.units[b] == 0);
+        load(a);
+      }
+    }
+    t = t_first = base + unit * pl.cost;
+    const int64_t item = quotient(unit, pl.tiles);
+    unit0 = (int32_t)(unit - item * pl.tiles);
     kvh = (int32_t)quotient(item, pl.chunks);
     chunk = (int32_t)(item - (int64_t)kvh * pl.chunks);
   }
@@ -377,7 +392,7 @@ struct Walk {
       kvh = 0;
     }
     const int32_t share = a.q_heads / a.kv.heads;
-    const int32_t units = (int32_t)min((int64_t)(pl.tiles - unit0), t_end - t);
+    const int32_t units = (int32_t)min((int64_t)(pl.tiles - unit0), quotient(t_end - t + pl.cost - 1, pl.cost));
     const int64_t c0 = (int64_t)chunk * pl.w;
     it.b = b, it.off = off, it.len = len, it.kvh = kvh;
     it.n = (int32_t)min((int64_t)pl.w, (int64_t)rows * share - c0);
@@ -393,8 +408,8 @@ struct Walk {
     it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
     it.whole = units == pl.tiles;
     if (!it.whole && unit0 == 0)  // the CTA's last item, and others go on with it
-      a.cuts[blockIdx.x] = Cut{it.n, it.slot, line.cta_of(t + pl.tiles - 1), kvh * share + it.g0, (int64_t)off + b + it.i0, it.g0, 0};
-    t += units;
+      a.cuts[blockIdx.x] = Cut{it.n, it.slot, line.cta_of(t + (int64_t)(pl.tiles - 1) * pl.cost), kvh * share + it.g0, (int64_t)off + b + it.i0, it.g0, 0};
+    t += (int64_t)units * pl.cost;
     unit0 = 0;
     if (++chunk == pl.chunks) {
       chunk = 0;
@@ -436,7 +451,7 @@ __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const Attend
     int64_t units = 0;
     if (st == SDCP_S_OK) {
       const SessionPlan p = session_plan(a.s.start[b], a.s.offsets[b + 1] - a.s.offsets[b] + 1, a.q_heads / a.kv.heads, a.s.window, a.cols);
-      units = (int64_t)p.chunks * p.tiles * a.kv.heads;
+      units = (int64_t)p.chunks * p.tiles * a.kv.heads * p.cost;
       a.plans[b] = p;
     }
     a.units[b] = units;
@@ -451,13 +466,15 @@ __device__ __forceinline__ void plan_item(const AttendArgs& a, AttendShared<kCol
   Item it;
   bool more;
   Walk walk = sh.walk;
-  while ((more = walk.next(a, line, it)) && it.k0 >= it.k1) {
-    Part<D, kCols>* const part = reinterpret_cast<Part<D, kCols>*>(a.parts) + it.slot;
+  auto nothing_in = [&](int32_t slot) {
+    Part<D, kCols>* const part = reinterpret_cast<Part<D, kCols>*>(a.parts) + slot;
     for (int x = 0; x < kCols; ++x) {
       part->m[x] = -INFINITY;
       part->l[x] = 0.0f;
     }
-  }
+  };
+  if (j == 0 && walk.t >= walk.t_end) nothing_in((int32_t)blockIdx.x * 2);  // no unit begins here
+  while ((more = walk.next(a, line, it)) && it.k0 >= it.k1) nothing_in(it.slot);
   if (!more) it.k0 = it.k1 = 0;
   sh.walk = walk;
   sh.item[j & 1u] = it;
