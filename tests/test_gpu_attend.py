@@ -201,3 +201,11 @@ def test_pages_past_2_32_bytes():
     c.n_pages = n
     y, st = c.run(pages=big)
     assert st.tolist() == [0] and torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ms,lens", [([23, 23], [300, 5]), ([23, 0, 22, 1, 11, 0, 40], [130, 900, 0, 257, 64, 1, 700])])
+def test_items_of_unlike_widths_on_a_short_line(ms, lens, D):
+    """Fewer tiles than there are thread blocks, some dearer than a block's share: blocks without any."""
+    c = Case(ms=ms, lens=lens, P=16, Hkv=2, share=4, D=D, seed=21)
+    c.check(*c.run())
