@@ -906,7 +906,8 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
 }
 
 // ---- the joining of parts -----------------------------------------------------------------
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
+constexpr int kJoinAhead = 4;  // parts whose O a warp has in flight
 
 // One warp per CTA and column: where the CTA's last item goes on in others, the column is the sum of
 // its parts, in the line's order.
@@ -916,44 +917,59 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   const int lane = (int)(threadIdx.x & 31u);
   const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)), cta = id / cols, j = id - cta * cols;
   wait_for_previous();
-  const bool failed = *a.error != 0u;
-  if (failed)
+  const uint32_t error = *a.error;
+  const Cut cut = a.cuts[min(cta, a.ctas - 1)];
+  if (error != 0u) {
     for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
       a.status[b] = SDCP_S_INTERNAL;
-  if (cta >= a.ctas) return;
-  const Cut cut = a.cuts[cta];
-  if (!failed && j < cut.n) {
-      const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
-      auto part = [&](int32_t c) -> const Part<D, kCols>& { return parts[c == cta ? cut.first_slot : 2 * c]; };
-      float m = -INFINITY;
-      for (int32_t c = cta + lane; c <= cut.last; c += 32) m = fmaxf(m, part(c).m[j]);
-      m = warp_max(m);
-      float sum = 0.0f, o[kPer];
+    return;
+  }
+  if (cta >= a.ctas || j >= cut.n) return;
+  const Part<D, kCols>* const parts = reinterpret_cast<const Part<D, kCols>*>(a.parts);
+  const int32_t n = cut.last - cta + 1;
+  auto part = [&](int32_t x) -> const Part<D, kCols>& { return parts[x == 0 ? cut.first_slot : 2 * (cta + x)]; };
+  // references, sums and the first O are asked for together (an O that was not written has no weight)
+  float pm = -INFINITY, pl = 0.0f, v[kJoinAhead][kPer], o[kPer], sum = 0.0f;
+  auto state = [&](int32_t x) {
+    pm = x < n ? part(x).m[j] : -INFINITY;
+    pl = x < n ? part(x).l[j] : 0.0f;
+  };
+  auto load = [&](int32_t x0) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
-      for (int32_t c0 = cta; c0 <= cut.last; c0 += 32) {
-        // a lane's part: its factor, 0 where it holds nothing of the column (its O may not be written)
-        const int32_t n = min(32, cut.last - c0 + 1);
-        float f = 0.0f;
-        if (lane < n) {
-          const float pm = part(c0 + lane).m[j], pl = part(c0 + lane).l[j];
-          if (pm != -INFINITY || pl != 0.0f) f = pm == m ? 1.0f : ex2(pm - m);
-          if (f != 0.0f) sum += pl * f;
-        }
-#pragma unroll 8
-        for (int32_t x = 0; x < n; ++x) {
-          const float fx = __shfl_sync(0xFFFFFFFFu, f, x);
-          const float* const po = part(c0 + x).o[j] + lane;
+    for (int u = 0; u < kJoinAhead; ++u)
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) o[k] += (fx != 0.0f ? po[32 * k] : 0.0f) * fx;
+      for (int k = 0; k < kPer; ++k) v[u][k] = x0 + u < n ? part(x0 + u).o[j][lane + 32 * k] : 0.0f;
+  };
+  state(lane);
+  load(0);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
+  float m = pm;
+  for (int32_t x = lane + 32; x < n; x += 32) m = fmaxf(m, part(x).m[j]);
+  m = warp_max(m);
+  for (int32_t x0 = 0; x0 < n; x0 += 32) {
+    if (x0 > 0) state(x0 + lane);
+    // a lane's part: its factor, 0 where it holds nothing of the column
+    const float f = pm != -INFINITY || pl != 0.0f ? (pm == m ? 1.0f : ex2(pm - m)) : 0.0f;
+    if (f != 0.0f) sum += pl * f;
+    const int32_t here = min(32, n - x0);
+    for (int32_t x = 0; x < here; x += kJoinAhead) {
+      if (x0 + x > 0) load(x0 + x);
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const float fx = __shfl_sync(0xFFFFFFFFu, f, (x + u) & 31);
+        if (x + u < here && fx != 0.0f) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) o[k] += v[u][k] * fx;
         }
       }
-      sum = warp_reduce(sum, [](float x, float y) { return x + y; });
-      const int32_t share = a.q_heads / a.kv.heads, r = (cut.g0 + j) / share;
-      __nv_bfloat16* const out = a.out + ((cut.row + r) * a.q_heads + cut.row_head - cut.g0 + (cut.g0 + j - r * share)) * D;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) out[lane + 32 * k] = __float2bfloat16_rn(__fdividef(o[k], sum));
+    }
   }
+  sum = warp_reduce(sum, [](float x, float y) { return x + y; });
+  const int32_t share = a.q_heads / a.kv.heads, r = (cut.g0 + j) / share;
+  __nv_bfloat16* const out = a.out + ((cut.row + r) * a.q_heads + cut.row_head - cut.g0 + (cut.g0 + j - r * share)) * D;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) out[lane + 32 * k] = __float2bfloat16_rn(__fdividef(o[k], sum));
 }
 
 constexpr size_t kHeader = 256;
