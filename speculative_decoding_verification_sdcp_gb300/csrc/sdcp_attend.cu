@@ -35,8 +35,8 @@
 // for the 20 columns below against 182 when the same eight warps did everything): several kinds of
 // instruction streams on a scheduler starve one another.
 //
-// Measured (128 channels, 8 cached heads): 4 contexts of about 105000 tokens, 5 rows, 32 heads: 166 us,
-// 454 MB of cache at 2.7 TB/s; 64 contexts of 500 .. 8200, 9 rows, 64 heads: 183 us, 60 % of the issue
+// Measured (128 channels, 8 cached heads): 4 contexts of about 105000 tokens, 5 rows, 32 heads: 161 us,
+// 454 MB of cache at 2.8 TB/s; 64 contexts of 500 .. 8200, 9 rows, 64 heads: 181 us, 60 % of the issue
 // slots and a quarter of the tensor cores' cycles used.  The time of a
 // tile hardly depends on its columns up to 32 (16 contexts of 30000: 166 us at 4 and at 16 columns,
 // 182 at 32), so what a tile costs is its turning, its waits and its votes.
@@ -907,12 +907,14 @@ __global__ void __launch_bounds__(kAttendThreads, Shape<kCols>::kCtas) attend_ke
 
 // ---- the joining of parts -----------------------------------------------------------------
 constexpr int kJoinThreads = 128;
+constexpr int kJoinCtas = 9;   // of an SM: as many as need no spills
 constexpr int kJoinAhead = 4;  // parts whose O a warp has in flight
 
 // One warp per CTA and column: where the CTA's last item goes on in others, the column is the sum of
-// its parts, in the line's order.
+// its parts, in the line's order.  Bound by latency (3 to 12 us of a call: one row of 2000 tokens, 72
+// columns of 304 cuts), so a warp asks for all it needs at once: 21 to 16 us for the one row's call.
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int32_t cols) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtas) attend_join_kernel(const AttendArgs a, int32_t cols) {
   constexpr int kPer = D / 32;
   const int lane = (int)(threadIdx.x & 31u);
   const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)), cta = id / cols, j = id - cta * cols;
@@ -929,7 +931,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   const int32_t n = cut.last - cta + 1;
   auto part = [&](int32_t x) -> const Part<D, kCols>& { return parts[x == 0 ? cut.first_slot : 2 * (cta + x)]; };
   // references, sums and the first O are asked for together (an O that was not written has no weight)
-  float pm = -INFINITY, pl = 0.0f, v[kJoinAhead][kPer], o[kPer], sum = 0.0f;
+  using Chunk = typename std::conditional<D == 128, float4, float2>::type;  // a lane's channels
+  float pm = -INFINITY, pl = 0.0f, o[kPer], sum = 0.0f;
+  __align__(16) float v[kJoinAhead][kPer];
   auto state = [&](int32_t x) {
     pm = x < n ? part(x).m[j] : -INFINITY;
     pl = x < n ? part(x).l[j] : 0.0f;
@@ -938,7 +942,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 #pragma unroll
     for (int u = 0; u < kJoinAhead; ++u)
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) v[u][k] = x0 + u < n ? part(x0 + u).o[j][lane + 32 * k] : 0.0f;
+      for (int k = 0; k < kPer; ++k) v[u][k] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u)
+      if (x0 + u < n) *reinterpret_cast<Chunk*>(v[u]) = *reinterpret_cast<const Chunk*>(&part(x0 + u).o[j][lane * kPer]);
   };
   state(lane);
   load(0);
@@ -969,7 +976,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   const int32_t share = a.q_heads / a.kv.heads, r = (cut.g0 + j) / share;
   __nv_bfloat16* const out = a.out + ((cut.row + r) * a.q_heads + cut.row_head - cut.g0 + (cut.g0 + j - r * share)) * D;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) out[lane + 32 * k] = __float2bfloat16_rn(__fdividef(o[k], sum));
+  for (int k = 0; k < kPer; k += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + lane * kPer + k) = __floats2bfloat162_rn(__fdividef(o[k], sum), __fdividef(o[k + 1], sum));
 }
 
 constexpr size_t kHeader = 256;
