@@ -38,12 +38,11 @@ cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* stat
 // angles).  A warp has a row: it finds the row's session, position, page and angles once, behind its
 // first loads, and goes over the heads, eight channels a lane (16 bytes of bfloat16, one word of
 // codes), a few heads' loads in flight.  Short rounds share a row's heads among several warps.
-// Measured: 15165 rows of 28 + 4 + 4 float heads of 64 channels, 256 MB read and written: 51 us, 5.0 TB/s;
-// 2597 rows of 64 + 8 + 8 bfloat16 heads of 128 channels, 99 MB: 26 us, 3.9 TB/s; a few rows: the
+// Measured: 15165 rows of 28 + 4 + 4 float heads of 64 channels, 256 MB read and written: 48 us, 5.4 TB/s;
+// 2597 rows of 64 + 8 + 8 bfloat16 heads of 128 channels, 99 MB: 25 us, 4.0 TB/s; a few rows: the
 // host's time for two launches.  With a CTA a row, each finding its session anew, these calls and a
-// read of the rows took 114 and 81 us against 66 and 41.
+// read of the rows took 114 and 81 us against 62 and 39.
 constexpr int kAppendThreads = 128;
-constexpr int kAppendCtas = 5;  // of an SM
 constexpr int kChan = 8;
 
 struct AppendArgs {
@@ -151,8 +150,11 @@ template <int kKind> struct Turn {
   }
 };
 
+// CTAs of an SM.  The calls above (15165 and 2597 rows), each with a read of its rows: 62 and 39 us with 7, 67 and 39 with 5,
+// 62 and 41 with 8, 65 and 46 with 10 (spills).  Channels that turn one by one need the registers of 5.
+template <int kKind> constexpr int kAppendCtas = kKind == kOneByOne ? 5 : 7;
 template <typename T, int D, int kKind>
-__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas<kKind>) append_kernel(const AppendArgs a) {
   constexpr int kLanes = D / kChan;               // lanes of a head
   constexpr int kHeads = 32 / kLanes;             // heads of a warp at once
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // and times that in flight
