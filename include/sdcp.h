@@ -415,7 +415,8 @@ typedef struct sdcp_logit_controls {
  *               SDCP_S_BAD_PARAMS (controls out of range, history_len above history_stride,
  *               prompt_len above history_len, biases out of the arrays' range or not strictly
  *               rising ids of [0, V), a mask index outside -1 .. n_masks - 1, or inconsistent
- *               offsets).  The rows of such a session are filled with NaN, so that
+ *               offsets: its own pair out of range, or any of the batch's out of order, which
+ *               refuses every session).  The rows of such a session are filled with NaN, so that
  *               sdcp_verify_batch commits nothing for it (with inconsistent offsets no row is
  *               known to be the session's own, and none is written).
  * A row whose mask leaves no token holds only -inf; sdcp_verify_batch reports it as
@@ -490,8 +491,9 @@ typedef struct sdcp_rotary {     /* host struct */
  *               aligned; NULL exactly when q is.  Must not overlap q.
  * status        device out, [B] int32: SDCP_S_OK; SDCP_S_LIMIT (a position past the page table's
  *               row or the rotary table); SDCP_S_BAD_PARAMS (a negative kv_len, a page outside
- *               [0, n_pages) or inconsistent offsets).  A session that is not SDCP_S_OK writes
- *               nothing to the cache; its rows of q_out are unspecified.
+ *               [0, n_pages) or inconsistent offsets, as for sdcp_adjust_logits).  A session
+ *               that is not SDCP_S_OK writes nothing to the cache; its rows of q_out are
+ *               unspecified.
  */
 int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
                    int64_t total_drafts, const int32_t* kv_len, int dtype, const void* k,

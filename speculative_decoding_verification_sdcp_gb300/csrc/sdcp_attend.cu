@@ -439,7 +439,7 @@ template <int kCols> struct AttendShared {
 __global__ void __launch_bounds__(kCheckThreads) attend_plan_kernel(const AttendArgs a) {
   let_next_start();
   const int32_t b = (int32_t)blockIdx.x;
-  const int32_t st = kv_session_status(a.kv, a.s, b);
+  const int32_t st = kv_session_status(a.kv, a.s, b, a.status);
   if (st != SDCP_S_OK) {  // its rows become zero (what another session has of them is written later)
     const int64_t lo = min(max((int64_t)a.s.offsets[b], (int64_t)0), a.s.total), hi = min(max((int64_t)a.s.offsets[b + 1], lo), a.s.total);
     const int64_t row = (int64_t)a.q_heads * a.dim / 8;
@@ -1018,8 +1018,9 @@ int32_t columns_of(int32_t B, int64_t total, int32_t share) { return (total + B)
 template <int D, int kCols>
 cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
   a.ctas = min(sms, kMaxSms) * Shape<kCols>::kCtas;
-  attend_plan_kernel<<<(unsigned)a.s.B, kCheckThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_offsets_check(a.s.offsets, a.s.B, a.status, st);
+  if (e != cudaSuccess) return e;
+  e = launch_after_if(a.s.B > kScanSessions, attend_plan_kernel, (unsigned)a.s.B, kCheckThreads, 0, st, a);
   if (e != cudaSuccess) return e;
   e = launch_after(attend_kernel<D, kCols>, (unsigned)a.ctas, kAttendThreads, AttendSmem<D, kCols>::kBytes, st, a);
   if (e != cudaSuccess) return e;

@@ -253,6 +253,45 @@ __device__ __forceinline__ int32_t find_session(const int32_t* __restrict__ m_of
   return (int32_t)lo;
 }
 
+// Launches `kernel` so that its blocks may start while the stream's previous kernel drains; it
+// orders itself behind that kernel with wait_for_previous().  (early = false: an ordinary launch.)
+template <typename... P, typename... A>
+cudaError_t launch_after_if(bool early, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+  return launch_after_if(true, kernel, grid, block, smem, stream, args...);
+}
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Offsets out of order would give a row to two sessions, whose blocks would both write it, so the
+// serving calls refuse every session of such a batch.  Up to kScanSessions each block of theirs looks the
+// offsets over (its threads' answers are to be joined by a vote); beyond, a kernel before them does it
+// once and leaves its answer in status[].  (1024 sessions of 38 blocks: 623 us with that kernel, 637 when
+// each block compared all offsets, 609 without any; 96 sessions: 82 us with the comparison, 81 without.)
+constexpr int32_t kScanSessions = 256;
+__device__ __forceinline__ bool offsets_in_order(const int32_t* __restrict__ offsets, int32_t B) {
+  bool in_order = true;
+#pragma unroll 4
+  for (int32_t k = (int32_t)threadIdx.x; k < B; k += (int32_t)blockDim.x) in_order &= offsets[k] <= offsets[k + 1];
+  return in_order;
+}
+// For B > kScanSessions: status[b] becomes SDCP_S_OK or SDCP_S_BAD_PARAMS, alike for all (sdcp_kv.cu).
+// The next kernel, launched by launch_after() for such a B alone, reads it behind wait_for_previous().
+cudaError_t launch_offsets_check(const int32_t* offsets, int32_t B, int32_t* status, cudaStream_t stream);
+
 // ---------------------------------------------------------------------------------
 // mbarrier and bulk-copy (TMA) primitives, PTX ISA 8.x, shared::cta addresses.
 // ---------------------------------------------------------------------------------

@@ -21,15 +21,34 @@ int kv_view(const sdcp_kv_cache* c, KvView* out) {
 
 namespace {
 
+constexpr int kOffsetsThreads = 1024;
+__global__ void __launch_bounds__(kOffsetsThreads) offsets_kernel(const int32_t* offsets, int32_t B, int32_t* status) {
+  let_next_start();
+  const bool bad = __syncthreads_or(!offsets_in_order(offsets, B)) != 0;
+  const int64_t b = (int64_t)blockIdx.x * kOffsetsThreads + threadIdx.x;
+  if (b < B) status[b] = bad ? SDCP_S_BAD_PARAMS : SDCP_S_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_offsets_check(const int32_t* offsets, int32_t B, int32_t* status, cudaStream_t stream) {
+  if (B <= kScanSessions) return cudaSuccess;
+  offsets_kernel<<<(unsigned)((B - 1) / kOffsetsThreads + 1), kOffsetsThreads, 0, stream>>>(offsets, B, status);
+  return cudaGetLastError();
+}
+
+namespace {
+
 __global__ void __launch_bounds__(kCheckThreads) kv_check_kernel(const KvView kv, const KvSessions s, int32_t* status) {
   let_next_start();
-  const int32_t st = kv_session_status(kv, s, (int32_t)blockIdx.x);
+  const int32_t st = kv_session_status(kv, s, (int32_t)blockIdx.x, status);
   if (threadIdx.x == 0) status[blockIdx.x] = st;
 }
 
 cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* status, cudaStream_t stream) {
-  kv_check_kernel<<<(unsigned)s.B, kCheckThreads, 0, stream>>>(kv, s, status);
-  return cudaGetLastError();
+  const cudaError_t e = launch_offsets_check(s.offsets, s.B, status, stream);
+  if (e != cudaSuccess) return e;
+  return launch_after_if(s.B > kScanSessions, kv_check_kernel, (unsigned)s.B, kCheckThreads, 0, stream, kv, s, status);
 }
 
 // ---- append ---------------------------------------------------------------------------

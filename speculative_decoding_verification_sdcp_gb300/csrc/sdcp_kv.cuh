@@ -36,44 +36,26 @@ struct KvSessions {
   int32_t limit;           // positions below this only (the rotary table); INT32_MAX: none
 };
 
-// The status of session b, found by a whole block of kCheckThreads: offsets in order and in range,
-// a start that is not negative, the last position inside the page table's row and the limit, every
-// page that the rows touch inside the pool.  A kernel of one block a session writes status[] before
+// The status of session b, found by a whole block of kCheckThreads: the batch's offsets in order, its own
+// in range, a start that is not negative, the last position inside the page table's row and the limit,
+// every page that the rows touch inside the pool.  A kernel of one block a session writes status[] before
 // the call's main kernel, which reads it.
 constexpr int kCheckThreads = 128;
-__device__ __forceinline__ int32_t kv_session_status(const KvView& kv, const KvSessions& s, int32_t b) {
+__device__ __forceinline__ int32_t kv_session_status(const KvView& kv, const KvSessions& s, int32_t b, const int32_t* status) {
   const int32_t lo = s.offsets[b], hi = s.offsets[b + 1], start = s.start[b];
+  if (s.B > kScanSessions) wait_for_previous();  // (it writes status[] too)
+  bool bad = s.B <= kScanSessions ? !offsets_in_order(s.offsets, s.B) : status[b] != SDCP_S_OK;
   if (lo < 0 || hi < lo || (int64_t)hi > s.total || start < 0) return SDCP_S_BAD_PARAMS;
   const int64_t end = (int64_t)start + (hi - lo) + s.extra;  // one past the last position
-  if (end == start) return SDCP_S_OK;                        // no rows
+  if (end == start) return __syncthreads_or(bad) ? SDCP_S_BAD_PARAMS : SDCP_S_OK;  // no rows
   if (end > min((int64_t)kv.max_pages << kv.log_page, (int64_t)s.limit)) return SDCP_S_LIMIT;
   const int64_t first = s.window < 0 ? start : s.window == 0 ? 0 : max((int64_t)0, (int64_t)start + 1 - s.window);
-  bool bad = false;
   for (int64_t p = (first >> kv.log_page) + threadIdx.x; p <= (end - 1) >> kv.log_page; p += kCheckThreads) {
     const int32_t page = kv.page_table[(int64_t)b * kv.max_pages + p];
     bad |= page < 0 || page >= kv.n_pages;
   }
   return __syncthreads_or(bad) ? SDCP_S_BAD_PARAMS : SDCP_S_OK;
 }
-
-// Launches `kernel` so that its blocks may start while the stream's previous kernel drains; it
-// orders itself behind that kernel with wait_for_previous().
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Scale bytes 8 e + m stand for (1 + m / 8) 2^(e - 15): the three mantissa bits and the exponent
 // of a binary32 whose exponent is re-biased by 112.

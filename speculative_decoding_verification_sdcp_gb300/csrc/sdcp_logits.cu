@@ -28,6 +28,7 @@ constexpr int kAdjThreads = 256;
 constexpr int kAdjUnroll = 4;             // blocks a thread has in flight
 constexpr int kAdjCtas = 5;               // CTAs of an SM
 constexpr int kAhead = 2;                 // rows of a listed token in flight (8.5 rows: 77 us with 2 or 4, 81 with 8, 99 one by one)
+static_assert(kAdjThreads >= kScanSessions, "an offset a thread");
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kInPrompt = 1u << 31;  // of a slice's word: the token is in the prompt
 constexpr uint32_t kCountMask = ~kInPrompt;
@@ -62,6 +63,9 @@ struct SliceDraft {
   int32_t at;
   int32_t pos;
 };
+
+// A vote of the block (rare: out of the way of the rest).
+__device__ __noinline__ bool all_in_order(const int32_t* offsets, int32_t B) { return __syncthreads_and(offsets_in_order(offsets, B)) != 0; }
 
 template <typename T> __device__ __forceinline__ T from_float(float x);
 template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
@@ -115,10 +119,17 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
   // the session: offsets, controls, masks and biases, checked by every CTA of it
   const int32_t lo = a.m_offsets[b], hi = a.m_offsets[b + 1];
   const sdcp_logit_controls ctl = a.controls[b];
-  if (lo < 0 || hi < lo || (int64_t)hi > a.total) {
+  auto refuse = [&] {  // no row is known to be the session's own: none is written
     if (part == 0 && tid == 0) a.status[b] = SDCP_S_BAD_PARAMS;
-    return;
-  }
+  };
+  const bool scan = a.B <= kScanSessions;
+  if (!scan) wait_for_previous();  // (it writes status[] too)
+  if (lo < 0 || hi < lo || (int64_t)hi > a.total) return refuse();
+  const bool fine = scan ? tid >= a.B || a.m_offsets[tid] <= a.m_offsets[tid + 1] : a.status[b] == SDCP_S_OK;
+  auto out_of_order = [&] {  // a vote, and so a barrier too
+    if (__syncthreads_and(fine)) return false;
+    return scan || !all_in_order(a.m_offsets, a.B);  // (status[b] may be of the session's first CTA, for something else)
+  };
   const int32_t M = hi - lo;
   const int32_t rows = M + a.extra;
   const int64_t row0 = (int64_t)lo + (int64_t)b * a.extra;
@@ -128,7 +139,9 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
              !isfinite(ctl.presence) || (int64_t)ctl.history_len > a.history_stride || ctl.prompt_len > ctl.history_len ||
              (int64_t)ctl.bias_offset + ctl.bias_count > a.n_bias;
 
-  if (!bad) {
+  if (bad) {
+    if (out_of_order()) return refuse();
+  } else {
     uint32_t* const words = reinterpret_cast<uint32_t*>(smem);
     uint32_t* const marks = words + a.slice;
     uint16_t* const listed = reinterpret_cast<uint16_t*>(marks + a.slice / 32);
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
       }
       s_mask[tid] = r < 0 ? nullptr : a.masks + (int64_t)r * a.mask_stride;
     }
-    __syncthreads();
+    if (out_of_order()) return refuse();
 
     // the slice's counts, biases and drafts
     for (uint32_t k0 = (uint32_t)tid; k0 < ctl.history_len; k0 += kBatch * kAdjThreads) {
@@ -331,8 +344,7 @@ __global__ void __launch_bounds__(kAdjThreads, kAdjCtas) adjust_kernel(const Adj
 template <typename T>
 cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
   const size_t smem = adjust_smem(a.slice, a.n_bias > 0);
-  adjust_kernel<T><<<(unsigned)a.B * (unsigned)a.n_slices, kAdjThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after_if(a.B > kScanSessions, adjust_kernel<T>, (unsigned)a.B * (unsigned)a.n_slices, kAdjThreads, smem, stream, a);
 }
 
 // Tokens of a slice: 4096 while a session has fewer than eight rows on average (what a CTA does
@@ -382,6 +394,7 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
                      // (3 waves, before the listed tokens' rows were loaded together: 99 us against 110; 51 waves, whose rows are better read one after another: 655 against 610)
                      n_slices * B < (int64_t)8 * kAdjCtas * di.sms ? 1 : 0};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_offsets_check(m_offsets, B, status, s) != cudaSuccess) return SDCP_E_LAUNCH;
   const cudaError_t e = dtype == SDCP_BF16 ? launch_adjust<__nv_bfloat16>(a, s) : launch_adjust<float>(a, s);
   return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
 }
