@@ -513,7 +513,8 @@ int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* offsets, 
                  const int32_t* start, int dtype, void* k_out, void* v_out, int32_t* status,
                  void* stream);
 
-/* Bytes of device workspace sdcp_attend_kv needs; 0 for invalid sizes. */
+/* Bytes of device workspace sdcp_attend_kv needs; 0 for invalid sizes.  What suffices for a batch does
+ * for any with no more sessions and no more drafts (and the same heads). */
 size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_heads,
                                    int32_t kv_heads, int32_t head_dim);
 

@@ -1029,9 +1029,10 @@ cudaError_t launch_attend(AttendArgs a, int sms, cudaStream_t st) {
   return launch_after(attend_join_kernel<D, kCols>, (unsigned)((warps + per - 1) / per), kJoinThreads, 0, st, a, cols);
 }
 
-template <int D>
-size_t parts_bytes(int32_t cols) {
-  return cols == 32 ? sizeof(Part<D, 32>) * kMaxSms * Shape<32>::kCtas * 2 : sizeof(Part<D, 96>) * kMaxSms * Shape<96>::kCtas * 2;
+// For either shape: a batch with fewer sessions may take the wider one, in the workspace of a larger batch.
+template <int D> constexpr size_t parts_bytes() {
+  constexpr size_t narrow = sizeof(Part<D, 32>) * Shape<32>::kCtas, wide = sizeof(Part<D, 96>) * Shape<96>::kCtas;
+  return (narrow > wide ? narrow : wide) * kMaxSms * 2;
 }
 
 }  // namespace
@@ -1043,9 +1044,8 @@ extern "C" size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, i
                                               int32_t kv_heads, int32_t head_dim) {
   if (B < 0 || total_drafts < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
-  const int32_t cols = columns_of(B, total_drafts, q_heads / kv_heads);
   return kHeader + round256((size_t)B * sizeof(SessionPlan)) + round256((size_t)B * sizeof(int64_t)) +
-         round256(kMaxSms * 3 * sizeof(Cut)) + (head_dim == 128 ? parts_bytes<128>(cols) : parts_bytes<64>(cols));
+         round256(kMaxSms * 3 * sizeof(Cut)) + (head_dim == 128 ? parts_bytes<128>() : parts_bytes<64>());
 }
 
 extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
