@@ -310,12 +310,15 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(fn, what, device, stream, *args):
-    """One call of the library on a device: on the given stream handle, or the device's current
-    stream.  (A serving step makes several calls of a few microseconds, so the device is only
-    switched where it is not the current one.)"""
+def _call(fn, what, tensors, stream, *args):
+    """One call of the library on the device that its tensors (None: not given) are all on: on the
+    given stream handle, or the device's current stream.  (A serving step makes several calls of a few
+    microseconds, so the device is only switched where it is not the current one.)"""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index or index < 0:  # -1: in host memory
+            raise ValueError("%s: all tensors must be on one CUDA device" % what)
     here = torch.cuda.current_device()
-    index = here if device.index is None else device.index
     if stream is None:
         stream = _raw_stream(index)
     if index == here:
@@ -360,7 +363,9 @@ def sdcp_adjust_logits(logits, out, m_offsets, total_drafts, draft_tokens, contr
             raise ValueError("bias_tokens and bias_values must have the same length")
     if masks is not None:
         n_masks, words = _is(masks, torch.int32, "masks").shape
-    _call(lib.sdcp_adjust_logits, "sdcp_adjust_logits", logits.device, stream, logits.data_ptr(), out.data_ptr(), code, V, B, int(rows),
+    _call(lib.sdcp_adjust_logits, "sdcp_adjust_logits",
+          (logits, out, m_offsets, draft_tokens, controls_dev, history, status, bias_tokens, bias_values, masks, mask_rows), stream,
+          logits.data_ptr(), out.data_ptr(), code, V, B, int(rows),
           m_offsets.data_ptr(), total, _addr(draft_tokens), controls_dev.data_ptr(), _addr(history), stride, _addr(bias_tokens),
           _addr(bias_values), n_bias, _addr(masks), words, n_masks, _addr(mask_rows), status.data_ptr())
 
@@ -428,7 +433,9 @@ def sdcp_append_kv(cache, page_table, m_offsets, total_drafts, kv_len, k, v, sta
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    _call(lib.sdcp_append_kv, "sdcp_append_kv", k.device, stream, ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
+    _call(lib.sdcp_append_kv, "sdcp_append_kv",
+          (k, v, q, q_out, page_table, cache.pages, m_offsets, kv_len, status, None if rotary is None else rotary.table), stream,
+          ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
           kv_len.data_ptr(), code, k.data_ptr(), ks, v.data_ptr(), vs, None if rotary is None else ctypes.byref(rotary.desc),
           _addr(q), qs, n_q, _addr(q_out), status.data_ptr())
 
@@ -451,7 +458,8 @@ def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, stat
     if offsets.numel() < B + 1 or start.numel() < B:
         raise ValueError("offsets and start must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    _call(lib.sdcp_read_kv, "sdcp_read_kv", status.device, stream, ctypes.byref(desc), B, offsets.data_ptr(), int(n_tokens),
+    _call(lib.sdcp_read_kv, "sdcp_read_kv", (status, page_table, cache.pages, offsets, start, k_out, v_out), stream,
+          ctypes.byref(desc), B, offsets.data_ptr(), int(n_tokens),
           start.data_ptr(), code, _addr(k_out), _addr(v_out), status.data_ptr())
 
 
@@ -483,7 +491,8 @@ def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, s
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
     desc = cache.desc(page_table, B)
-    _call(lib.sdcp_attend_kv, "sdcp_attend_kv", q.device, stream, ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
+    _call(lib.sdcp_attend_kv, "sdcp_attend_kv", (q, out, page_table, cache.pages, m_offsets, kv_len, status, workspace), stream,
+          ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
           kv_len.data_ptr(), q.data_ptr(), qs, q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), int(window),
           out.data_ptr(), status.data_ptr(), workspace.data_ptr(), workspace.numel())
 
