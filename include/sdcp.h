@@ -77,8 +77,9 @@ extern "C" {
 #define SDCP_OK           0
 #define SDCP_E_INVALID    1  /* null pointer, B < 0, V < 1, unknown dtype, sizes overflow */
 #define SDCP_E_WORKSPACE  2  /* workspace null, too small or not 256-byte aligned */
-#define SDCP_E_ALIGN      3  /* a logits pointer is not aligned to its element size, or a pointer
-                                or stride of the cache calls not to 16 bytes */
+#define SDCP_E_ALIGN      3  /* a logits pointer is not aligned to its element size, a pointer or
+                                stride of the cache calls not to 16 bytes, or another array of
+                                the serving calls not to the 4 bytes of its words */
 #define SDCP_E_TOO_LARGE  4  /* V above SDCP_MAX_VOCAB or a row count above INT32_MAX */
 #define SDCP_E_LAUNCH     5  /* a CUDA launch failed (cudaGetLastError after launch) */
 #define SDCP_E_DEVICE     6  /* no usable CUDA device / device query failed */

@@ -81,7 +81,7 @@ const char* sdcp_strerror(int code) {
     case SDCP_OK: return "success";
     case SDCP_E_INVALID: return "invalid argument (null pointer, negative size, V < 1 or unknown dtype)";
     case SDCP_E_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
-    case SDCP_E_ALIGN: return "logits pointer not aligned to its element size";
+    case SDCP_E_ALIGN: return "a pointer or stride not aligned (logits: their element size; the cache calls: 16 bytes; other arrays: their words)";
     case SDCP_E_TOO_LARGE: return "vocabulary or row count above the supported maximum";
     case SDCP_E_LAUNCH: return "CUDA kernel launch failed";
     case SDCP_E_DEVICE: return "no usable CUDA device";

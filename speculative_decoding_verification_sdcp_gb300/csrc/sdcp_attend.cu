@@ -1064,6 +1064,7 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   if (!m_offsets || !kv_len || !q || !out || !status) return SDCP_E_INVALID;
   if (q_stride < (int64_t)q_heads * D) return SDCP_E_INVALID;
   if (((uintptr_t)q & 15u) != 0 || ((uintptr_t)out & 15u) != 0 || q_stride % 8 != 0) return SDCP_E_ALIGN;
+  if (!on_words(m_offsets, kv_len, status)) return SDCP_E_ALIGN;
   if (!workspace || ((uintptr_t)workspace & 255u) != 0 || workspace_bytes < need) return SDCP_E_WORKSPACE;
   DeviceInfo di;
   if (!device_info(&di) || !attend_ready()) return SDCP_E_DEVICE;

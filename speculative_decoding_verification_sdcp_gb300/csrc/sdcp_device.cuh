@@ -288,6 +288,9 @@ __device__ __forceinline__ bool offsets_in_order(const int32_t* __restrict__ off
   for (int32_t k = (int32_t)threadIdx.x; k < B; k += (int32_t)blockDim.x) in_order &= offsets[k] <= offsets[k + 1];
   return in_order;
 }
+// Host: whether arrays of 32-bit words (null: none) are on their boundary.
+template <typename... P> bool on_words(const P*... p) { return ((... | (uintptr_t)p) & 3u) == 0; }
+
 // For B > kScanSessions: status[b] becomes SDCP_S_OK or SDCP_S_BAD_PARAMS, alike for all (sdcp_kv.cu).
 // The next kernel, launched by launch_after() for such a B alone, reads it behind wait_for_previous().
 cudaError_t launch_offsets_check(const int32_t* offsets, int32_t B, int32_t* status, cudaStream_t stream);

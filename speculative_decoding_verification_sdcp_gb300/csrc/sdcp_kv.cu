@@ -11,7 +11,7 @@ int kv_view(const sdcp_kv_cache* c, KvView* out) {
   const size_t page = sdcp_kv_page_bytes(c->page_tokens, c->kv_heads, c->head_dim);
   if (page == 0 || c->n_pages < 1 || c->max_pages < 1 || !c->pages || !c->page_table) return SDCP_E_INVALID;
   if ((int64_t)c->max_pages * c->page_tokens > (int64_t)INT32_MAX) return SDCP_E_TOO_LARGE;
-  if (((uintptr_t)c->pages & 15u) != 0) return SDCP_E_ALIGN;
+  if (((uintptr_t)c->pages & 15u) != 0 || !on_words(c->page_table)) return SDCP_E_ALIGN;
   int log_page = 0;
   while ((1 << log_page) < c->page_tokens) ++log_page;
   *out = KvView{c->pages, c->page_table, c->n_pages, c->max_pages, c->kv_heads, log_page,
@@ -377,6 +377,7 @@ extern "C" int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   if ((q != nullptr) != (q_out != nullptr) || (q != nullptr && q_heads < 1)) return SDCP_E_INVALID;
   const int64_t kv_row = (int64_t)cache->kv_heads * D, q_row = (int64_t)q_heads * D;
   if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < q_row)) return SDCP_E_INVALID;
+  if (!on_words(m_offsets, kv_len, status)) return SDCP_E_ALIGN;
   const int64_t per16 = dtype == SDCP_BF16 ? 8 : 4;
   if (!aligned16(k) || !aligned16(v) || k_stride % per16 != 0 || v_stride % per16 != 0) return SDCP_E_ALIGN;
   if (q && (!aligned16(q) || !aligned16(q_out) || q_stride % per16 != 0)) return SDCP_E_ALIGN;
@@ -411,7 +412,7 @@ extern "C" int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t
   if (n_tokens > (int64_t)INT32_MAX / 2) return SDCP_E_TOO_LARGE;
   if (B == 0) return SDCP_OK;
   if (!offsets || !start || !status || (n_tokens > 0 && !k_out && !v_out)) return SDCP_E_INVALID;
-  if (!aligned16(k_out) || !aligned16(v_out)) return SDCP_E_ALIGN;
+  if (!aligned16(k_out) || !aligned16(v_out) || !on_words(offsets, start, status)) return SDCP_E_ALIGN;
   DeviceInfo di;
   if (!device_info(&di)) return SDCP_E_DEVICE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -382,6 +382,7 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
   if (mask_rows && n_masks > 0 && (!masks || mask_stride < (V + 31) / 32)) return SDCP_E_INVALID;
   const size_t esz = dtype == SDCP_BF16 ? 2 : 4;
   if (((uintptr_t)logits % esz) != 0 || ((uintptr_t)out % esz) != 0) return SDCP_E_ALIGN;
+  if (!on_words(m_offsets, draft_tokens, controls, history, bias_tokens, bias_values, masks, mask_rows, status)) return SDCP_E_ALIGN;
   DeviceInfo di;
   if (!device_info(&di)) return SDCP_E_DEVICE;
   const int32_t slice = adjust_slice(V, B, total_drafts + (rows == SDCP_ROWS_TARGET ? B : 0), di.sms);
