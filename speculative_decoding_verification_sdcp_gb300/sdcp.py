@@ -409,7 +409,7 @@ class Rotary:
 
 def _heads(t, rows, heads, dim, what):
     """Row stride of a [rows, heads, dim] view whose rows may lie apart."""
-    if t.dim() != 3 or t.shape[0] < rows or t.shape[1:] != (heads, dim) or t.stride()[1:] != (dim, 1):
+    if t.dim() != 3 or t.shape[0] < rows or t.shape[1:] != (heads, dim) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
         raise ValueError("%s must be [%d, %d, %d] with contiguous rows" % (what, rows, heads, dim))
     return t.stride(0) if t.shape[0] > 1 else heads * dim
 
