@@ -14,6 +14,10 @@ order of the calls, not the text).  Each round, for a ragged batch of proposals:
      sdcp_commit_batch truncates and updates the session's state;
   5. the host adds n_out[b] to kv_len[b] and to the history: what was rejected is overwritten by
      the next round's append.
+
+Each call has a status of its own for every session, and they refuse different things (a position past
+the rotation's table is the append's to see, the attention then reads what was in the cache before).  So
+the statuses are joined, and a session that any call refused commits nothing.
 """
 from __future__ import annotations
 
@@ -79,28 +83,32 @@ class Rounds:
         cp["max_new"], cp["m_max"], cp["low_rounds"], cp["self_load"] = max_tokens, sdcp.MAX_M, 4, sdcp.NO_SELF_LOAD
         cp["fallback_len"], cp["fallback"][:, 0] = 1, sdcp.ACTION_REDUCE
         self.cparams = torch.from_numpy(cp.view(np.uint8).copy()).to(dev)
+        self.refused = {}  # status of the sessions that the last round refused
         # all of a prompt but its last token, which is the first row of the first round, is one long round
         self.kv_len = [0] * self.B
         if all(len(p) > 1 for p in prompts):
-            self.score([p[:-1] for p in prompts])
+            status = self.score([p[:-1] for p in prompts])[3].tolist()
+            if any(status):
+                raise ValueError("prompts refused: %s" % {b: st for b, st in enumerate(status) if st})
             self.kv_len = [len(p) - 1 for p in prompts]
 
     def _int(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.device)
 
     def score(self, rows):
-        """Logits of the sessions' new rows (lists of tokens), which are appended to the cache."""
+        """Logits of the sessions' new rows (lists of tokens), which are appended to the cache; offsets,
+        number of drafts, and the sessions' status."""
         m = self.model
         off = self._int(np.concatenate([[0], np.cumsum([len(r) - 1 for r in rows])]).tolist())
         total = sum(len(r) - 1 for r in rows)
         x = m.embed[torch.tensor([t for r in rows for t in r], device=self.device)]
         q, k, v = m.qkv(x)
         turned, out = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(q, memory_format=torch.contiguous_format)
-        kv_len, status = self._int(self.kv_len), self._int([0] * self.B)
-        sdcp.sdcp_append_kv(self.cache, self.page_table, off, total, kv_len, k, v, status, rotary=self.rotary, q=q, q_out=turned)
+        kv_len, appended, attended = self._int(self.kv_len), self._int([0] * self.B), self._int([0] * self.B)
+        sdcp.sdcp_append_kv(self.cache, self.page_table, off, total, kv_len, k, v, appended, rotary=self.rotary, q=q, q_out=turned)
         scratch = sdcp.alloc_attend_workspace(self.B, total, m.q_heads, m.kv_heads, m.head_dim, self.device)
-        sdcp.sdcp_attend_kv(self.cache, self.page_table, off, total, kv_len, turned, out, status, scratch)
-        return m.logits(x, out), off, total
+        sdcp.sdcp_attend_kv(self.cache, self.page_table, off, total, kv_len, turned, out, attended, scratch)
+        return m.logits(x, out), off, total, torch.maximum(appended, attended)
 
     def controls(self):
         c = np.zeros(self.B, dtype=sdcp.CONTROLS_DTYPE)
@@ -109,25 +117,26 @@ class Rounds:
         return sdcp.controls_tensor(c, self.device)
 
     def round(self, drafts, number):
-        """One round with the sessions' drafts (lists of 1 .. 64 tokens): the tokens it emitted."""
-        logits, off, total = self.score([[h[-1]] + list(d) for h, d in zip(self.history, drafts)])
+        """One round with the sessions' drafts (lists of 1 .. 64 tokens): the tokens it emitted, none for
+        the sessions that it refused."""
+        logits, off, total, scored = self.score([[h[-1]] + list(d) for h, d in zip(self.history, drafts)])
         tokens = self._int([t for d in drafts for t in d])
         longest = max(len(h) for h in self.history)
         history = self._int([h + [-1] * (longest - len(h)) for h in self.history])
-        status = self._int([0] * self.B)
-        sdcp.sdcp_adjust_logits(logits, logits, off, total, tokens, self.controls(), history, status, masks=self.masks,
+        adjusted = self._int([0] * self.B)
+        sdcp.sdcp_adjust_logits(logits, logits, off, total, tokens, self.controls(), history, adjusted, masks=self.masks,
                                 mask_rows=self._int([0] * logits.shape[0]))
         params = np.zeros(self.B, dtype=sdcp.PARAMS_DTYPE)
         params["rule_id"], params["temperature_milli"], params["top_p_milli"] = sdcp.SDCP_RULE_GREEDY, 1000, 1000
         params["seed"], params["round"], params["session_tag"] = 1, number, np.arange(self.B)
         ver = sdcp.Verifier(self.model.vocab, self.B, total, self.device)
         accepted, n_out, out, st = ver(logits, None, off, tokens, sdcp.params_tensor(params, self.device))
-        action = self._int([0] * self.B)
-        sdcp.sdcp_commit_batch(off, accepted, n_out, out, st, self.cparams, None, self.state, 0, action)
-        if st.tolist() != [0] * self.B:
-            raise RuntimeError("a session was refused: %s" % st.tolist())
+        status, action = torch.maximum(torch.maximum(scored, adjusted), st), self._int([0] * self.B)
+        sdcp.sdcp_commit_batch(off, accepted, n_out, out, status, self.cparams, None, self.state, 0, action)
+        self.refused = {b: s for b, s in enumerate(status.tolist()) if s != sdcp.S_OK}
         emitted, first = [], off.tolist()
         for b, n in enumerate(n_out.tolist()):
+            n = 0 if b in self.refused else n
             got = out[first[b] + b:first[b] + b + n].tolist()
             self.history[b] += got
             self.kv_len[b] += n
@@ -146,7 +155,7 @@ def main():
     sessions = Rounds(model, [rng.integers(0, model.vocab, 5 + 9 * b).tolist() for b in range(a.sessions)])
     for r in range(1, a.rounds + 1):
         got = sessions.round([rng.integers(0, model.vocab, int(rng.integers(1, a.drafts + 1))).tolist() for _ in range(a.sessions)], r)
-        print("round %d emitted %s" % (r, got))
+        print("round %d emitted %s%s" % (r, got, " refused %s" % sessions.refused if sessions.refused else ""))
 
 
 if __name__ == "__main__":

@@ -495,6 +495,10 @@ typedef struct sdcp_rotary {     /* host struct */
  *               [0, n_pages) or inconsistent offsets, as for sdcp_adjust_logits).  A session
  *               that is not SDCP_S_OK writes nothing to the cache; its rows of q_out are
  *               unspecified.
+ * A refusal is this call's alone: sdcp_attend_kv knows no rotary table and would attend what the
+ * cache held before.  Keep the calls' statuses apart and give sdcp_commit_batch, for each
+ * session, one that is not SDCP_S_OK where any call's is not (the largest will do); n_out of such
+ * a session is not added to kv_len.
  */
 int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
                    int64_t total_drafts, const int32_t* kv_len, int dtype, const void* k,
@@ -534,7 +538,9 @@ size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_he
  * out           device out, [total_drafts + B][q_heads][head_dim] bfloat16, contiguous, 16-byte
  *               aligned.
  * status        device out, [B] int32, as for sdcp_append_kv (only the pages a row attends are
- *               looked at); the rows of a session that is not SDCP_S_OK are zero.
+ *               looked at; there is no rotary table's limit here); the rows of a session that
+ *               is not SDCP_S_OK are zero, which a model turns into ordinary logits: see
+ *               sdcp_append_kv on what to do with a refusal.
  * workspace     device scratch of sdcp_attend_workspace_bytes bytes, 256-byte aligned, no
  *               initialisation needed.
  * M_b has no upper limit here.  A query row holding NaN or infinities gives NaN in its own
