@@ -85,29 +85,37 @@ class Rounds:
         self.cparams = torch.from_numpy(cp.view(np.uint8).copy()).to(dev)
         self.refused = {}  # status of the sessions that the last round refused
         # all of a prompt but its last token, which is the first row of the first round, is one long round
+        # of the sessions that have more
+        if not all(prompts):
+            raise ValueError("a prompt has at least one token")
         self.kv_len = [0] * self.B
-        if all(len(p) > 1 for p in prompts):
-            status = self.score([p[:-1] for p in prompts])[3].tolist()
+        longer = [b for b, p in enumerate(prompts) if len(p) > 1]
+        if longer:
+            status = self.score([prompts[b][:-1] for b in longer], longer)[3].tolist()
             if any(status):
-                raise ValueError("prompts refused: %s" % {b: st for b, st in enumerate(status) if st})
+                raise ValueError("prompts refused: %s" % {b: st for b, st in zip(longer, status) if st})
             self.kv_len = [len(p) - 1 for p in prompts]
 
     def _int(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.device)
 
-    def score(self, rows):
-        """Logits of the sessions' new rows (lists of tokens), which are appended to the cache; offsets,
-        number of drafts, and the sessions' status."""
+    def score(self, rows, sessions=None):
+        """Logits of new rows (lists of tokens) of the sessions (default: all), which are appended to the
+        cache; offsets, number of drafts, and the sessions' status."""
         m = self.model
+        kv_len, table = self.kv_len, self.page_table
+        if sessions is not None:
+            kv_len, table = [kv_len[b] for b in sessions], table[sessions]
         off = self._int(np.concatenate([[0], np.cumsum([len(r) - 1 for r in rows])]).tolist())
         total = sum(len(r) - 1 for r in rows)
         x = m.embed[torch.tensor([t for r in rows for t in r], device=self.device)]
         q, k, v = m.qkv(x)
         turned, out = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty_like(q, memory_format=torch.contiguous_format)
-        kv_len, appended, attended = self._int(self.kv_len), self._int([0] * self.B), self._int([0] * self.B)
-        sdcp.sdcp_append_kv(self.cache, self.page_table, off, total, kv_len, k, v, appended, rotary=self.rotary, q=q, q_out=turned)
-        scratch = sdcp.alloc_attend_workspace(self.B, total, m.q_heads, m.kv_heads, m.head_dim, self.device)
-        sdcp.sdcp_attend_kv(self.cache, self.page_table, off, total, kv_len, turned, out, attended, scratch)
+        n = len(rows)
+        kv_len, appended, attended = self._int(kv_len), self._int([0] * n), self._int([0] * n)
+        sdcp.sdcp_append_kv(self.cache, table, off, total, kv_len, k, v, appended, rotary=self.rotary, q=q, q_out=turned)
+        scratch = sdcp.alloc_attend_workspace(n, total, m.q_heads, m.kv_heads, m.head_dim, self.device)
+        sdcp.sdcp_attend_kv(self.cache, table, off, total, kv_len, turned, out, attended, scratch)
         return m.logits(x, out), off, total, torch.maximum(appended, attended)
 
     def controls(self):
