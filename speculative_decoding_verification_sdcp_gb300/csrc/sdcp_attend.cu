@@ -566,7 +566,10 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
   bool dead = false;  // a wait gave up: the eight warps agree on it at a vote, all nine at an item's start
   for (uint32_t j = 0;; ++j) {
     __syncthreads();
-    if (sh.dead) return;
+    if (sh.dead) {  // copies under way end before the shared memory is given back
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      return;
+    }
     const Item& it = sh.item[j & 1u];
     const int32_t tiles = it.k1 - it.k0;
     if (tiles <= 0) return;
@@ -782,7 +785,13 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
         }
       }
       if (gone) break;
+#ifdef SDCP_TEST_WAIT_EXPIRY
+      // Test build only (the flag is never set in the library): every fourth CTA keeps the weights of its
+      // first tile to itself, so that the waits of its nine warps run out on purpose.
+      if (tid == 0 && (blockIdx.x % 4 != 0 || i != 0)) mbar_arrive(&sh.p_full);
+#else
       if (tid == 0) mbar_arrive(&sh.p_full);
+#endif
     }
 
     // O, references and sums of the item's columns
