@@ -1067,7 +1067,7 @@ extern "C" int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   if (rc != SDCP_OK) return rc;
   const size_t need = sdcp_attend_workspace_bytes(B, total_drafts, q_heads, cache->kv_heads, cache->head_dim);
   if (need == 0 || window < 0 || !isfinite(scale)) return SDCP_E_INVALID;
-  if (total_drafts + B > (int64_t)INT32_MAX / 2 || q_heads > (1 << 20)) return SDCP_E_TOO_LARGE;
+  if (total_drafts > (int64_t)INT32_MAX / 2 - B || q_heads > (1 << 20)) return SDCP_E_TOO_LARGE;
   if (B == 0) return SDCP_OK;
   const int32_t D = cache->head_dim;
   if (!m_offsets || !kv_len || !q || !out || !status) return SDCP_E_INVALID;

@@ -364,7 +364,7 @@ extern "C" int sdcp_append_kv(const sdcp_kv_cache* cache, int32_t B, const int32
   if (rc != SDCP_OK) return rc;
   if (B < 0 || total_drafts < 0 || q_heads < 0) return SDCP_E_INVALID;
   if (dtype != SDCP_F32 && dtype != SDCP_BF16) return SDCP_E_INVALID;
-  if (total_drafts + B > (int64_t)INT32_MAX / 2) return SDCP_E_TOO_LARGE;
+  if (total_drafts > (int64_t)INT32_MAX / 2 - B) return SDCP_E_TOO_LARGE;
   const int32_t D = cache->head_dim;
   if (rotary) {
     if (rotary->struct_size < sizeof(sdcp_rotary) || !rotary->table || rotary->n_positions < 1) return SDCP_E_INVALID;

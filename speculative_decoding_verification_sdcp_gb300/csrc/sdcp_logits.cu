@@ -373,7 +373,7 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
   if (dtype != SDCP_F32 && dtype != SDCP_BF16) return SDCP_E_INVALID;
   if (rows != SDCP_ROWS_TARGET && rows != SDCP_ROWS_DRAFT) return SDCP_E_INVALID;
   if (V > SDCP_MAX_VOCAB) return SDCP_E_TOO_LARGE;
-  if (total_drafts + B + total_drafts > (int64_t)INT32_MAX / 2) return SDCP_E_TOO_LARGE;
+  if (total_drafts > INT32_MAX || total_drafts + B + total_drafts > (int64_t)INT32_MAX / 2) return SDCP_E_TOO_LARGE;
   if (B == 0) return SDCP_OK;
   if (!m_offsets || !controls || !status || (total_drafts > 0 && !draft_tokens)) return SDCP_E_INVALID;
   if (rows == SDCP_ROWS_TARGET || total_drafts > 0)
