@@ -487,6 +487,8 @@ def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, s
     qs = _heads(q, rows, q.shape[1], cache.head_dim, "q")
     if not out.is_contiguous() or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
         raise ValueError("out must be contiguous and have q's shape")
+    if window > 0x7FFFFFFF:
+        raise ValueError("window must be below 2^31")
     _ints("m_offsets, kv_len and status", m_offsets, kv_len, status)
     if m_offsets.numel() < B + 1 or kv_len.numel() < B:
         raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
