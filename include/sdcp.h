@@ -529,7 +529,10 @@ size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_he
  * so each row sees the cached context, the round's earlier rows and itself (sdcp_append_kv has
  * put them there).  Query head h reads cached head h / (q_heads / kv_heads):
  *   out[row][h] = sum_t softmax_t(scale * q[row][h] . key_t) value_t.
- * Scores, the softmax's statistics and the sums are binary32; out is rounded once.
+ * Scores, the softmax's statistics and the sums are binary32.  A weight is rounded to binary16
+ * for the product with the values (11 significant bits down to 2^-21 of the row's largest weight,
+ * a spacing of 2^-31 of it below), and the sum is of the weights so rounded; exponentials and the last division are the
+ * hardware's approximate ones (2 units in the last place); out is rounded once.
  *
  * q             device, [total_drafts + B] rows of q_heads * head_dim bfloat16, q_stride elements
  *               apart (16-byte aligned, stride a multiple of 8); q_heads a multiple of kv_heads.

@@ -17,7 +17,10 @@
 // four significant bits each, so n s is exact in bfloat16 and, for scales up to 60, in binary16, and
 // one fused multiply-add gives it: with the code as the low bits of a constant 128 + 8 + n (bfloat16)
 // or 1024 + 8 + n (binary16), the subtrahends 136 s and 1032 s are exact too.  Keys are bfloat16 (as
-// the queries are), values and weights binary16: a weight keeps 11 bits.
+// the queries are), values and weights binary16: a weight keeps 11 bits (bfloat16 would keep 8, the matrix
+// instruction's 32-bit type 11 as well at half the rate), which is little beside the output's own rounding
+// to bfloat16 (relative error against 64 bits 0.0017, 0.0017 with weights of 32 bits).
+// Exponentials are the hardware's (2 units in the last place of binary32), and so is the last division.
 //
 // The reference m only has to keep the weights in range: weights are 2^7 at m, and m moves only
 // when a weight would pass 2^15 (binary16 ends below 2^16), which after an item's first tile is rare.
@@ -42,8 +45,11 @@
 // 182 at 32), so what a tile costs is its turning, its waits and its votes.
 //
 // Work: the tiles of all (session, cached head, block of columns) items in one line, a tile as
-// long as its columns make it, cut evenly over the CTAs, whatever the lengths.  A CTA's first and last items may be parts; their O, m and sum
-// go to the workspace, and a second kernel joins them in the order of the line.
+// long as its columns make it, cut evenly over the CTAs.  All blocks of columns of a session count as many
+// tiles as its longest: that is even where they see about as many tokens, but of a long round into a
+// short context (a prompt) the first blocks see few, and about half of the line is then no work.  A CTA's
+// first and last items may be parts; their O, m and sum go to the workspace, and a second kernel joins
+// them in the order of the line.
 #include <climits>
 #include <math.h>
 #include <mutex>
@@ -1017,7 +1023,8 @@ bool attend_ready() {
   return d.err == cudaSuccess;
 }
 
-// Columns of an item: the small shape where a session has at most 32 on average.  Sessions with more
+// Columns of an item: the small shape where a session has at most 32 on average (so one long round among
+// many single rows is cut into small items).  Sessions with more
 // are cut into several items by either shape.  16 contexts of 30000 tokens, 8 cached heads of 128
 // channels, small shape against large: 166 and 199 us at 4 columns, 182 and 215 at 32, but 336 and 230
 // at 36 (two small items read the cache twice) and 494 and 281 at 96.  64 channels: 157 and 178 at 32,

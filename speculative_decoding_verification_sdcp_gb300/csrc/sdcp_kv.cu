@@ -53,14 +53,16 @@ cudaError_t launch_kv_check(const KvView& kv, const KvSessions& s, int32_t* stat
 
 // ---- append ---------------------------------------------------------------------------
 
-// Bound by memory for long rounds and by its chain of loads for short ones (offsets, session, page,
-// angles).  A warp has a row: it finds the row's session, position, page and angles once, behind its
-// first loads, and goes over the heads, eight channels a lane (16 bytes of bfloat16, one word of
-// codes), a few heads' loads in flight.  Short rounds share a row's heads among several warps.
-// Measured: 15165 rows of 28 + 4 + 4 float heads of 64 channels, 256 MB read and written: 48 us, 5.4 TB/s;
-// 2597 rows of 64 + 8 + 8 bfloat16 heads of 128 channels, 99 MB: 25 us, 4.0 TB/s; a few rows: the
-// host's time for two launches.  With a CTA a row, each finding its session anew, these calls and a
-// read of the rows took 114 and 81 us against 62 and 39.
+// Bound by latency: by its chain of loads (offsets, session, page, angles) in short rounds, and in long
+// ones by the bytes it has in flight (15165 rows: DRAM at 55 % of its cycles, 38 % of the warps that an SM
+// holds, three of four stalls wait for a load).  A warp has a row: it finds the row's session, position,
+// page and angles once, behind its first loads, and goes over the heads, eight channels a lane (16 bytes
+// of bfloat16, one word of codes), a few heads' loads in flight.  Short rounds share a row's heads among
+// several warps.
+// Measured: 15165 rows of 28 + 4 + 4 float heads of 64 channels, 256 MB read and written: 49 us, 5.3 TB/s;
+// 2597 rows of 64 + 8 + 8 bfloat16 heads of 128 channels, 99 MB: 26 us, 3.8 TB/s; a few rows: the
+// host's time for two launches (10 us on the GPU with a read of the rows).  With a CTA a row, each finding
+// its session anew, these calls and a read of the rows took 114 and 81 us against 64 and 44.
 constexpr int kAppendThreads = 128;
 constexpr int kChan = 8;
 
@@ -169,8 +171,11 @@ template <int kKind> struct Turn {
   }
 };
 
-// CTAs of an SM.  The calls above (15165 and 2597 rows), each with a read of its rows: 62 and 39 us with 7, 67 and 39 with 5,
-// 62 and 41 with 8, 65 and 46 with 10 (spills).  Channels that turn one by one need the registers of 5.
+// CTAs of an SM, each call with a read of its rows, us with 5 / 6 / 7 / 8: the calls above 70 / 70 / 66 / 67
+// and 46 / 47 / 47 / 47; prompts of 16004 rows, 32 + 8 + 8 heads of 128 channels: bfloat16 in halves
+// 131 / 125 / 123 / 119, with neighbours 120 / 112 / 105 / 104, float in halves 169 / 159 / 148 / 152;
+// 28 + 4 + 4 bfloat16 heads of 64, 53 / 53 / 50 / 51.  (bfloat16 in halves spills 24 bytes with 7.)
+// Channels that turn one by one need the registers of 5.
 template <int kKind> constexpr int kAppendCtas = kKind == kOneByOne ? 5 : 7;
 template <typename T, int D, int kKind>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas<kKind>) append_kernel(const AppendArgs a) {

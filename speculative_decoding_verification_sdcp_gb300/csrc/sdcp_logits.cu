@@ -14,9 +14,10 @@
 // streaming loop (unrolled over a block's elements) the kernel starved for instructions (3058 us for
 // the large call below).
 //
-// Measured: 1024 sessions, 5 rows of 152064 bfloat16, histories of up to 2048 tokens: 607 us, 3.1 GB
-// at 5.2 TB/s.  96 sessions, 1 .. 16 draft rows of 50257, histories of up to 16384: 77 us, 170 MB; there
-// the listed tokens are as much work as the rows, and the slices of frequent ones take longest.
+// Measured: 1024 sessions, 5 rows of 152064 bfloat16, histories of up to 1024 tokens: 620 us, 3.1 GB
+// at 5.1 TB/s; in place, where a quarter of the rows is masked and the others are not streamed: 508 us.
+// 96 sessions, 1 .. 16 draft rows of 50257, histories of up to 16384: 80 us, 170 MB; there the listed
+// tokens are as much work as the rows, and the slices of frequent ones take longest.
 #include <climits>
 
 #include "sdcp_device.cuh"
@@ -27,7 +28,7 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kAdjUnroll = 4;             // blocks a thread has in flight
 constexpr int kAdjCtas = 5;               // CTAs of an SM
-constexpr int kAhead = 2;                 // rows of a listed token in flight (8.5 rows: 77 us with 2 or 4, 81 with 8, 99 one by one)
+constexpr int kAhead = 2;                 // rows of a listed token in flight (8.5 rows: 82 us with 2 or 4, 86 with 8, 88 one by one)
 static_assert(kAdjThreads >= kScanSessions, "an offset a thread");
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kInPrompt = 1u << 31;  // of a slice's word: the token is in the prompt
@@ -348,9 +349,9 @@ cudaError_t launch_adjust(const AdjustArgs& a, cudaStream_t stream) {
 }
 
 // Tokens of a slice: 4096 while a session has fewer than eight rows on average (what a CTA does
-// besides streaming is then spread over more tokens: 5 rows of 152064, 601 us against 630 with
-// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 77 us
-// against 94 with 4096, 109 with 1024), and down to 512 where that leaves SMs without a CTA.
+// besides streaming is then spread over more tokens: 5 rows of 152064, 623 us against 814 with
+// 2048), else 2048 (unevenly repeated tokens are spread over more CTAs: 8.5 rows of 50257, 82 us
+// against 110 with 4096, 112 with 1024), and down to 512 where that leaves SMs without a CTA.
 int32_t adjust_slice(int64_t V, int32_t B, int64_t rows, int sms) {
   int32_t slice = rows < (int64_t)8 * B ? 4096 : 2048;
   while (slice > 512 && (V + slice - 1) / slice * B < (int64_t)2 * sms) slice /= 2;
@@ -392,7 +393,7 @@ extern "C" int sdcp_adjust_logits(const void* logits, void* out, int dtype, int6
                      controls, history, history_stride, bias_tokens, bias_values, n_bias, masks, mask_stride,
                      n_masks, mask_rows, status, slice, (int32_t)n_slices,
                      // the slices of frequent tokens (low ids) take longest: first, where the grid is a few waves
-                     // (3 waves, before the listed tokens' rows were loaded together: 99 us against 110; 51 waves, whose rows are better read one after another: 655 against 610)
+                     // (3 waves: 82 us against 97; 51 waves, whose rows are better read one after another: 659 against 623)
                      n_slices * B < (int64_t)8 * kAdjCtas * di.sms ? 1 : 0};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (launch_offsets_check(m_offsets, B, status, s) != cudaSuccess) return SDCP_E_LAUNCH;
