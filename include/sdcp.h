@@ -518,6 +518,124 @@ int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* offsets, 
                  const int32_t* start, int dtype, void* k_out, void* v_out, int32_t* status,
                  void* stream);
 
+/* ---- the pages between rounds: fork, reserve, copy, release, compact --------------- */
+/*
+ * A pool keeps who holds which page, in three device arrays that these calls alone change: slot b (a
+ * session, or a place for one) has row b of page_table, whose first held[b] entries are pages; refs[p]
+ * is the number of rows that hold page p, 0 for a free one.  An empty pool is held = 0, refs = 0.  Rows
+ * may share pages (sdcp_fork_kv); a page is written only while one row holds it (sdcp_reserve_kv).  The
+ * arrays serve all layers of a model: each layer's cache has the same n_pages and page_tokens, its batch
+ * rows are rows of page_table, and only sdcp_copy_pages, the bytes themselves, runs once for each.
+ *
+ * The calls work on all slots at once; arrays of one entry a slot say what is to happen to it.  No call
+ * reads a number back: counts stay on the device (n_copies), and a slot whose request is refused is left
+ * as it was.  A round of a program that branches:
+ *   sdcp_fork_kv (new continuations), sdcp_reserve_kv (room for the round), for each layer
+ *   sdcp_copy_pages and the layer itself, the verdict, sdcp_release_kv (what was rejected or has ended).
+ * All are deterministic and asynchronous on `stream`; free pages are taken lowest first.  Calls on one
+ * pool must not overlap.
+ */
+typedef struct sdcp_kv_pool {    /* host struct */
+  uint32_t struct_size;          /* sizeof(sdcp_kv_pool) */
+  int32_t n_pages;               /* 1..2^30 */
+  int32_t page_tokens;           /* a power of two, 16..1024 */
+  int32_t n_slots;               /* rows of page_table, 0..2^30 */
+  int32_t max_pages;             /* entries of a row; max_pages * page_tokens below 2^31 */
+  int32_t* page_table;           /* device, [n_slots][max_pages] */
+  int32_t* held;                 /* device, [n_slots] */
+  int32_t* refs;                 /* device, [n_pages] */
+} sdcp_kv_pool;
+
+/* One page to copy, 16 bytes, device memory: the first `tokens` tokens of every head's keys and values. */
+typedef struct sdcp_page_copy {
+  int32_t from, to;
+  int32_t tokens;                /* 0..page_tokens */
+  int32_t reserved;
+} sdcp_page_copy;
+
+/*
+ * Forks sessions: slot b with parent[b] = a takes the pages of a's first length[b] tokens as its own,
+ * shared with a (no page is taken, no byte copied: a page that either will write is replaced by
+ * sdcp_reserve_kv).
+ *
+ * parent        device, [n_slots] int32: a slot, or -1: b is not forked.
+ * length        device, [n_slots] int32: tokens, looked at where parent[b] is not -1.
+ * status        device out, [n_slots] int32: SDCP_S_OK; SDCP_S_LIMIT (length beyond the parent's pages);
+ *               SDCP_S_BAD_PARAMS (parent outside the slots, b itself or forked in this call too, b holds
+ *               pages, a negative length, a row that is not in order: held[] outside 0..max_pages or an
+ *               entry outside the pool).
+ */
+int sdcp_fork_kv(const sdcp_kv_pool* pool, const int32_t* parent, const int32_t* length, int32_t* status,
+                 void* stream);
+
+/* Bytes of device workspace sdcp_reserve_kv and sdcp_compact_kv need; 0 for invalid sizes. */
+size_t sdcp_pool_workspace_bytes(int32_t n_pages, int32_t n_slots);
+
+/*
+ * Pages for what slots are to write: positions kv_len[b] .. upto[b] - 1 (upto[b] <= kv_len[b]: nothing).
+ * Of the entries that these positions lie in, those past held[b] get new pages, and those whose page
+ * other rows hold too get a new page in its stead (copy on write); where the first of them already holds
+ * tokens (kv_len[b] is inside a page), they are to be copied.  New pages are the lowest free ones (free
+ * when the call began), in the order of the slots and of their entries.  If all holders of a shared page
+ * write it in one call, each gets a page and the shared one becomes free.
+ *
+ * kv_len, upto  device, [n_slots] int32.
+ * copies        device out, [max_copies], 16-byte aligned, max_copies >= n_slots: the copies to make
+ *               before the round (sdcp_copy_pages), at most one a slot, in the order of the slots.
+ * n_copies      device out, [1] int32.
+ * status        device out, [n_slots] int32: SDCP_S_OK; SDCP_S_LIMIT (the row has no entry for upto[b], or
+ *               too few pages are free: more than there are, counted over the needs of the slots up to and
+ *               with b); SDCP_S_BAD_PARAMS (kv_len[b] is negative or beyond the pages held, held[b] is
+ *               outside 0..max_pages, or one of these entries is outside the pool).
+ * workspace     device scratch of sdcp_pool_workspace_bytes bytes, 256-byte aligned, no initialisation
+ *               needed.
+ */
+int sdcp_reserve_kv(const sdcp_kv_pool* pool, const int32_t* kv_len, const int32_t* upto,
+                    sdcp_page_copy* copies, int32_t max_copies, int32_t* n_copies, int32_t* status,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Executes a list of page copies on one cache (of one layer).  The destination's other tokens stay as they
+ * are.  cache->page_table and max_pages are not looked at.
+ *
+ * copies        device, [max_copies], 16-byte aligned; n_copies is device, [1] int32, the number of them
+ *               that are there.  No page may be the destination of two copies, or the source of one and
+ *               the destination of another (the lists of sdcp_reserve_kv and sdcp_compact_kv are so).
+ * status        device out, [1] int32: SDCP_S_OK, or SDCP_S_BAD_PARAMS: a record is not usable (a page
+ *               outside [0, n_pages), from equal to to, tokens outside 0..page_tokens) and was left out, or
+ *               n_copies is outside 0..max_copies and nothing was copied.
+ */
+int sdcp_copy_pages(const sdcp_kv_cache* cache, const sdcp_page_copy* copies, int32_t max_copies,
+                    const int32_t* n_copies, int32_t* status, void* stream);
+
+/*
+ * Gives pages back: slot b keeps the pages of its first keep[b] tokens (keep[b] < 0: all of them, 0: none;
+ * beyond what it holds: all), the entries past them become -1, and a page that no row holds any more is
+ * free.  Usual values: the committed length after a verdict, and 0 for a session that has ended.
+ *
+ * keep          device, [n_slots] int32.
+ * status        device out, [n_slots] int32: SDCP_S_OK; SDCP_S_BAD_PARAMS (a row that is not in order, as
+ *               for sdcp_fork_kv).
+ */
+int sdcp_release_kv(const sdcp_kv_pool* pool, const int32_t* keep, int32_t* status, void* stream);
+
+/*
+ * Moves live pages to the front of the pool, so that its end can be given to something else: of L live
+ * pages, the k-th highest of those at or past L goes to the k-th lowest free page.  Rows and counts are
+ * changed by this call; the bytes move with sdcp_copy_pages, of each layer, behind it.
+ *
+ * copies        device out, [max_copies], 16-byte aligned: the moves, whole pages.  With max_copies below
+ *               their number (at most n_pages / 2) the first max_copies are made, highest pages first; call
+ *               again for the others.
+ * n_copies      device out, [1] int32: the moves made.
+ * n_live        device out, [1] int32: L.
+ * workspace     as for sdcp_reserve_kv.
+ * Entries outside the pool stay as they are; rows are looked at up to held[b] (at most max_pages) entries.
+ */
+int sdcp_compact_kv(const sdcp_kv_pool* pool, sdcp_page_copy* copies, int32_t max_copies,
+                    int32_t* n_copies, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
 /* Bytes of device workspace sdcp_attend_kv needs; 0 for invalid sizes.  What suffices for a batch does
  * for any with no more sessions and no more drafts (and the same heads). */
 size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_heads,

@@ -69,6 +69,13 @@ class RotaryDesc(ctypes.Structure):
                 ("n_positions", ctypes.c_int32), ("table", ctypes.c_void_p)]
 
 
+class KvPoolDesc(ctypes.Structure):
+    """sdcp_kv_pool."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("held", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
+
+
 class SdcpError(RuntimeError):
     pass
 
@@ -111,6 +118,18 @@ def _load():
     L.sdcp_append_kv.restype = ctypes.c_int
     L.sdcp_read_kv.argtypes = [vp, i32, vp, i64, vp, ctypes.c_int, vp, vp, vp, vp]
     L.sdcp_read_kv.restype = ctypes.c_int
+    L.sdcp_fork_kv.argtypes = [vp, vp, vp, vp, vp]
+    L.sdcp_fork_kv.restype = ctypes.c_int
+    L.sdcp_pool_workspace_bytes.argtypes = [i32, i32]
+    L.sdcp_pool_workspace_bytes.restype = sz
+    L.sdcp_reserve_kv.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.sdcp_reserve_kv.restype = ctypes.c_int
+    L.sdcp_copy_pages.argtypes = [vp, vp, i32, vp, vp, vp]
+    L.sdcp_copy_pages.restype = ctypes.c_int
+    L.sdcp_release_kv.argtypes = [vp, vp, vp, vp]
+    L.sdcp_release_kv.restype = ctypes.c_int
+    L.sdcp_compact_kv.argtypes = [vp, vp, i32, vp, vp, vp, sz, vp]
+    L.sdcp_compact_kv.restype = ctypes.c_int
     L.sdcp_attend_workspace_bytes.argtypes = [i32, i64, i32, i32, i32]
     L.sdcp_attend_workspace_bytes.restype = sz
     L.sdcp_attend_kv.argtypes = [vp, i32, vp, i64, vp, vp, i64, i32, ctypes.c_float, i32, vp, vp, vp, sz, vp]
@@ -461,6 +480,95 @@ def sdcp_read_kv(cache, page_table, offsets, n_tokens, start, k_out, v_out, stat
     _call(lib.sdcp_read_kv, "sdcp_read_kv", (status, page_table, cache.pages, offsets, start, k_out, v_out), stream,
           ctypes.byref(desc), B, offsets.data_ptr(), int(n_tokens),
           start.data_ptr(), code, _addr(k_out), _addr(v_out), status.data_ptr())
+
+
+class KvPool:
+    """Who holds which page of a cache (sdcp_kv_pool): page_table int32 [n_slots, max_pages], held int32
+    [n_slots] and refs int32 [n_pages], allocated empty here or given.  One pool serves the caches of all
+    layers; a batch's page table is made of rows of page_table."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_slots=None, max_pages=None, device=None, page_table=None, held=None, refs=None):
+        if page_table is None:
+            page_table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device)
+        if held is None:
+            held = torch.zeros(page_table.shape[0], dtype=torch.int32, device=page_table.device)
+        if refs is None:
+            refs = torch.zeros(n_pages, dtype=torch.int32, device=page_table.device)
+        for t, what in ((page_table, "page_table"), (held, "held"), (refs, "refs")):
+            _is(t, torch.int32, what)
+        if page_table.dim() != 2 or held.shape != page_table.shape[:1] or refs.shape != (n_pages,):
+            raise ValueError("page_table must be [n_slots, max_pages], held [n_slots] and refs [n_pages]")
+        self.page_table, self.held, self.refs = page_table, held, refs
+        self.n_pages, self.page_tokens = n_pages, page_tokens
+        self.n_slots, self.max_pages = page_table.shape
+        self.desc = KvPoolDesc(ctypes.sizeof(KvPoolDesc), n_pages, page_tokens, self.n_slots, self.max_pages, page_table.data_ptr(),
+                               held.data_ptr(), refs.data_ptr())
+        self._at = ctypes.byref(self.desc)
+
+    def _slots(self, *named):
+        """The arrays of one entry a slot among a call's arguments."""
+        for t, what in named:
+            if _is(t, torch.int32, what).shape != (self.n_slots,):
+                raise ValueError("%s must have an entry for each of the %d slots" % (what, self.n_slots))
+
+
+def _copy_list(copies, n_copies):
+    if _is(copies, torch.int32, "copies").dim() != 2 or copies.shape[1] != 4 or _is(n_copies, torch.int32, "n_copies").numel() < 1:
+        raise ValueError("copies must be [max_copies, 4] and n_copies [1]")
+    return copies.shape[0]
+
+
+def alloc_pool_workspace(pool) -> torch.Tensor:
+    return torch.empty(int(lib.sdcp_pool_workspace_bytes(pool.n_pages, pool.n_slots)), dtype=torch.uint8, device=pool.refs.device)
+
+
+def sdcp_fork_kv(pool, parent, length, status, stream=None):
+    """Slot b with parent[b] >= 0 (-1: none) takes the pages of its parent's first length[b] tokens, shared
+    with it; parent, length and status (written): int32 [n_slots]."""
+    pool._slots((parent, "parent"), (length, "length"), (status, "status"))
+    _call(lib.sdcp_fork_kv, "sdcp_fork_kv", (status, parent, length, pool.page_table, pool.held, pool.refs), stream,
+          pool._at, parent.data_ptr(), length.data_ptr(), status.data_ptr())
+
+
+def sdcp_reserve_kv(pool, kv_len, upto, copies, n_copies, status, workspace, stream=None):
+    """Pages for positions kv_len[b] .. upto[b] - 1 of each slot, shared ones that lie there replaced.
+    copies int32 [max_copies >= n_slots, 4] and n_copies int32 [1] receive the copies to make
+    (sdcp_copy_pages); kv_len, upto and status (written): int32 [n_slots]."""
+    pool._slots((kv_len, "kv_len"), (upto, "upto"), (status, "status"))
+    most = _copy_list(copies, n_copies)
+    _call(lib.sdcp_reserve_kv, "sdcp_reserve_kv",
+          (status, kv_len, upto, copies, n_copies, workspace, pool.page_table, pool.held, pool.refs), stream,
+          pool._at, kv_len.data_ptr(), upto.data_ptr(), copies.data_ptr(), most, n_copies.data_ptr(), status.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+
+
+def sdcp_copy_pages(cache, copies, n_copies, status, stream=None):
+    """The first n_copies[0] records of copies int32 [max_copies, 4] (from, to, tokens, reserved), on one
+    cache; status int32 [1], written."""
+    most = _copy_list(copies, n_copies)
+    if _is(status, torch.int32, "status").numel() < 1:
+        raise ValueError("status must be [1]")
+    desc = KvCacheDesc(_DESC_SIZE, cache.n_pages, cache.page_tokens, cache.kv_heads, cache.head_dim, 0, None, cache.pages.data_ptr())
+    _call(lib.sdcp_copy_pages, "sdcp_copy_pages", (status, copies, n_copies, cache.pages), stream,
+          ctypes.byref(desc), copies.data_ptr(), most, n_copies.data_ptr(), status.data_ptr())
+
+
+def sdcp_release_kv(pool, keep, status, stream=None):
+    """Each slot keeps the pages of its first keep[b] tokens (negative: all) and gives the others back;
+    keep and status (written): int32 [n_slots]."""
+    pool._slots((keep, "keep"), (status, "status"))
+    _call(lib.sdcp_release_kv, "sdcp_release_kv", (status, keep, pool.page_table, pool.held, pool.refs), stream,
+          pool._at, keep.data_ptr(), status.data_ptr())
+
+
+def sdcp_compact_kv(pool, copies, n_copies, n_live, workspace, stream=None):
+    """Live pages to the front of the pool: rows and counts are changed, copies int32 [max_copies, 4] and
+    n_copies int32 [1] receive the moves for sdcp_copy_pages, n_live int32 [1] the number of live pages."""
+    most = _copy_list(copies, n_copies)
+    if _is(n_live, torch.int32, "n_live").numel() < 1:
+        raise ValueError("n_live must be [1]")
+    _call(lib.sdcp_compact_kv, "sdcp_compact_kv", (n_live, copies, n_copies, workspace, pool.page_table, pool.held, pool.refs), stream,
+          pool._at, copies.data_ptr(), most, n_copies.data_ptr(), n_live.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def sdcp_attend_workspace_bytes(B: int, total_drafts: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
