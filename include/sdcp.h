@@ -673,6 +673,36 @@ int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offse
                    int32_t q_heads, float scale, int32_t window, void* out, int32_t* status,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace sdcp_attend_shared_kv needs (n_groups 0: as 1); 0 for invalid sizes.  What
+ * suffices for a batch does for any with no more sessions, drafts and groups (and the same heads). */
+size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32_t n_groups,
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+
+/*
+ * sdcp_attend_kv without a window, for a batch in which sessions have their first pages in common (a
+ * system prompt, branches of one session: sdcp_fork_kv).  The sessions of a group are neighbours in the
+ * batch, and the call finds what they share from the page table: the leading entries on which all rows of
+ * the group agree, as far as every one of them has cached whole pages.  These pages are read and turned
+ * once for the group's rows together; the rest of each session for its own rows.  A group whose sessions
+ * share less than 128 tokens is attended session by session.  What a group is only decides how the sum is
+ * cut: the output is sdcp_attend_kv's up to rounding for any grouping.
+ *
+ * group_offsets device, [n_groups + 1] int32: group g is sessions group_offsets[g] ..
+ *               group_offsets[g+1] - 1; from 0, non-decreasing, to B.  NULL with n_groups 0: all sessions
+ *               are one group.
+ * workspace     device scratch of sdcp_attend_shared_workspace_bytes bytes, 256-byte aligned, no
+ *               initialisation needed.
+ * Everything else, the arithmetic and the statuses among it, as for sdcp_attend_kv; group offsets that are
+ * not in order refuse every session with SDCP_S_BAD_PARAMS, and a session that is refused leaves its
+ * group.  (total_drafts + B) * q_heads is below 2^31.  A row's sum of weights is of the weights before
+ * their rounding to binary16.
+ */
+int sdcp_attend_shared_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
+                          int64_t total_drafts, const int32_t* kv_len, int32_t n_groups,
+                          const int32_t* group_offsets, const void* q, int64_t q_stride,
+                          int32_t q_heads, float scale, void* out, int32_t* status, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 /*
  * Host-side split of one ragged batch into n_parts contiguous blocks of sessions for
  * n_parts GPUs (one process per GPU).  Sessions are independent (Section 6.3 "Scoring":

@@ -1,0 +1,1039 @@
+// sdcp_attend_shared.cu - sdcp_attend_shared_kv: attention of a round's rows over the paged 4-bit cache in
+// groups of sessions whose first pages are the same.
+//
+//   out[row][h] = sum_t p_t value_t / sum_t p_t,   p_t = 2^(c q.key_t - m),  c = scale log2(e)
+//
+// The tokens of a group's shared pages are attended once, by the rows of all its sessions, and what lies
+// behind them by each session's rows; the two sums are joined by their references m:
+//   m = max(m1, m2),  out = (2^(m1 - m) O1 + 2^(m2 - m) O2) / (2^(m1 - m) l1 + 2^(m2 - m) l2).
+//
+// An item is a cached head and up to 256 pairs of a row and a query head of it, over a stretch of tokens
+// in tiles of 128.  The pairs are the rows of both products on the tensor cores (tcgen05, M = 128):
+//   S[j][t] = q_j . key_t        A = queries, B = keys, both from shared memory
+//   O[j][d] += p_j[t] v_t[d]     A = weights, from tensor memory; B = values, from shared memory
+// so a thread of the softmax owns a pair: its reference and sum are the thread's own, and a tile that is
+// read and turned once serves two blocks of 128 pairs.  (The attention of sessions by themselves has few
+// pairs for its tokens; its kernel makes the tokens the rows.)
+//
+// Thirteen warps: two groups of four for the softmax of a block each, four that read codes and turn them
+// into 16-bit numbers in shared memory, and one that issues the products and plans the items.  With more
+// than 128 pairs each tile goes through both blocks; an item with fewer has its tiles go through the
+// blocks in turn, as two sums over every other tile that are joined at its end, so the products of one
+// run beside the softmax of the other either way.
+//
+// A weight is 2^7 at the reference, and the reference moves (O and the sum are rescaled, by the pair's
+// thread alone) when a tile's weights sum to more than 2^15: they are 2^7 at most at the tile's start, 128
+// of them reach 2^14, and none can pass binary16's range before the sum tells.
+#include <climits>
+#include <mutex>
+#include <type_traits>
+
+#include "sdcp_tensor.cuh"
+
+namespace sdcp {
+namespace {
+
+constexpr int kPairs = 128;           // of a block
+constexpr int kMostPairs = 2 * kPairs;  // of an item
+constexpr int kTile = 128;            // tokens
+constexpr int kThreads = 13 * 32;
+constexpr int kMaxSms = 160;          // sizes the workspace
+constexpr int kItems = 4;             // planned ahead
+constexpr float kLift = 7.0f;         // a weight is 2^kLift at its reference
+constexpr float kTopSum = 32768.0f;   // and a tile's weights sum to this at most
+constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // tensor memory: S (and the weights) of two blocks, O of two
+
+// What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.
+constexpr int32_t kOneBlock = 5, kTwoBlocks = 8, kItemUnits = 3;
+// A group shares its pages from this many tokens on.
+constexpr int32_t kLeastShared = kTile;
+
+// Rows over a stretch of tokens: of a group over its shared pages, or of a session over what is behind them.
+struct Entry {
+  int32_t row0, rows;      // output rows
+  int32_t begin;           // first token
+  int32_t last;            // last token of the first row; later rows see `step` more each
+  int32_t step;
+  int32_t table_row;
+  int32_t tiles;           // of any item
+  int32_t full, rest;      // items of 256 pairs a cached head, and the pairs of the last one (0: none)
+  int32_t joined;          // its pairs have another part
+};
+__device__ __forceinline__ int32_t cost_of(int32_t pairs) { return pairs > kPairs ? kTwoBlocks : kOneBlock; }
+struct Lengths {  // on the line
+  int64_t item, rest, head;
+  __device__ __forceinline__ explicit Lengths(const Entry& e) {
+    const int64_t u = e.tiles + kItemUnits;
+    item = u * kTwoBlocks;
+    rest = e.rest > 0 ? u * cost_of(e.rest) : 0;
+    head = e.full * item + rest;
+  }
+};
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// The line over the CTAs: CTA k has the units that begin in [first(k), first(k + 1)).
+struct Line {
+  int64_t total, each, more;
+  int32_t ctas;
+  __device__ __forceinline__ Line(int64_t t, int32_t most) {
+    total = t;
+    ctas = (int32_t)min((int64_t)most, max(quotient(t, kOneBlock), (int64_t)1));
+    each = quotient(t, ctas);
+    more = t - each * ctas;
+  }
+  __device__ __forceinline__ int64_t first(int32_t k) const { return k * each + min((int64_t)k, more); }
+  __device__ __forceinline__ int32_t cta_of(int64_t t) const {
+    const int64_t big = more * (each + 1);
+    return t < big ? (int32_t)quotient(t, each + 1) : (int32_t)(more + quotient(t - big, each));
+  }
+};
+
+struct Header {
+  uint32_t error;   // non-zero: a bounded wait gave up
+  uint32_t pad;
+  int64_t total;    // length of the line
+};
+
+struct SharedArgs {
+  KvView kv;
+  KvSessions s;
+  const int32_t* group_offsets;  // null: one group
+  int32_t groups;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int32_t q_heads;
+  float c;
+  __nv_bfloat16* out;
+  int32_t* status;
+  int32_t dim;
+  int32_t ctas;
+  Header* header;
+  int32_t* group_status;  // [groups] where there are many: whether the group offsets are in order
+  int32_t* group_of;      // [B]
+  int32_t* common;        // [B] leading pages a session has in common with its group's first
+  Entry* entries;         // [groups + B]: groups, then sessions
+  int64_t* units;         // [groups + B] length on the line
+  int64_t* base;          // [groups + B] place on the line
+  int32_t* first_slot;    // [ctas] where a CTA's last item goes on in others: its part
+  float* parts;           // [ctas * 2] of Part
+  float* acc;             // [2][rows * q_heads] of O, where a pair has two parts
+  float2* acc_ml;         // [2][rows * q_heads] references and sums
+};
+
+template <int D> struct Part {
+  float o[kMostPairs][D];
+  float m[kMostPairs];
+  float l[kMostPairs];
+};
+
+// ---- plan ---------------------------------------------------------------------------------
+// A block a session: its status, its group, and the pages that it has in common with the group's first.
+__global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const SharedArgs a) {
+  __shared__ int32_t common;
+  let_next_start();
+  const int32_t b = (int32_t)blockIdx.x;
+  const bool kernel_before = a.s.B > kScanSessions || a.groups > kScanSessions;
+  if (kernel_before) wait_for_previous();
+  int32_t st = kv_session_status(a.kv, a.s, b, a.status);
+  int32_t g = 0, first = 0;
+  if (a.group_offsets != nullptr) {
+    bool bad = a.group_offsets[0] != 0 || a.group_offsets[a.groups] != a.s.B;
+    bad |= a.groups <= kScanSessions ? !offsets_in_order(a.group_offsets, a.groups) : a.group_status[0] != SDCP_S_OK;
+    if (__syncthreads_or(bad)) {
+      st = SDCP_S_BAD_PARAMS;
+    } else {
+      g = find_session(a.group_offsets, a.groups, b, false);
+      first = a.group_offsets[g];
+    }
+  }
+  if (st != SDCP_S_OK) {  // its rows become zero (what another session has of them is written later)
+    const int64_t lo = min(max((int64_t)a.s.offsets[b], (int64_t)0), a.s.total), hi = min(max((int64_t)a.s.offsets[b + 1], lo), a.s.total);
+    const int64_t row = (int64_t)a.q_heads * a.dim / 8;
+    uint4* const out = reinterpret_cast<uint4*>(a.out);
+    for (int64_t x = (lo + b) * row + threadIdx.x; x < (hi + b + 1) * row; x += kCheckThreads) out[x] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    // (pages that all rows of the round see whole)
+    const int32_t n = a.s.start[b] >> a.kv.log_page;
+    if (threadIdx.x == 0) common = n;
+    __syncthreads();
+    const int32_t* const mine = a.kv.page_table + (int64_t)b * a.kv.max_pages;
+    const int32_t* const other = a.kv.page_table + (int64_t)first * a.kv.max_pages;
+    if (first != b)
+      for (int32_t p = (int32_t)threadIdx.x; p < n; p += kCheckThreads)
+        if (mine[p] != other[p]) {
+          atomicMin(&common, p);
+          break;
+        }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    a.status[b] = st;
+    a.group_of[b] = g;
+    a.common[b] = st == SDCP_S_OK ? common : 0;
+    if (st != SDCP_S_OK) a.units[a.groups + b] = 0;
+    if (b == 0) {
+      a.header->error = 0u;
+      a.header->total = 0;
+    }
+  }
+}
+
+__device__ __forceinline__ void plan_entry(const SharedArgs& a, int32_t id, Entry e) {
+  const int64_t pairs = (int64_t)e.rows * (a.q_heads / a.kv.heads);
+  const int64_t tokens = (int64_t)e.last + (int64_t)e.step * (e.rows - 1) + 1 - e.begin;
+  e.tiles = (int32_t)((tokens + kTile - 1) / kTile);
+  e.full = (int32_t)(pairs / kMostPairs);
+  e.rest = (int32_t)(pairs % kMostPairs);
+  a.entries[id] = e;
+  a.units[id] = Lengths(e).head * a.kv.heads;
+}
+
+// A block a group: the pages that its sessions share, its entry and theirs.
+__global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const SharedArgs a) {
+  __shared__ int32_t pages, low, high;  // of the members that are not refused
+  let_next_start();
+  wait_for_previous();
+  const int32_t g = (int32_t)blockIdx.x;
+  const int32_t b0 = a.group_offsets ? min(max(a.group_offsets[g], 0), a.s.B) : 0, b1 = a.group_offsets ? min(max(a.group_offsets[g + 1], 0), a.s.B) : a.s.B;
+  if (threadIdx.x == 0) {
+    pages = INT_MAX;
+    low = INT_MAX;
+    high = -1;
+  }
+  __syncthreads();
+  int32_t least = INT_MAX, lowest = INT_MAX, highest = -1;
+  for (int32_t b = b0 + (int32_t)threadIdx.x; b < b1; b += kCheckThreads)
+    if (a.status[b] == SDCP_S_OK) {
+      least = min(least, a.common[b]);
+      lowest = min(lowest, b);
+      highest = b;
+    }
+  if (highest >= 0) {
+    atomicMin(&pages, least);
+    atomicMin(&low, lowest);
+    atomicMax(&high, highest);
+  }
+  __syncthreads();
+  const int64_t all = high > low ? (int64_t)pages << a.kv.log_page : 0;
+  const int32_t shared = all >= kLeastShared ? (int32_t)all : 0;
+  if (threadIdx.x == 0) {
+    if (shared > 0) {
+      const int32_t row0 = a.s.offsets[low] + low;  // (a refused one's offsets may be outside the batch)
+      plan_entry(a, g, Entry{row0, a.s.offsets[high + 1] + high + 1 - row0, 0, shared - 1, 0, b0, 0, 0, 0, 1});
+    } else {
+      a.units[g] = 0;
+    }
+  }
+  for (int32_t b = b0 + (int32_t)threadIdx.x; b < b1; b += kCheckThreads)
+    if (a.status[b] == SDCP_S_OK) {
+      const int32_t off = a.s.offsets[b];
+      plan_entry(a, a.groups + b, Entry{off + b, a.s.offsets[b + 1] - off + 1, shared, a.s.start[b], 1, b, 0, 0, 0, shared > 0});
+    }
+}
+
+// ---- items --------------------------------------------------------------------------------
+struct Item {
+  int32_t n;                    // pairs; 0: no more items
+  int32_t i0, g0;               // row (of the entry) and head of the first
+  int32_t row0;                 // output row of the entry
+  int32_t kvh, table_row;
+  int32_t begin, end;           // first token of tile 0, one past the last token read
+  int32_t last, step;           // of the entry
+  int32_t k0, k1;               // tiles
+  int32_t slot;                 // of the parts
+  int32_t whole;                // all of the item's tiles are here
+  int32_t joined;               // 0: alone; 1: a group's part; 2: a session's
+};
+// A CTA's way along the line, walked by the thread that issues the products, items ahead of it.
+struct Walk {
+  int64_t t, t_end, t_first;
+  Entry en;
+  int32_t e, kvh, chunk, unit0;
+  __device__ __forceinline__ int32_t chunks() const { return en.full + (en.rest > 0); }
+  __device__ __forceinline__ int32_t pairs() const { return chunk < en.full ? kMostPairs : en.rest; }
+  __device__ __forceinline__ void begin(const SharedArgs& a, const Line& line, int32_t entry, int64_t base) {
+    const int64_t from = line.first((int32_t)blockIdx.x);
+    t_end = line.first((int32_t)blockIdx.x + 1);
+    e = entry;
+    en = a.entries[e];
+    const Lengths len(en);
+    int64_t r = from - base;
+    kvh = (int32_t)quotient(r, len.head);
+    r -= kvh * len.head;
+    chunk = (int32_t)min(quotient(r, len.item), (int64_t)en.full);
+    r -= chunk * len.item;
+    const int32_t cost = cost_of(pairs());
+    unit0 = (int32_t)quotient(r + cost - 1, cost);
+    t = t_first = base + kvh * len.head + chunk * len.item + (int64_t)unit0 * cost;
+    if (unit0 == en.tiles + kItemUnits) advance();
+  }
+  __device__ __forceinline__ void advance() {
+    unit0 = 0;
+    if (++chunk == chunks()) {
+      chunk = 0;
+      ++kvh;
+    }
+  }
+  // the next item; false at the end of the CTA's part
+  __device__ __forceinline__ bool next(const SharedArgs& a, const Line& line, Item& it) {
+    if (t >= t_end) return false;
+    if (kvh == a.kv.heads) {  // the next entry that has work
+      do ++e;
+      while (a.units[e] == 0);
+      en = a.entries[e];
+      kvh = 0;
+    }
+    const int32_t share = a.q_heads / a.kv.heads, all = en.tiles + kItemUnits, cost = cost_of(pairs());
+    const int32_t units = (int32_t)min((int64_t)(all - unit0), quotient(t_end - t + cost - 1, cost));
+    const int32_t c0 = chunk * kMostPairs;
+    it.n = pairs();
+    it.i0 = c0 / share;
+    it.g0 = c0 - it.i0 * share;
+    it.row0 = en.row0;
+    it.kvh = kvh;
+    it.table_row = en.table_row;
+    it.begin = en.begin;
+    it.last = en.last;
+    it.step = en.step;
+    it.end = en.last + en.step * (it.i0 + (it.g0 + it.n - 1) / share) + 1;
+    const int32_t real = (it.end - it.begin + kTile - 1) / kTile;
+    it.k0 = max(unit0 - kItemUnits, 0);
+    it.k1 = min(max(unit0 + units - kItemUnits, 0), real);
+    it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
+    it.whole = units == all;
+    it.joined = en.joined ? (e < a.groups ? 1 : 2) : 0;
+    if (!it.whole && unit0 == 0) a.first_slot[blockIdx.x] = it.slot;  // the CTA's last item, and others go on with it
+    t += (int64_t)units * cost;
+    advance();
+    return true;
+  }
+};
+
+template <int D> struct SharedSmem {
+  static constexpr int kAtoms = D / 64;                   // 128-byte atoms along the channels
+  static constexpr int kBlock = kAtoms * kTile * 128;     // [atom][pair or token][128 bytes]
+  static constexpr int kCodes = kTile * (D / 2 + 4);      // of the next keys, or values: [group][token][16 bytes], [token][4 bytes] of scales
+  static constexpr size_t kBytes = (size_t)6 * kBlock + 2 * kCodes + 1024;  // two of queries, keys and values; and the alignment to 1024
+};
+struct SharedState {
+  Item item[kItems];
+  float2 ml[2][2][kPairs];  // references and sums of the blocks, at an item's end; the next such item's beside them
+  uint64_t item_full[kItems], item_free[kItems];
+  uint64_t q_free[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], pv_done[2], o_free, ml_full, drained;
+  long long scan[kThreads / 32];
+  long long base;
+  int32_t entry;
+  uint32_t tmem;
+  int dead;
+};
+
+template <int D> __device__ __forceinline__ void nothing_in(const SharedArgs& a, int32_t slot) {
+  Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + slot;
+  for (int x = 0; x < kMostPairs; ++x) {
+    part->m[x] = -INFINITY;
+    part->l[x] = 0.0f;
+  }
+}
+// The next item that has tiles, into the ring; a part that holds no tile of its item is marked at once.
+template <int D> __device__ __forceinline__ void plan_item(const SharedArgs& a, SharedState& sh, const Line& line, Walk& walk, bool& more, uint32_t j) {
+  Item it;
+  it.n = 0;
+  if (j == 0 && walk.t >= walk.t_end) nothing_in<D>(a, (int32_t)blockIdx.x * 2);  // no unit begins here
+  while (more && (more = walk.next(a, line, it)) && it.k0 >= it.k1) nothing_in<D>(a, it.slot);
+  if (!more) it.n = it.k0 = it.k1 = 0;
+  sh.item[j % kItems] = it;
+  mbar_arrive(&sh.item_full[j % kItems]);
+}
+
+// ---- the products: one thread ---------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, const Line& line, Walk& walk, const unsigned char* s_q, const unsigned char* s_k,
+                                         const unsigned char* s_v, uint32_t tmem) {
+  using Sm = SharedSmem<D>;
+  const uint64_t q_mat = smem_matrix(s_q, 0, 1024, kSwizzle128), k_mat = smem_matrix(s_k, 0, 1024, kSwizzle128),
+                 v_mat = smem_matrix(s_v, D == 128 ? kTile * 128 : 0, 1024, kSwizzle128);
+  constexpr uint32_t kIdescS = kIdescF32 | kIdescBf16 | kIdescM128 | (uint32_t)(kTile / 8) << 17;
+  constexpr uint32_t kIdescO = kIdescF32 | kIdescM128 | (uint32_t)(D / 8) << 17 | 1u << 16;  // values: tokens along the rows
+  bool more = true;
+  plan_item<D>(a, sh, line, walk, more, 0);
+  plan_item<D>(a, sh, line, walk, more, 1);
+  uint32_t tiles = 0, q_used = 0, used[2] = {0, 0};  // tiles, blocks of queries and steps of a block so far
+  bool ok = true;
+  for (uint32_t j = 0; ok; ++j) {
+    const Item& it = sh.item[j % kItems];
+    const bool two = it.n > kPairs;
+    const int32_t n_tiles = it.k1 - it.k0, steps = two ? 2 * n_tiles : n_tiles;
+    if (n_tiles <= 0) break;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !wait_phase(bar, parity, &sh.dead)) ok = false;
+      return ok;
+    };
+    auto score = [&](int32_t h) {  // S of step h
+      const int x = h & 1;
+      const uint32_t tile = tiles + (uint32_t)(two ? h >> 1 : h), buf = tile & 1u;
+      if (!two || x == 0) wait(&sh.k_full[buf], (tile >> 1) & 1u);
+      if (used[x] > 0) wait(&sh.pv_done[x], (used[x] - 1u) & 1u);  // the weights of the step before, in the same place
+      if (!ok) return;
+      fence_after();
+      const uint32_t qb = (q_used + (two ? (uint32_t)x : 0u)) & 1u;
+      const uint64_t qm = q_mat + (uint64_t)(qb * Sm::kBlock >> 4), km = k_mat + (uint64_t)(buf * Sm::kBlock >> 4);
+#pragma unroll
+      for (int y = 0; y < D / 16; ++y) {
+        const uint64_t at = (uint64_t)(((y / 4) * (kTile * 128) + (y % 4) * 32) >> 4);
+        mma_smem_a(tmem + kTmemS + (uint32_t)x * 128u, qm + at, km + at, kIdescS, y > 0);
+      }
+      mma_commit(&sh.s_full[x]);
+      if (!two || x == 1) mma_commit(&sh.k_free[buf]);
+      if (h == steps - 1) {
+        mma_commit(&sh.q_free[q_used & 1u]);
+        if (two) mma_commit(&sh.q_free[(q_used + 1u) & 1u]);
+      }
+      ++used[x];
+    };
+    score(0);
+    for (int32_t h = 0; h < steps && ok; ++h) {
+      if (h + 1 < steps) score(h + 1);
+      if (h == 0 && ok) {
+        if (j >= 2) wait(&sh.item_free[(j + 2) % kItems], ((j - 2) / kItems) & 1u);
+        if (ok) plan_item<D>(a, sh, line, walk, more, j + 2);
+      }
+      const int x = h & 1;
+      const uint32_t tile = tiles + (uint32_t)(two ? h >> 1 : h), buf = tile & 1u;
+      // (of its own step: the one after may have been asked for, but needs this product first)
+      if (!two || x == 0) wait(&sh.v_full[buf], (tile >> 1) & 1u);
+      wait(&sh.p_full[x], (used[x] - 1u) & 1u);
+      if (h == 0 && j > 0) wait(&sh.o_free, (j - 1u) & 1u);
+      if (!ok) break;
+      fence_after();
+#pragma unroll
+      for (int y = 0; y < kTile / 16; ++y)
+        mma_tmem_a(tmem + kTmemO + (uint32_t)(x * D), tmem + kTmemS + (uint32_t)(x * 128 + y * 8), v_mat + (uint64_t)((buf * Sm::kBlock + y * 2048) >> 4),
+                   kIdescO, h > 1 || y > 0);
+      if (!two || x == 1) mma_commit(&sh.v_free[buf]);
+      mma_commit(&sh.pv_done[x]);  // the last of a step: when it is seen, none is under way
+    }
+    tiles += (uint32_t)n_tiles;
+    q_used += two ? 2u : 1u;
+  }
+  if (!ok) {  // products under way end before the tensor memory is given back
+    sh.dead = 1;
+    mma_commit(&sh.drained);
+    (void)wait_phase(&sh.drained, 0u, nullptr);
+  }
+}
+
+// ---- the turning: four warps, a token of the tile a thread -----------------------------------
+template <int D>
+__device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsigned char* s_q, unsigned char* s_k, unsigned char* s_v, unsigned char* s_c) {
+  using Sm = SharedSmem<D>;
+  constexpr int kGroups = D / kKvGroup;
+  const int tok = (int)threadIdx.x & 127, lane = tok & 31;
+  const uint32_t one_k = kept(0x43004300u), one_v = kept(0x64006400u);
+  const uint32_t to = (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);  // a token's line in an atom, swizzled
+  const uint32_t c_at = smem_u32(s_c) + (uint32_t)tok * 16u, sb_at = smem_u32(s_c) + kTile * (D / 2) + (uint32_t)tok * 4u;
+  const int sb_shift = D == 128 ? 0 : (tok & 1) * 16;  // of the thread's own scales (tiles start at even tokens)
+  // a token that is not read keeps old codes: finite numbers, whose weight is zero
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at + Sm::kCodes), "r"(0u) : "memory");
+  const int32_t share = a.q_heads / a.kv.heads;
+  uint32_t tiles = 0, q_used = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // a warp agrees on it
+    if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &sh.dead));
+  };
+  for (uint32_t j = 0;; ++j) {
+    wait(&sh.item_full[j % kItems], (j / kItems) & 1u);
+    if (!ok) break;
+    const Item it = sh.item[j % kItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_free[j % kItems]);
+    const int32_t n_tiles = it.k1 - it.k0;
+    if (n_tiles <= 0) break;
+    // queries of the pairs, zero past them (the oldest group of copies: they are there with the first keys)
+    for (int x = 0; x < (it.n > kPairs ? 2 : 1); ++x, ++q_used) {
+      if (q_used >= 2) wait(&sh.q_free[q_used & 1u], ((q_used >> 1) - 1u) & 1u);
+      if (!ok) break;
+      const __nv_bfloat16* const q0 = a.q + ((int64_t)it.row0 + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
+      const int ch = tok % (D / 8);
+      const uint32_t dst = smem_u32(s_q) + (q_used & 1u) * Sm::kBlock + (uint32_t)(ch / 8) * (kTile * 128);
+#pragma unroll 4
+      for (int col = tok / (D / 8); col < kPairs; col += 128 / (D / 8)) {
+        const int32_t at = x * kPairs + col, c = min(at, it.n - 1) + it.g0, r = c / share;
+        copy_async16_or_zero(dst + (uint32_t)col * 128u + (uint32_t)(((ch & 7) ^ (col & 7)) << 4), q0 + r * a.q_stride + (c - r * share) * D + ch * 8,
+                             at < it.n);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    // a tile ahead: the page of the next token, and the copy of its codes to the thread's own places
+    uint32_t pos = (uint32_t)it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok;
+    const uint32_t end = (uint32_t)it.end, in_page = (uint32_t)it.kvh * 2u * (uint32_t)a.kv.block;
+    const int32_t* const table = a.kv.page_table + (int64_t)it.table_row * a.kv.max_pages;
+    auto page_of = [&](uint32_t p, bool some) { return some && p < end ? table[p >> a.kv.log_page] : -1; };
+    auto fetch = [&](int which, uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read)
+      if (page >= 0) {
+        const uint32_t slot = p & ((1u << a.kv.log_page) - 1u);
+        const uint8_t* const blk = a.kv.pages + (uint64_t)(uint32_t)page * (uint32_t)a.kv.page + (in_page + (which ? (uint32_t)a.kv.block : 0u));
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          copy_async16(c_at + (uint32_t)(which * Sm::kCodes + g * kTile * 16), blk + ((((uint32_t)g << a.kv.log_page) + slot) * 16u));
+        // four scale bytes of a token, or two each of a pair of tokens
+        copy_async4(sb_at + (uint32_t)which * Sm::kCodes, blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int32_t page = page_of(pos, true);
+    fetch(0, pos, page);
+    fetch(1, pos, page);
+    page = page_of(pos + kTile, n_tiles > 1);
+    for (int32_t k = 0; k < n_tiles && ok; ++k, ++tiles, pos += kTile) {
+      const uint32_t buf = tiles & 1u, parity = ((tiles >> 1) - 1u) & 1u;
+      // keys, once the products that read the ones before are done
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      uint32_t sb = ld_shared4(sb_at) >> sb_shift;
+      if (tiles >= 2) wait(&sh.k_free[buf], parity);
+      if (!ok) break;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint4 c = ld_shared16(c_at + (uint32_t)(g * kTile * 16));
+        const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
+        const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
+        uint32_t r[16];
+        word_bf16(c.x, one_k, s, m, r);
+        word_bf16(c.y, one_k, s, m, r + 4);
+        word_bf16(c.z, one_k, s, m, r + 8);
+        word_bf16(c.w, one_k, s, m, r + 12);
+        const uint32_t line = smem_u32(s_k) + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128) + to;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) st_shared16(line ^ (uint32_t)(((g & 1) * 4 + y) << 4), r[4 * y], r[4 * y + 1], r[4 * y + 2], r[4 * y + 3]);
+      }
+      fence_async_smem();  // (the item's queries too)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[buf]);
+      fetch(0, pos + kTile, page);
+      // values
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      sb = ld_shared4(sb_at + Sm::kCodes) >> sb_shift;
+      if (tiles >= 2) wait(&sh.v_free[buf], parity);
+      if (!ok) break;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const uint4 c = ld_shared16(c_at + (uint32_t)(Sm::kCodes + g * kTile * 16));
+        const uint32_t s = twice(sb, g) << 7;
+        const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
+        const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
+        uint32_t r[16];
+        word_f16(c.x, one_v, s, m, s16, m16, r);
+        word_f16(c.y, one_v, s, m, s16, m16, r + 4);
+        word_f16(c.z, one_v, s, m, s16, m16, r + 8);
+        word_f16(c.w, one_v, s, m, s16, m16, r + 12);
+        const uint32_t line = smem_u32(s_v) + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128) + to;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) st_shared16(line ^ (uint32_t)(((g & 1) * 4 + y) << 4), r[4 * y], r[4 * y + 1], r[4 * y + 2], r[4 * y + 3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.v_full[buf]);
+      fetch(1, pos + kTile, page);
+      page = page_of(pos + 2 * kTile, k + 2 < n_tiles);
+    }
+    if (!ok) break;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // before the shared memory is given back
+  if (!ok) sh.dead = 1;
+}
+
+// ---- the softmax: four warps a block of pairs, a pair a thread --------------------------------
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
+        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]),
+        "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(at)
+      : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int x, uint32_t tmem) {
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = (int)threadIdx.x & 31, pair = (int)threadIdx.x & 127;
+  const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes of tensor memory, in bits 16 up
+  const uint32_t s_at = lanes + kTmemS + (uint32_t)x * 128u, o_at = lanes + kTmemO + (uint32_t)(x * D);
+  const int32_t share = a.q_heads / a.kv.heads;
+  uint32_t used[2] = {0, 0}, halves = 0;  // steps of the blocks, and items of halves, so far
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // a warp agrees on it
+    if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &sh.dead));
+    return ok;
+  };
+  for (uint32_t j = 0;; ++j) {
+    if (!wait(&sh.item_full[j % kItems], (j / kItems) & 1u)) break;
+    const Item it = sh.item[j % kItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_free[j % kItems]);
+    const int32_t n_tiles = it.k1 - it.k0;
+    if (n_tiles <= 0) break;
+    const bool two = it.n > kPairs;
+    const int32_t at = two ? x * kPairs + pair : pair;                   // of the item's pairs
+    const int32_t row = it.i0 + (it.g0 + min(at, it.n - 1)) / share;     // of the entry's rows
+    const bool live = at < it.n, some = __any_sync(0xFFFFFFFFu, live);
+    int32_t limit = it.last + it.step * row - it.begin - it.k0 * kTile;  // last token that it sees, from the tile's start
+    float nm = INFINITY, l = 0.0f;  // kLift - m: what a scaled score is shifted by (infinity: no score yet), and the sum
+    bool first = true;
+    for (int32_t k = two ? 0 : x; k < n_tiles; k += two ? 1 : 2, ++used[x]) {
+      if (!wait(&sh.s_full[x], used[x] & 1u)) break;
+      fence_after();
+      if (some) {
+        const int32_t lim = limit - k * kTile;
+        const bool masked = __any_sync(0xFFFFFFFFu, lim < kTile - 1);
+        uint32_t p[kTile / 2];
+        float sum;
+        auto weigh = [&](auto with_mask) {
+          sum = 0.0f;
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_ld32(s_at + (uint32_t)c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              float u = fmaf(s[y], a.c, nm), v = fmaf(s[y + 1], a.c, nm);
+              if (with_mask) {
+                if (c + y > lim) u = -INFINITY;
+                if (c + y + 1 > lim) v = -INFINITY;
+              }
+              u = ex2(u);
+              v = ex2(v);
+              sum += u + v;
+              p[(c + y) / 2] = pack_f16x2(u, v);
+            }
+          }
+        };
+        auto weights = [&] {
+          if (masked) weigh(std::true_type{});
+          else weigh(std::false_type{});
+        };
+        if (!first) weights();
+        if (first || __any_sync(0xFFFFFFFFu, sum > kTopSum)) {
+          // the pair's largest score, its new reference, O and the sum rescaled, and the weights again
+          float m = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_ld32(s_at + (uint32_t)c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) m = fmaxf(m, c + y > lim ? -INFINITY : s[y] * a.c);  // NaN left out
+          }
+          const float old = nm;
+          nm = fminf(nm, kLift - m);
+          if (!first) {
+            if (!wait(&sh.pv_done[x], (used[x] - 1u) & 1u)) break;
+            fence_after();
+            const float f = nm == old ? 1.0f : ex2(nm - old);
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D; c += 8) {
+              float o[8];
+              tmem_ld8(o_at + (uint32_t)c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 8; ++y) o[y] *= f;
+              tmem_st8(o_at + (uint32_t)c, o);
+            }
+          }
+          weights();
+        }
+        l += sum;
+#pragma unroll
+        for (int c = 0; c < kTile / 2; c += 16) tmem_st16(s_at + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
+        tmem_wait_st();
+        first = false;
+      }
+      fence_before();
+      __syncwarp();
+#ifdef SDCP_TEST_WAIT_EXPIRY
+      // Test build only (the flag is never set in the library): every fourth CTA keeps the weights of its
+      // first step to itself, so that the waits of its warps run out on purpose.
+      if (lane == 0 && (blockIdx.x % 4 != 0 || used[x] != 0)) mbar_arrive(&sh.p_full[x]);
+#else
+      if (lane == 0) mbar_arrive(&sh.p_full[x]);
+#endif
+    }
+    // O of the pairs: by the block's own threads, all channels, or half of the channels by each group's
+    used[x ^ 1] += (uint32_t)(two ? n_tiles : x == 0 ? n_tiles / 2 : (n_tiles + 1) / 2);
+    if (ok && (two || x == 0 || n_tiles > 1)) wait(&sh.pv_done[x], (used[x] - 1u) & 1u);
+    if (ok && !two && (x == 1 || n_tiles > 1)) wait(&sh.pv_done[x ^ 1], (used[x ^ 1] - 1u) & 1u);
+    if (!ok) break;
+    fence_after();
+    float f0 = nm == INFINITY && l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f, top = nm, all = l;
+    if (!two) {
+      sh.ml[halves & 1u][x][pair] = make_float2(nm, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ml_full);
+      if (!wait(&sh.ml_full, halves & 1u)) break;
+      const float2 u = sh.ml[halves & 1u][0][pair], v = sh.ml[halves & 1u][1][pair];
+      ++halves;
+      top = fminf(u.x, v.x);
+      auto factor = [&](const float2& w) { return w.x == INFINITY && w.y == 0.0f ? 0.0f : w.x == top ? 1.0f : ex2(top - w.x); };
+      f0 = factor(u);
+      f1 = factor(v);
+      all = (f0 != 0.0f ? u.y * f0 : 0.0f) + (f1 != 0.0f ? v.y * f1 : 0.0f);
+    }
+    const int32_t g = it.g0 + at - (row - it.i0) * share;  // head of the cached head's
+    const int64_t place = ((int64_t)it.row0 + row) * a.q_heads + (int64_t)it.kvh * share + g;
+    const bool direct = it.whole && it.joined == 0;
+    const float scale = direct ? __fdividef(1.0f, all) : 1.0f;
+    const int64_t pairs_all = (a.s.total + a.s.B) * a.q_heads;
+    Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
+    float* const to = it.whole ? a.acc + ((it.joined == 2 ? pairs_all : 0) + place) * D : part->o[at];
+    if (live && !direct && (two || x == 0)) {
+      if (it.whole) {
+        a.acc_ml[(it.joined == 2 ? pairs_all : 0) + place] = make_float2(-top, all);
+      } else {
+        part->m[at] = -top;
+        part->l[at] = all;
+      }
+    }
+    const uint32_t o0 = two ? o_at : lanes + kTmemO, o1 = lanes + kTmemO + (uint32_t)D;
+    const int c0 = two ? 0 : x * (D / 2), c1 = two ? D : c0 + D / 2;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 8) {
+      float o[8], w[8];
+      tmem_ld8(o0 + (uint32_t)c, o);
+      if (!two) tmem_ld8(o1 + (uint32_t)c, w);
+      tmem_wait_ld();
+      if (live) {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        o[y] = f0 != 0.0f ? o[y] * f0 : 0.0f;
+        if (!two && f1 != 0.0f) o[y] += w[y] * f1;
+        o[y] *= scale;
+      }
+      if (direct) {
+        uint32_t b[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
+          b[y] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(a.out + place * D + c) = make_uint4(b[0], b[1], b[2], b[3]);
+      } else {
+        *reinterpret_cast<float4*>(to + c) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(to + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
+      }
+      }
+      __syncwarp();
+    }
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.o_free);
+  }
+  if (!ok) sh.dead = 1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const SharedArgs a) {
+  using Sm = SharedSmem<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* const s_q = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* const s_k = s_q + 2 * Sm::kBlock;
+  unsigned char* const s_v = s_k + 2 * Sm::kBlock;
+  unsigned char* const s_c = s_v + 2 * Sm::kBlock;
+  __shared__ SharedState sh;
+
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t cta = (int32_t)blockIdx.x, entries = a.groups + a.s.B;
+  wait_for_previous();
+
+  // this CTA's part of the line: a prefix sum over the entries, a stretch of them per thread
+  const int32_t per = (entries + kThreads - 1) / kThreads;
+  const int32_t e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+  long long mine = 0;
+  for (int32_t e = e0; e < e1; ++e) mine += a.units[e];
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  if (tid == 0) sh.dead = 0;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    all += sh.scan[w];
+  }
+  const long long start = before + incl - mine;
+  const Line line(all, a.ctas);
+  if (cta == 0) {  // for the joining
+    long long at = start;
+    for (int32_t e = e0; e < e1; at += a.units[e++]) a.base[e] = at;
+    if (tid == 0) a.header->total = all;
+  }
+  if (cta >= line.ctas || all == 0) return;
+  const int64_t here = line.first(cta);
+  if (here >= start && here < start + mine) {
+    long long at = start;
+    int32_t e = e0;
+    while (here >= at + a.units[e]) at += a.units[e++];
+    sh.entry = e;
+    sh.base = at;
+  }
+  if (warp == 12) tmem_alloc(&sh.tmem, kTmemCols);
+  if (tid == 0) {
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_free[i], 12);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_free[i], 1);
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.v_free[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    mbar_init(&sh.o_free, 8);
+    mbar_init(&sh.ml_full, 8);
+    mbar_init(&sh.drained, 1);
+    fence_barrier_init();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+  if (warp < 8) {
+    soften<D>(a, sh, warp >> 2, tmem);
+  } else if (warp < 12) {
+    turn<D>(a, sh, s_q, s_k, s_v, s_c);
+  } else if (lane == 0) {
+    Walk walk;
+    walk.begin(a, line, sh.entry, sh.base);
+    multiply<D>(a, sh, line, walk, s_q, s_k, s_v, tmem);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_free(tmem, kTmemCols);
+  if (tid == 0 && sh.dead) atomicOr(&a.header->error, 1u);
+}
+
+// ---- the joining of parts -----------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+constexpr int kJoinAhead = 4;  // parts whose O a warp has in flight
+
+// The parts of a pair in one entry: where they are, in the line's order.
+template <int D> struct Source {
+  int32_t n = 0;       // parts
+  int32_t cta, slot0;  // of the first
+  int64_t place;       // of a single part among the sums of joined pairs; < 0: in the CTAs' parts
+  int32_t col;
+  __device__ __forceinline__ const float* o(const SharedArgs& a, int32_t x) const {
+    return place >= 0 ? a.acc + place * D : reinterpret_cast<const Part<D>*>(a.parts)[x == 0 ? slot0 : 2 * (cta + x)].o[col];
+  }
+  __device__ __forceinline__ float2 ml(const SharedArgs& a, int32_t x) const {
+    if (place >= 0) return a.acc_ml[place];
+    const Part<D>& p = reinterpret_cast<const Part<D>*>(a.parts)[x == 0 ? slot0 : 2 * (cta + x)];
+    return make_float2(p.m[col], p.l[col]);
+  }
+};
+
+// A warp a pair of a row and a head: the sum of its parts, where it has more than one.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedArgs a) {
+  constexpr int kPer = D / 32;
+  const int lane = (int)(threadIdx.x & 31u);
+  const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), pairs_all = (a.s.total + a.s.B) * a.q_heads;
+  wait_for_previous();
+  if (a.header->error != 0u) {
+    for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
+      a.status[b] = SDCP_S_INTERNAL;
+    return;
+  }
+  if (id >= pairs_all || a.header->total == 0) return;
+  const int64_t row = id / a.q_heads;
+  const int32_t h = (int32_t)(id - row * a.q_heads), share = a.q_heads / a.kv.heads, kvh = h / share;
+  const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
+  if (a.status[b] != SDCP_S_OK) return;
+  const Line line(a.header->total, a.ctas);
+  auto source = [&](int32_t id_of, const Entry& e, int64_t offset) {
+    Source<D> s;
+    const Lengths len(e);
+    const int32_t c = (int32_t)(row - e.row0) * share + (h - kvh * share), chunk = c / kMostPairs;
+    const int32_t cost = chunk < e.full ? kTwoBlocks : cost_of(e.rest), all = e.tiles + kItemUnits;
+    const int64_t t0 = a.base[id_of] + kvh * len.head + chunk * len.item;
+    s.cta = line.cta_of(t0);
+    s.n = line.cta_of(t0 + (int64_t)(all - 1) * cost) - s.cta + 1;
+    s.col = c - chunk * kMostPairs;
+    s.place = s.n == 1 ? offset + row * a.q_heads + h : -1;
+    s.slot0 = s.n == 1 ? 0 : a.first_slot[s.cta];
+    return s;
+  };
+  const Entry mine = a.entries[a.groups + b];
+  if (row < mine.row0 || row >= (int64_t)mine.row0 + mine.rows) return;  // (offsets that do not begin at 0)
+  Source<D> one = source(a.groups + b, mine, pairs_all), two;
+  if (mine.joined) {
+    const int32_t g = a.group_of[b];
+    two = source(g, a.entries[g], 0);
+  } else if (one.n == 1) {
+    return;  // written already
+  }
+  const int32_t n = one.n + two.n;
+  auto ml_of = [&](int32_t x) { return x < one.n ? one.ml(a, x) : two.ml(a, x - one.n); };
+  float m = -INFINITY;
+  for (int32_t x = lane; x < n; x += 32) m = fmaxf(m, ml_of(x).x);
+  m = warp_max(m);
+  using Chunk = typename std::conditional<D == 128, float4, float2>::type;  // a lane's channels
+  float o[kPer], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
+  for (int32_t x0 = 0; x0 < n; x0 += 32) {
+    float f = 0.0f;
+    if (x0 + lane < n) {
+      const float2 w = ml_of(x0 + lane);
+      f = w.x != -INFINITY || w.y != 0.0f ? (w.x == m ? 1.0f : ex2(w.x - m)) : 0.0f;  // 0 where it holds nothing of the pair
+      if (f != 0.0f) sum += w.y * f;
+    }
+    const int32_t here = min(32, n - x0);
+    for (int32_t x = 0; x < here; x += kJoinAhead) {
+      __align__(16) float v[kJoinAhead][kPer];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const int32_t y = x0 + x + u;
+        if (x + u < here && __shfl_sync(0xFFFFFFFFu, f, (x + u) & 31) != 0.0f)
+          *reinterpret_cast<Chunk*>(v[u]) = *reinterpret_cast<const Chunk*>((y < one.n ? one.o(a, y) : two.o(a, y - one.n)) + lane * kPer);
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const float fx = __shfl_sync(0xFFFFFFFFu, f, (x + u) & 31);
+        if (x + u < here && fx != 0.0f) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) o[k] += v[u][k] * fx;
+        }
+      }
+    }
+  }
+  sum = warp_reduce(sum, [](float x, float y) { return x + y; });
+  __nv_bfloat16* const out = a.out + (row * a.q_heads + h) * D;
+#pragma unroll
+  for (int k = 0; k < kPer; k += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + lane * kPer + k) = __floats2bfloat162_rn(__fdividef(o[k], sum), __fdividef(o[k + 1], sum));
+}
+
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// The workspace, piece by piece.
+struct Layout {
+  size_t group_status, group_of, common, entries, units, base, first_slot, parts, acc, acc_ml, bytes;
+  Layout(int64_t B, int64_t total, int64_t groups, int64_t q_heads, int64_t dim) {
+    size_t at = 256;  // the header
+    auto take = [&](size_t n) {
+      const size_t here = at;
+      at += round256(n);
+      return here;
+    };
+    const size_t pairs = (size_t)(total + B) * (size_t)q_heads;
+    group_status = take((size_t)groups * 4);
+    group_of = take((size_t)B * 4);
+    common = take((size_t)B * 4);
+    entries = take((size_t)(groups + B) * sizeof(Entry));
+    units = take((size_t)(groups + B) * 8);
+    base = take((size_t)(groups + B) * 8);
+    first_slot = take(kMaxSms * 4);
+    parts = take((size_t)kMaxSms * 2 * (dim == 128 ? sizeof(Part<128>) : sizeof(Part<64>)));
+    acc = take(pairs * 2 * (size_t)dim * 4);
+    acc_ml = take(pairs * 2 * 8);
+    bytes = at;
+  }
+};
+
+// Once per device: the kernels' dynamic shared memory.
+constexpr int kMaxDevices = 64;
+struct SharedDevice {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+SharedDevice g_shared_device[kMaxDevices];
+template <int D> void set_shared(cudaError_t* e) {
+  if (*e == cudaSuccess)
+    *e = cudaFuncSetAttribute(attend_shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SharedSmem<D>::kBytes);
+}
+bool shared_ready() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  SharedDevice& d = g_shared_device[dev];
+  std::call_once(d.once, [&] {
+    set_shared<64>(&d.err);
+    set_shared<128>(&d.err);
+  });
+  return d.err == cudaSuccess;
+}
+
+template <int D> cudaError_t launch_shared(const SharedArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_offsets_check(a.s.offsets, a.s.B, a.status, st);
+  if (e != cudaSuccess) return e;
+  if (a.group_offsets != nullptr) e = launch_offsets_check(a.group_offsets, a.groups, a.group_status, st);
+  if (e != cudaSuccess) return e;
+  const bool kernel_before = a.s.B > kScanSessions || a.groups > kScanSessions;
+  e = launch_after_if(kernel_before, shared_check_kernel, (unsigned)a.s.B, kCheckThreads, 0, st, a);
+  if (e != cudaSuccess) return e;
+  e = launch_after(shared_plan_kernel, (unsigned)a.groups, kCheckThreads, 0, st, a);
+  if (e != cudaSuccess) return e;
+  e = launch_after(attend_shared_kernel<D>, (unsigned)a.ctas, kThreads, SharedSmem<D>::kBytes, st, a);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = (a.s.total + a.s.B) * a.q_heads, per = kJoinThreads / 32;
+  return launch_after(shared_join_kernel<D>, (unsigned)((pairs + per - 1) / per), kJoinThreads, 0, st, a);
+}
+
+}  // namespace
+}  // namespace sdcp
+
+using namespace sdcp;
+
+extern "C" size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32_t n_groups, int32_t q_heads, int32_t kv_heads,
+                                                     int32_t head_dim) {
+  if (B < 0 || total_drafts < 0 || n_groups < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (total_drafts > (int64_t)INT32_MAX / 2 - B || q_heads > (1 << 20) || (total_drafts + B) * q_heads > (int64_t)INT32_MAX) return 0;
+  return Layout(B, total_drafts, n_groups > 0 ? n_groups : 1, q_heads, head_dim).bytes;
+}
+
+extern "C" int sdcp_attend_shared_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets, int64_t total_drafts, const int32_t* kv_len,
+                                     int32_t n_groups, const int32_t* group_offsets, const void* q, int64_t q_stride, int32_t q_heads, float scale,
+                                     void* out, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  KvView kv;
+  const int rc = kv_view(cache, &kv);
+  if (rc != SDCP_OK) return rc;
+  const int32_t D = cache->head_dim;
+  if (B < 0 || total_drafts < 0 || n_groups < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0 || !isfinite(scale)) return SDCP_E_INVALID;
+  const size_t need = sdcp_attend_shared_workspace_bytes(B, total_drafts, n_groups, q_heads, cache->kv_heads, D);
+  if (need == 0) return SDCP_E_TOO_LARGE;
+  if (B == 0) return SDCP_OK;
+  if (!m_offsets || !kv_len || !q || !out || !status || (n_groups > 0) != (group_offsets != nullptr)) return SDCP_E_INVALID;
+  if (q_stride < (int64_t)q_heads * D) return SDCP_E_INVALID;
+  if (((uintptr_t)q & 15u) != 0 || ((uintptr_t)out & 15u) != 0 || q_stride % 8 != 0) return SDCP_E_ALIGN;
+  if (!on_words(m_offsets, kv_len, group_offsets, status)) return SDCP_E_ALIGN;
+  if (!workspace || ((uintptr_t)workspace & 255u) != 0 || workspace_bytes < need) return SDCP_E_WORKSPACE;
+  DeviceInfo di;
+  if (!device_info(&di) || !shared_ready()) return SDCP_E_DEVICE;
+  const int32_t groups = n_groups > 0 ? n_groups : 1;
+  char* const w = static_cast<char*>(workspace);
+  const Layout at(B, total_drafts, groups, q_heads, D);
+  const KvSessions s{B, m_offsets, total_drafts, 1, kv_len, 0, INT32_MAX};
+  const SharedArgs a{kv, s, group_offsets, groups, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
+                     static_cast<__nv_bfloat16*>(out), status, D, min(di.sms, kMaxSms), reinterpret_cast<Header*>(w),
+                     reinterpret_cast<int32_t*>(w + at.group_status), reinterpret_cast<int32_t*>(w + at.group_of), reinterpret_cast<int32_t*>(w + at.common),
+                     reinterpret_cast<Entry*>(w + at.entries), reinterpret_cast<int64_t*>(w + at.units), reinterpret_cast<int64_t*>(w + at.base),
+                     reinterpret_cast<int32_t*>(w + at.first_slot), reinterpret_cast<float*>(w + at.parts), reinterpret_cast<float*>(w + at.acc),
+                     reinterpret_cast<float2*>(w + at.acc_ml)};
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 128 ? launch_shared<128>(a, st) : launch_shared<64>(a, st);
+  return e == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
+}

@@ -134,6 +134,10 @@ def _load():
     L.sdcp_attend_workspace_bytes.restype = sz
     L.sdcp_attend_kv.argtypes = [vp, i32, vp, i64, vp, vp, i64, i32, ctypes.c_float, i32, vp, vp, vp, sz, vp]
     L.sdcp_attend_kv.restype = ctypes.c_int
+    L.sdcp_attend_shared_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
+    L.sdcp_attend_shared_workspace_bytes.restype = sz
+    L.sdcp_attend_shared_kv.argtypes = [vp, i32, vp, i64, vp, i32, vp, vp, i64, i32, ctypes.c_float, vp, vp, vp, sz, vp]
+    L.sdcp_attend_shared_kv.restype = ctypes.c_int
     L.sdcp_strerror.argtypes = [ctypes.c_int]
     L.sdcp_strerror.restype = ctypes.c_char_p
     L.sdcp_abi_version.argtypes = []
@@ -605,6 +609,40 @@ def sdcp_attend_kv(cache, page_table, m_offsets, total_drafts, kv_len, q, out, s
           ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts),
           kv_len.data_ptr(), q.data_ptr(), qs, q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), int(window),
           out.data_ptr(), status.data_ptr(), workspace.data_ptr(), workspace.numel())
+
+
+def alloc_attend_shared_workspace(B: int, total_drafts: int, n_groups: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    n = int(lib.sdcp_attend_shared_workspace_bytes(B, total_drafts, n_groups, q_heads, kv_heads, head_dim))
+    if n == 0:
+        raise SdcpError("invalid sizes for the workspace (B=%d, total=%d, %d groups, heads %d / %d of %d)"
+                        % (B, total_drafts, n_groups, q_heads, kv_heads, head_dim))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sdcp_attend_shared_kv(cache, page_table, m_offsets, total_drafts, kv_len, group_offsets, q, out, status, workspace, scale=None,
+                          stream=None):
+    """sdcp_attend_kv (without a window) for sessions that have their first pages in common: sessions
+    group_offsets[g] .. group_offsets[g+1] - 1 (int32 [groups + 1]; None: all) are a group, and the pages on
+    which its rows of page_table agree are read once for it."""
+    B = status.shape[0]
+    rows = int(total_drafts) + B
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise TypeError("q and out must be torch.bfloat16")
+    qs = _heads(q, rows, q.shape[1], cache.head_dim, "q")
+    if not out.is_contiguous() or out.shape[0] < rows or out.shape[1:] != q.shape[1:]:
+        raise ValueError("out must be contiguous and have q's shape")
+    _ints("m_offsets, kv_len and status", m_offsets, kv_len, status)
+    if m_offsets.numel() < B + 1 or kv_len.numel() < B:
+        raise ValueError("m_offsets and kv_len must cover the %d sessions" % B)
+    groups = 0 if group_offsets is None else _is(group_offsets, torch.int32, "group_offsets").numel() - 1
+    if groups < (group_offsets is not None):
+        raise ValueError("group_offsets must be [groups + 1]")
+    desc = cache.desc(page_table, B)
+    _call(lib.sdcp_attend_shared_kv, "sdcp_attend_shared_kv",
+          (q, out, page_table, cache.pages, m_offsets, kv_len, status, group_offsets, workspace), stream,
+          ctypes.byref(desc), B, m_offsets.data_ptr(), int(total_drafts), kv_len.data_ptr(), groups, _addr(group_offsets), q.data_ptr(), qs,
+          q.shape[1], float(cache.head_dim ** -0.5 if scale is None else scale), out.data_ptr(), status.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
 
 
 def sdcp_split_sessions(m_offsets: np.ndarray, params: np.ndarray | None, n_parts: int) -> np.ndarray:
