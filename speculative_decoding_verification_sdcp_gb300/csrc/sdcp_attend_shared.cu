@@ -15,15 +15,15 @@
 // read and turned once serves two blocks of 128 pairs.  (The attention of sessions by themselves has few
 // pairs for its tokens; its kernel makes the tokens the rows.)
 //
-// Thirteen warps: two groups of four for the softmax of a block each, four that read codes and turn them
-// into 16-bit numbers in shared memory, and one that issues the products and plans the items.  With more
-// than 128 pairs each tile goes through both blocks; an item with fewer has its tiles go through the
+// Seventeen warps: two groups of four for the softmax of a block each, four that read keys' codes and turn
+// them into 16-bit numbers in shared memory, four for the values', and one that issues the products and
+// plans the items.  With more than 128 pairs each tile goes through both blocks; an item with fewer has its tiles go through the
 // blocks in turn, as two sums over every other tile that are joined at its end, so the products of one
 // run beside the softmax of the other either way.
 //
-// A weight is 2^7 at the reference, and the reference moves (O and the sum are rescaled, by the pair's
-// thread alone) when a tile's weights sum to more than 2^15: they are 2^7 at most at the tile's start, 128
-// of them reach 2^14, and none can pass binary16's range before the sum tells.
+// A weight is 2^8 at the reference, and the reference moves (O, the sums and the tile's weights so far are
+// rescaled, by the pair's thread alone) when the weights of 32 tokens sum to more than 2^15: no weight can
+// pass binary16's range before the sum tells, and 32 tokens at the reference sum to 2^13.
 #include <climits>
 #include <mutex>
 #include <type_traits>
@@ -36,11 +36,13 @@ namespace {
 constexpr int kPairs = 128;           // of a block
 constexpr int kMostPairs = 2 * kPairs;  // of an item
 constexpr int kTile = 128;            // tokens
-constexpr int kThreads = 13 * 32;
+// Warps: four of each block's softmax, four that turn keys and four values, and one that issues products.
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16;
+constexpr int kThreads = (kProductWarp + 1) * 32;
 constexpr int kMaxSms = 160;          // sizes the workspace
 constexpr int kItems = 4;             // planned ahead
-constexpr float kLift = 7.0f;         // a weight is 2^kLift at its reference
-constexpr float kTopSum = 32768.0f;   // and a tile's weights sum to this at most
+constexpr float kLift = 8.0f;         // a weight is 2^kLift at its reference
+constexpr float kTopSum = 32768.0f;   // and 32 tokens' weights sum to this at most
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // tensor memory: S (and the weights) of two blocks, O of two
 
 // What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.
@@ -331,7 +333,7 @@ struct SharedState {
 
 template <int D> __device__ __forceinline__ void nothing_in(const SharedArgs& a, int32_t slot) {
   Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + slot;
-  for (int x = 0; x < kMostPairs; ++x) {
+  for (int x = (int)(threadIdx.x & 31u); x < kMostPairs; x += 32) {
     part->m[x] = -INFINITY;
     part->l[x] = 0.0f;
   }
@@ -343,11 +345,34 @@ template <int D> __device__ __forceinline__ void plan_item(const SharedArgs& a, 
   if (j == 0 && walk.t >= walk.t_end) nothing_in<D>(a, (int32_t)blockIdx.x * 2);  // no unit begins here
   while (more && (more = walk.next(a, line, it)) && it.k0 >= it.k1) nothing_in<D>(a, it.slot);
   if (!more) it.n = it.k0 = it.k1 = 0;
-  sh.item[j % kItems] = it;
-  mbar_arrive(&sh.item_full[j % kItems]);
+  if ((threadIdx.x & 31u) == 0) {
+    sh.item[j % kItems] = it;
+    mbar_arrive(&sh.item_full[j % kItems]);
+  }
+  __syncwarp();
 }
 
-// ---- the products: one thread ---------------------------------------------------------------
+// ---- the products: a warp, whose registers of a product are uniform; one lane issues ----------
+// (Issued from a branch that one thread takes, each product had its operands moved to uniform registers
+// anew: 180 cycles each against 64 that it takes.)
+__device__ __forceinline__ void issue_smem_a(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{ .reg .pred p, e; elect.sync _|e, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+      "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void issue_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{ .reg .pred p, e; elect.sync _|e, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+      "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void issue_commit(uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred e; elect.sync _|e, 0xFFFFFFFF; @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int D>
 __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, const Line& line, Walk& walk, const unsigned char* s_q, const unsigned char* s_k,
                                          const unsigned char* s_v, uint32_t tmem) {
@@ -362,13 +387,12 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
   uint32_t tiles = 0, q_used = 0, used[2] = {0, 0};  // tiles, blocks of queries and steps of a block so far
   bool ok = true;
   for (uint32_t j = 0; ok; ++j) {
-    const Item& it = sh.item[j % kItems];
-    const bool two = it.n > kPairs;
-    const int32_t n_tiles = it.k1 - it.k0, steps = two ? 2 * n_tiles : n_tiles;
+    const int32_t n = __shfl_sync(0xFFFFFFFFu, sh.item[j % kItems].n, 0);
+    const bool two = n > kPairs;
+    const int32_t n_tiles = __shfl_sync(0xFFFFFFFFu, sh.item[j % kItems].k1 - sh.item[j % kItems].k0, 0), steps = two ? 2 * n_tiles : n_tiles;
     if (n_tiles <= 0) break;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !wait_phase(bar, parity, &sh.dead)) ok = false;
-      return ok;
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &sh.dead));
     };
     auto score = [&](int32_t h) {  // S of step h
       const int x = h & 1;
@@ -382,13 +406,13 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
 #pragma unroll
       for (int y = 0; y < D / 16; ++y) {
         const uint64_t at = (uint64_t)(((y / 4) * (kTile * 128) + (y % 4) * 32) >> 4);
-        mma_smem_a(tmem + kTmemS + (uint32_t)x * 128u, qm + at, km + at, kIdescS, y > 0);
+        issue_smem_a(tmem + kTmemS + (uint32_t)x * 128u, qm + at, km + at, kIdescS, y > 0);
       }
-      mma_commit(&sh.s_full[x]);
-      if (!two || x == 1) mma_commit(&sh.k_free[buf]);
+      issue_commit(&sh.s_full[x]);
+      if (!two || x == 1) issue_commit(&sh.k_free[buf]);
       if (h == steps - 1) {
-        mma_commit(&sh.q_free[q_used & 1u]);
-        if (two) mma_commit(&sh.q_free[(q_used + 1u) & 1u]);
+        issue_commit(&sh.q_free[q_used & 1u]);
+        if (two) issue_commit(&sh.q_free[(q_used + 1u) & 1u]);
       }
       ++used[x];
     };
@@ -409,35 +433,36 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
       fence_after();
 #pragma unroll
       for (int y = 0; y < kTile / 16; ++y)
-        mma_tmem_a(tmem + kTmemO + (uint32_t)(x * D), tmem + kTmemS + (uint32_t)(x * 128 + y * 8), v_mat + (uint64_t)((buf * Sm::kBlock + y * 2048) >> 4),
+        issue_tmem_a(tmem + kTmemO + (uint32_t)(x * D), tmem + kTmemS + (uint32_t)(x * 128 + y / 2 * 32 + y % 2 * 8), v_mat + (uint64_t)((buf * Sm::kBlock + y * 2048) >> 4),
                    kIdescO, h > 1 || y > 0);
-      if (!two || x == 1) mma_commit(&sh.v_free[buf]);
-      mma_commit(&sh.pv_done[x]);  // the last of a step: when it is seen, none is under way
+      if (!two || x == 1) issue_commit(&sh.v_free[buf]);
+      issue_commit(&sh.pv_done[x]);  // the last of a step: when it is seen, none is under way
     }
     tiles += (uint32_t)n_tiles;
     q_used += two ? 2u : 1u;
   }
   if (!ok) {  // products under way end before the tensor memory is given back
     sh.dead = 1;
-    mma_commit(&sh.drained);
+    issue_commit(&sh.drained);
     (void)wait_phase(&sh.drained, 0u, nullptr);
   }
 }
 
-// ---- the turning: four warps, a token of the tile a thread -----------------------------------
-template <int D>
-__device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsigned char* s_q, unsigned char* s_k, unsigned char* s_v, unsigned char* s_c) {
+// ---- the turning: four warps for the keys and four for the values, a token of the tile a thread ----
+template <int D, bool kValues>
+__device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsigned char* s_q, unsigned char* s_to, unsigned char* s_c) {
   using Sm = SharedSmem<D>;
   constexpr int kGroups = D / kKvGroup;
   const int tok = (int)threadIdx.x & 127, lane = tok & 31;
-  const uint32_t one_k = kept(0x43004300u), one_v = kept(0x64006400u);
-  const uint32_t to = (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);  // a token's line in an atom, swizzled
+  const uint32_t one = kept(kValues ? 0x64006400u : 0x43004300u);
+  const uint32_t to = smem_u32(s_to) + (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);  // a token's line in an atom, swizzled
   const uint32_t c_at = smem_u32(s_c) + (uint32_t)tok * 16u, sb_at = smem_u32(s_c) + kTile * (D / 2) + (uint32_t)tok * 4u;
   const int sb_shift = D == 128 ? 0 : (tok & 1) * 16;  // of the thread's own scales (tiles start at even tokens)
   // a token that is not read keeps old codes: finite numbers, whose weight is zero
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at + Sm::kCodes), "r"(0u) : "memory");
   const int32_t share = a.q_heads / a.kv.heads;
+  uint64_t* const full = kValues ? sh.v_full : sh.k_full;
+  uint64_t* const freed = kValues ? sh.v_free : sh.k_free;
   uint32_t tiles = 0, q_used = 0;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // a warp agrees on it
@@ -451,91 +476,74 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
     if (lane == 0) mbar_arrive(&sh.item_free[j % kItems]);
     const int32_t n_tiles = it.k1 - it.k0;
     if (n_tiles <= 0) break;
-    // queries of the pairs, zero past them (the oldest group of copies: they are there with the first keys)
-    for (int x = 0; x < (it.n > kPairs ? 2 : 1); ++x, ++q_used) {
-      if (q_used >= 2) wait(&sh.q_free[q_used & 1u], ((q_used >> 1) - 1u) & 1u);
-      if (!ok) break;
-      const __nv_bfloat16* const q0 = a.q + ((int64_t)it.row0 + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
-      const int ch = tok % (D / 8);
-      const uint32_t dst = smem_u32(s_q) + (q_used & 1u) * Sm::kBlock + (uint32_t)(ch / 8) * (kTile * 128);
-#pragma unroll 4
-      for (int col = tok / (D / 8); col < kPairs; col += 128 / (D / 8)) {
-        const int32_t at = x * kPairs + col, c = min(at, it.n - 1) + it.g0, r = c / share;
-        copy_async16_or_zero(dst + (uint32_t)col * 128u + (uint32_t)(((ch & 7) ^ (col & 7)) << 4), q0 + r * a.q_stride + (c - r * share) * D + ch * 8,
-                             at < it.n);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     // a tile ahead: the page of the next token, and the copy of its codes to the thread's own places
     uint32_t pos = (uint32_t)it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok;
-    const uint32_t end = (uint32_t)it.end, in_page = (uint32_t)it.kvh * 2u * (uint32_t)a.kv.block;
+    const uint32_t end = (uint32_t)it.end, in_page = ((uint32_t)it.kvh * 2u + (kValues ? 1u : 0u)) * (uint32_t)a.kv.block;
     const int32_t* const table = a.kv.page_table + (int64_t)it.table_row * a.kv.max_pages;
     auto page_of = [&](uint32_t p, bool some) { return some && p < end ? table[p >> a.kv.log_page] : -1; };
-    auto fetch = [&](int which, uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read)
+    auto fetch = [&](uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read)
       if (page >= 0) {
         const uint32_t slot = p & ((1u << a.kv.log_page) - 1u);
-        const uint8_t* const blk = a.kv.pages + (uint64_t)(uint32_t)page * (uint32_t)a.kv.page + (in_page + (which ? (uint32_t)a.kv.block : 0u));
+        const uint8_t* const blk = a.kv.pages + (uint64_t)(uint32_t)page * (uint32_t)a.kv.page + in_page;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-          copy_async16(c_at + (uint32_t)(which * Sm::kCodes + g * kTile * 16), blk + ((((uint32_t)g << a.kv.log_page) + slot) * 16u));
+        for (int g = 0; g < kGroups; ++g) copy_async16(c_at + (uint32_t)(g * kTile * 16), blk + ((((uint32_t)g << a.kv.log_page) + slot) * 16u));
         // four scale bytes of a token, or two each of a pair of tokens
-        copy_async4(sb_at + (uint32_t)which * Sm::kCodes, blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
+        copy_async4(sb_at, blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int32_t page = page_of(pos, true);
-    fetch(0, pos, page);
-    fetch(1, pos, page);
+    if (!kValues) {  // queries of the pairs, zero past them: they are there with the first keys
+      for (int x = 0; x < (it.n > kPairs ? 2 : 1); ++x, ++q_used) {
+        if (q_used >= 2) wait(&sh.q_free[q_used & 1u], ((q_used >> 1) - 1u) & 1u);
+        if (!ok) break;
+        const __nv_bfloat16* const q0 = a.q + ((int64_t)it.row0 + it.i0) * a.q_stride + (int64_t)it.kvh * share * D;
+        const int ch = tok % (D / 8);
+        const uint32_t dst = smem_u32(s_q) + (q_used & 1u) * Sm::kBlock + (uint32_t)(ch / 8) * (kTile * 128);
+#pragma unroll 4
+        for (int col = tok / (D / 8); col < kPairs; col += 128 / (D / 8)) {
+          const int32_t at = x * kPairs + col, c = min(at, it.n - 1) + it.g0, r = c / share;
+          copy_async16_or_zero(dst + (uint32_t)col * 128u + (uint32_t)(((ch & 7) ^ (col & 7)) << 4), q0 + r * a.q_stride + (c - r * share) * D + ch * 8,
+                               at < it.n);
+        }
+      }
+    }
+    fetch(pos, page);
     page = page_of(pos + kTile, n_tiles > 1);
     for (int32_t k = 0; k < n_tiles && ok; ++k, ++tiles, pos += kTile) {
-      const uint32_t buf = tiles & 1u, parity = ((tiles >> 1) - 1u) & 1u;
-      // keys, once the products that read the ones before are done
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      uint32_t sb = ld_shared4(sb_at) >> sb_shift;
-      if (tiles >= 2) wait(&sh.k_free[buf], parity);
+      const uint32_t buf = tiles & 1u;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      const uint32_t sb = ld_shared4(sb_at) >> sb_shift;
+      if (tiles >= 2) wait(&freed[buf], ((tiles >> 1) - 1u) & 1u);  // the products that read the ones before are done
       if (!ok) break;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const uint4 c = ld_shared16(c_at + (uint32_t)(g * kTile * 16));
-        const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
-        const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
         uint32_t r[16];
-        word_bf16(c.x, one_k, s, m, r);
-        word_bf16(c.y, one_k, s, m, r + 4);
-        word_bf16(c.z, one_k, s, m, r + 8);
-        word_bf16(c.w, one_k, s, m, r + 12);
-        const uint32_t line = smem_u32(s_k) + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128) + to;
+        if (kValues) {
+          const uint32_t s = twice(sb, g) << 7;
+          const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
+          const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
+          word_f16(c.x, one, s, m, s16, m16, r);
+          word_f16(c.y, one, s, m, s16, m16, r + 4);
+          word_f16(c.z, one, s, m, s16, m16, r + 8);
+          word_f16(c.w, one, s, m, s16, m16, r + 12);
+        } else {
+          const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
+          const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
+          word_bf16(c.x, one, s, m, r);
+          word_bf16(c.y, one, s, m, r + 4);
+          word_bf16(c.z, one, s, m, r + 8);
+          word_bf16(c.w, one, s, m, r + 12);
+        }
+        const uint32_t line = to + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128);
 #pragma unroll
         for (int y = 0; y < 4; ++y) st_shared16(line ^ (uint32_t)(((g & 1) * 4 + y) << 4), r[4 * y], r[4 * y + 1], r[4 * y + 2], r[4 * y + 3]);
       }
       fence_async_smem();  // (the item's queries too)
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[buf]);
-      fetch(0, pos + kTile, page);
-      // values
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      sb = ld_shared4(sb_at + Sm::kCodes) >> sb_shift;
-      if (tiles >= 2) wait(&sh.v_free[buf], parity);
-      if (!ok) break;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const uint4 c = ld_shared16(c_at + (uint32_t)(Sm::kCodes + g * kTile * 16));
-        const uint32_t s = twice(sb, g) << 7;
-        const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
-        const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
-        uint32_t r[16];
-        word_f16(c.x, one_v, s, m, s16, m16, r);
-        word_f16(c.y, one_v, s, m, s16, m16, r + 4);
-        word_f16(c.z, one_v, s, m, s16, m16, r + 8);
-        word_f16(c.w, one_v, s, m, s16, m16, r + 12);
-        const uint32_t line = smem_u32(s_v) + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128) + to;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) st_shared16(line ^ (uint32_t)(((g & 1) * 4 + y) << 4), r[4 * y], r[4 * y + 1], r[4 * y + 2], r[4 * y + 3]);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.v_full[buf]);
-      fetch(1, pos + kTile, page);
+      if (lane == 0) mbar_arrive(&full[buf]);
+      fetch(pos + kTile, page);
       page = page_of(pos + 2 * kTile, k + 2 < n_tiles);
     }
     if (!ok) break;
@@ -546,14 +554,92 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
 
 // ---- the softmax: four warps a block of pairs, a pair a thread --------------------------------
 __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
-        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]),
-        "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(at)
-      : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+               : "r"(at)
+               : "memory");
+}
+// The loads are done, and r is what they brought (named, so that no use of it is moved before).
+__device__ __forceinline__ void tmem_loaded(float (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+// Two numbers of binary32 in an instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void halves_of(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Where the weights of tokens c .. c + 31 are too large (or there is no reference yet): the largest of the
+// pair's scores from here to the tile's end, the reference that it sets, and what has been summed so far
+// rescaled.  References are whole numbers apart, so that rescaling is exact (but for weights below binary16's
+// normal ones).
+struct Moved {
+  float nm, f;  // kLift - m, and the factor of what has been summed
+  bool ok;
+};
+template <int D>
+__device__ __noinline__ Moved move_reference(SharedState& sh, int c, int32_t lim, float scale, uint32_t s_at, uint32_t o_at, bool some_before, int x,
+                                             uint32_t used, float nm) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int d = c; d < kTile; d += 8) {
+    float r[8];
+    tmem_ld8(s_at + (uint32_t)d, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 8; ++y) m = fmaxf(m, d + y > lim ? -INFINITY : r[y] * scale);  // NaN left out
+  }
+  const float old = nm;
+  nm = fminf(nm, kLift - ceilf(m));
+  const float by = nm - old;  // a whole number (NaN: both infinite, nothing changes)
+  const float f = nm == old ? 1.0f : by > -126.0f ? __int_as_float((127 + (int)by) << 23) : 0.0f;
+  bool ok = true;
+#pragma unroll 1
+  for (int d = 0; d < c; d += 32) {  // the tile's weights so far
+#pragma unroll 1
+    for (int e = 0; e < 16; e += 8) {
+      float r[8];
+      tmem_ld8(s_at + (uint32_t)(d + e), r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float lo = __half2float(__ushort_as_half((unsigned short)(__float_as_uint(r[y]) & 0xFFFFu)));
+        const float hi = __half2float(__ushort_as_half((unsigned short)(__float_as_uint(r[y]) >> 16)));
+        r[y] = __uint_as_float(pack_f16x2(lo * f, hi * f));
+      }
+      tmem_st8(s_at + (uint32_t)(d + e), r);
+    }
+  }
+  if (some_before) {
+    ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.pv_done[x], (used - 1u) & 1u, &sh.dead));
+    fence_after();
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+      float o[8];
+      tmem_ld8(o_at + (uint32_t)d, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] *= f;
+      tmem_st8(o_at + (uint32_t)d, o);
+    }
+  }
+  tmem_wait_st();
+  return Moved{nm, f, ok};
 }
 
 template <int D>
@@ -587,68 +673,58 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
       fence_after();
       if (some) {
         const int32_t lim = limit - k * kTile;
-        const bool masked = __any_sync(0xFFFFFFFFu, lim < kTile - 1);
-        uint32_t p[kTile / 2];
-        float sum;
-        auto weigh = [&](auto with_mask) {
-          sum = 0.0f;
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            float s[32];
-            tmem_ld32(s_at + (uint32_t)c, s);
-            tmem_wait_ld();
+        float sum = 0.0f;  // of the tile's weights
+        // 32 tokens' weights, over the scores they come from
+        auto weigh = [&](float(&s)[32], int c, auto with_mask) {
+          uint32_t w[16];
+          float part;
+          auto weights = [&] {
+            const uint64_t c2 = pair_of(a.c, a.c), nm2 = pair_of(nm, nm);
+            uint64_t sums[2] = {0, 0};
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
-              float u = fmaf(s[y], a.c, nm), v = fmaf(s[y + 1], a.c, nm);
+              float u, v;
+              halves_of(fma_pair(pair_of(s[y], s[y + 1]), c2, nm2), u, v);
               if (with_mask) {
                 if (c + y > lim) u = -INFINITY;
                 if (c + y + 1 > lim) v = -INFINITY;
               }
               u = ex2(u);
               v = ex2(v);
-              sum += u + v;
-              p[(c + y) / 2] = pack_f16x2(u, v);
+              sums[y / 2 % 2] = add_pair(sums[y / 2 % 2], pair_of(u, v));
+              w[y / 2] = pack_f16x2(u, v);
             }
+            float u, v;
+            halves_of(add_pair(sums[0], sums[1]), u, v);
+            part = u + v;
+          };
+          weights();
+          if (__any_sync(0xFFFFFFFFu, part > kTopSum)) {
+            const Moved moved = move_reference<D>(sh, c, lim, a.c, s_at, o_at, !first, x, used[x], nm);
+            nm = moved.nm;
+            ok &= moved.ok;
+            l *= moved.f;
+            sum *= moved.f;
+            tmem_ld32(s_at + (uint32_t)c, s);
+            tmem_loaded(s);
+            weights();
           }
+          sum += part;
+          tmem_st16(s_at + (uint32_t)c, w);
         };
-        auto weights = [&] {
-          if (masked) weigh(std::true_type{});
-          else weigh(std::false_type{});
-        };
-        if (!first) weights();
-        if (first || __any_sync(0xFFFFFFFFu, sum > kTopSum)) {
-          // the pair's largest score, its new reference, O and the sum rescaled, and the weights again
-          float m = -INFINITY;
-#pragma unroll
+        auto tile = [&](auto with_mask) {
+#pragma unroll 1
           for (int c = 0; c < kTile; c += 32) {
             float s[32];
             tmem_ld32(s_at + (uint32_t)c, s);
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 32; ++y) m = fmaxf(m, c + y > lim ? -INFINITY : s[y] * a.c);  // NaN left out
+            tmem_loaded(s);
+            weigh(s, c, with_mask);
           }
-          const float old = nm;
-          nm = fminf(nm, kLift - m);
-          if (!first) {
-            if (!wait(&sh.pv_done[x], (used[x] - 1u) & 1u)) break;
-            fence_after();
-            const float f = nm == old ? 1.0f : ex2(nm - old);
-            l *= f;
-#pragma unroll
-            for (int c = 0; c < D; c += 8) {
-              float o[8];
-              tmem_ld8(o_at + (uint32_t)c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 8; ++y) o[y] *= f;
-              tmem_st8(o_at + (uint32_t)c, o);
-            }
-          }
-          weights();
-        }
+        };
+        if (__any_sync(0xFFFFFFFFu, lim < kTile - 1)) tile(std::true_type{});
+        else tile(std::false_type{});
+        if (!ok) break;
         l += sum;
-#pragma unroll
-        for (int c = 0; c < kTile / 2; c += 16) tmem_st16(s_at + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(&p[c]));
         tmem_wait_st();
         first = false;
       }
@@ -744,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   unsigned char* const s_c = s_v + 2 * Sm::kBlock;
   __shared__ SharedState sh;
 
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int32_t cta = (int32_t)blockIdx.x, entries = a.groups + a.s.B;
   wait_for_previous();
 
@@ -784,11 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
     sh.entry = e;
     sh.base = at;
   }
-  if (warp == 12) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == kProductWarp) tmem_alloc(&sh.tmem, kTmemCols);
   if (tid == 0) {
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_free[i], 12);
+      mbar_init(&sh.item_free[i], kProductWarp);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_free[i], 1);
@@ -808,12 +884,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sh.tmem;
-  if (warp < 8) {
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
+  if (warp < kKeyWarp) {
     soften<D>(a, sh, warp >> 2, tmem);
-  } else if (warp < 12) {
-    turn<D>(a, sh, s_q, s_k, s_v, s_c);
-  } else if (lane == 0) {
+  } else if (warp < kValueWarp) {
+    turn<D, false>(a, sh, s_q, s_k, s_c);
+  } else if (warp < kProductWarp) {
+    turn<D, true>(a, sh, s_q, s_v, s_c + Sm::kCodes);
+  } else {
     Walk walk;
     walk.begin(a, line, sh.entry, sh.base);
     multiply<D>(a, sh, line, walk, s_q, s_k, s_v, tmem);
@@ -821,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == 12) tmem_free(tmem, kTmemCols);
+  if (warp == kProductWarp) tmem_free(tmem, kTmemCols);
   if (tid == 0 && sh.dead) atomicOr(&a.header->error, 1u);
 }
 
