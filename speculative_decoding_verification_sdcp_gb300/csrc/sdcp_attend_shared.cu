@@ -36,9 +36,9 @@ namespace {
 constexpr int kPairs = 128;           // of a block
 constexpr int kMostPairs = 2 * kPairs;  // of an item
 constexpr int kTile = 128;            // tokens
-// Warps: four of each block's softmax, four that turn keys and four values, and one that issues products.
-constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16;
-constexpr int kThreads = (kProductWarp + 1) * 32;
+// Warps: one that issues products, four of each block's softmax, four that turn keys and four values.
+constexpr int kProductWarp = 0, kSoftWarp = 4, kKeyWarp = 12, kValueWarp = 16;  // (warps 1..3 only take part in the barriers)
+constexpr int kThreads = 20 * 32;
 constexpr int kMaxSms = 160;          // sizes the workspace
 constexpr int kItems = 4;             // planned ahead
 constexpr float kLift = 8.0f;         // a weight is 2^kLift at its reference
@@ -316,8 +316,7 @@ struct Walk {
 template <int D> struct SharedSmem {
   static constexpr int kAtoms = D / 64;                   // 128-byte atoms along the channels
   static constexpr int kBlock = kAtoms * kTile * 128;     // [atom][pair or token][128 bytes]
-  static constexpr int kCodes = kTile * (D / 2 + 4);      // of the next keys, or values: [group][token][16 bytes], [token][4 bytes] of scales
-  static constexpr size_t kBytes = (size_t)6 * kBlock + 2 * kCodes + 1024;  // two of queries, keys and values; and the alignment to 1024
+  static constexpr size_t kBytes = (size_t)6 * kBlock + 1024;  // two of queries, keys and values; and the alignment to 1024
 };
 struct SharedState {
   Item item[kItems];
@@ -373,6 +372,24 @@ __device__ __forceinline__ void issue_commit(uint64_t* bar) {
       : "memory");
 }
 
+// Bounded wait for the phases of two barriers (if wanted), looked at together: a look takes some 150 cycles
+// beside the stores of the warps that turn.
+__device__ __forceinline__ bool wait_both(bool want_a, uint64_t* a, uint32_t parity_a, bool want_b, uint64_t* b, uint32_t parity_b, const volatile int* dead) {
+  const bool odd = (threadIdx.x & 1u) != 0;
+  uint64_t* const bar = odd ? b : a;
+  const uint32_t parity = odd ? parity_b : parity_a;
+  bool done = odd ? !want_b : !want_a;
+  unsigned long long t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (!done) done = mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    if (n % 1024u == 0u) {
+      if (t0 == 0) t0 = global_ns();
+      if (__any_sync(0xFFFFFFFFu, *dead != 0 || global_ns() - t0 > kWaitNs)) return false;
+    }
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, const Line& line, Walk& walk, const unsigned char* s_q, const unsigned char* s_k,
                                          const unsigned char* s_v, uint32_t tmem) {
@@ -384,21 +401,19 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
   bool more = true;
   plan_item<D>(a, sh, line, walk, more, 0);
   plan_item<D>(a, sh, line, walk, more, 1);
-  uint32_t tiles = 0, q_used = 0, used[2] = {0, 0};  // tiles, blocks of queries and steps of a block so far
+  uint32_t tiles = 0, q_used = 0, used0 = 0, used1 = 0;  // tiles, blocks of queries and steps of the blocks so far
   bool ok = true;
   for (uint32_t j = 0; ok; ++j) {
     const int32_t n = __shfl_sync(0xFFFFFFFFu, sh.item[j % kItems].n, 0);
     const bool two = n > kPairs;
     const int32_t n_tiles = __shfl_sync(0xFFFFFFFFu, sh.item[j % kItems].k1 - sh.item[j % kItems].k0, 0), steps = two ? 2 * n_tiles : n_tiles;
     if (n_tiles <= 0) break;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &sh.dead));
-    };
     auto score = [&](int32_t h) {  // S of step h
       const int x = h & 1;
       const uint32_t tile = tiles + (uint32_t)(two ? h >> 1 : h), buf = tile & 1u;
-      if (!two || x == 0) wait(&sh.k_full[buf], (tile >> 1) & 1u);
-      if (used[x] > 0) wait(&sh.pv_done[x], (used[x] - 1u) & 1u);  // the weights of the step before, in the same place
+      const uint32_t used = x ? used1 : used0;
+      // the keys, and the end of the product of the weights of the step before, in the same place
+      ok = wait_both(!two || x == 0, &sh.k_full[buf], (tile >> 1) & 1u, used > 0, &sh.pv_done[x], (used - 1u) & 1u, &sh.dead);
       if (!ok) return;
       fence_after();
       const uint32_t qb = (q_used + (two ? (uint32_t)x : 0u)) & 1u;
@@ -414,21 +429,22 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
         issue_commit(&sh.q_free[q_used & 1u]);
         if (two) issue_commit(&sh.q_free[(q_used + 1u) & 1u]);
       }
-      ++used[x];
+      used0 += x ? 0u : 1u;
+      used1 += x ? 1u : 0u;
     };
     score(0);
     for (int32_t h = 0; h < steps && ok; ++h) {
       if (h + 1 < steps) score(h + 1);
+      if (!ok) break;
       if (h == 0 && ok) {
-        if (j >= 2) wait(&sh.item_free[(j + 2) % kItems], ((j - 2) / kItems) & 1u);
+        if (j >= 2) ok = wait_both(true, &sh.item_free[(j + 2) % kItems], ((j - 2) / kItems) & 1u, false, nullptr, 0u, &sh.dead);
         if (ok) plan_item<D>(a, sh, line, walk, more, j + 2);
       }
       const int x = h & 1;
       const uint32_t tile = tiles + (uint32_t)(two ? h >> 1 : h), buf = tile & 1u;
       // (of its own step: the one after may have been asked for, but needs this product first)
-      if (!two || x == 0) wait(&sh.v_full[buf], (tile >> 1) & 1u);
-      wait(&sh.p_full[x], (used[x] - 1u) & 1u);
-      if (h == 0 && j > 0) wait(&sh.o_free, (j - 1u) & 1u);
+      if (ok) ok = wait_both(!two || x == 0, &sh.v_full[buf], (tile >> 1) & 1u, true, &sh.p_full[x], ((x ? used1 : used0) - 1u) & 1u, &sh.dead);
+      if (ok && h == 0 && j > 0) ok = wait_both(true, &sh.o_free, (j - 1u) & 1u, false, nullptr, 0u, &sh.dead);
       if (!ok) break;
       fence_after();
 #pragma unroll
@@ -450,16 +466,13 @@ __device__ __forceinline__ void multiply(const SharedArgs& a, SharedState& sh, c
 
 // ---- the turning: four warps for the keys and four for the values, a token of the tile a thread ----
 template <int D, bool kValues>
-__device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsigned char* s_q, unsigned char* s_to, unsigned char* s_c) {
+__device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsigned char* s_q, unsigned char* s_to) {
   using Sm = SharedSmem<D>;
   constexpr int kGroups = D / kKvGroup;
   const int tok = (int)threadIdx.x & 127, lane = tok & 31;
   const uint32_t one = kept(kValues ? 0x64006400u : 0x43004300u);
   const uint32_t to = smem_u32(s_to) + (uint32_t)(tok * 128) + ((uint32_t)(tok & 7) << 4);  // a token's line in an atom, swizzled
-  const uint32_t c_at = smem_u32(s_c) + (uint32_t)tok * 16u, sb_at = smem_u32(s_c) + kTile * (D / 2) + (uint32_t)tok * 4u;
   const int sb_shift = D == 128 ? 0 : (tok & 1) * 16;  // of the thread's own scales (tiles start at even tokens)
-  // a token that is not read keeps old codes: finite numbers, whose weight is zero
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb_at), "r"(0u) : "memory");
   const int32_t share = a.q_heads / a.kv.heads;
   uint64_t* const full = kValues ? sh.v_full : sh.k_full;
   uint64_t* const freed = kValues ? sh.v_free : sh.k_free;
@@ -476,21 +489,25 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
     if (lane == 0) mbar_arrive(&sh.item_free[j % kItems]);
     const int32_t n_tiles = it.k1 - it.k0;
     if (n_tiles <= 0) break;
-    // a tile ahead: the page of the next token, and the copy of its codes to the thread's own places
+    // a tile ahead: the next token's codes and scales, and a tile before that its page
     uint32_t pos = (uint32_t)it.begin + (uint32_t)it.k0 * kTile + (uint32_t)tok;
     const uint32_t end = (uint32_t)it.end, in_page = ((uint32_t)it.kvh * 2u + (kValues ? 1u : 0u)) * (uint32_t)a.kv.block;
     const int32_t* const table = a.kv.page_table + (int64_t)it.table_row * a.kv.max_pages;
     auto page_of = [&](uint32_t p, bool some) { return some && p < end ? table[p >> a.kv.log_page] : -1; };
-    auto fetch = [&](uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read)
+    uint4 c[kGroups], next[kGroups];
+    uint32_t sb, next_sb;
+    auto load = [&](uint32_t p, int32_t page) {  // of the token at p, whose page is known (-1: nothing to read, zeros)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) next[g] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      next_sb = 0u;
       if (page >= 0) {
         const uint32_t slot = p & ((1u << a.kv.log_page) - 1u);
         const uint8_t* const blk = a.kv.pages + (uint64_t)(uint32_t)page * (uint32_t)a.kv.page + in_page;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) copy_async16(c_at + (uint32_t)(g * kTile * 16), blk + ((((uint32_t)g << a.kv.log_page) + slot) * 16u));
+        for (int g = 0; g < kGroups; ++g) next[g] = *reinterpret_cast<const uint4*>(blk + ((((uint32_t)g << a.kv.log_page) + slot) * 16u));
         // four scale bytes of a token, or two each of a pair of tokens
-        copy_async4(sb_at, blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
+        next_sb = *reinterpret_cast<const uint32_t*>(blk + ((D / 2u << a.kv.log_page) + (D == 128 ? slot * 4u : (slot & ~1u) * 2u)));
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int32_t page = page_of(pos, true);
     if (!kValues) {  // queries of the pairs, zero past them: they are there with the first keys
@@ -508,33 +525,36 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
         }
       }
     }
-    fetch(pos, page);
+    load(pos, page);
     page = page_of(pos + kTile, n_tiles > 1);
+    if (!kValues) asm volatile("cp.async.wait_all;" ::: "memory");
     for (int32_t k = 0; k < n_tiles && ok; ++k, ++tiles, pos += kTile) {
       const uint32_t buf = tiles & 1u;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      const uint32_t sb = ld_shared4(sb_at) >> sb_shift;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) c[g] = next[g];
+      sb = next_sb >> sb_shift;
+      load(pos + kTile, page);
+      page = page_of(pos + 2 * kTile, k + 2 < n_tiles);
       if (tiles >= 2) wait(&freed[buf], ((tiles >> 1) - 1u) & 1u);  // the products that read the ones before are done
       if (!ok) break;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const uint4 c = ld_shared16(c_at + (uint32_t)(g * kTile * 16));
         uint32_t r[16];
         if (kValues) {
           const uint32_t s = twice(sb, g) << 7;
           const uint32_t s16 = fma_f16x2(s, 0x2C002C00u, 0u);                                   // s / 16
           const uint32_t m = fma_f16x2(s, 0xE408E408u, 0u), m16 = fma_f16x2(s, 0xD480D480u, 0u);  // -1032 s, -72 s
-          word_f16(c.x, one, s, m, s16, m16, r);
-          word_f16(c.y, one, s, m, s16, m16, r + 4);
-          word_f16(c.z, one, s, m, s16, m16, r + 8);
-          word_f16(c.w, one, s, m, s16, m16, r + 12);
+          word_f16(c[g].x, one, s, m, s16, m16, r);
+          word_f16(c[g].y, one, s, m, s16, m16, r + 4);
+          word_f16(c[g].z, one, s, m, s16, m16, r + 8);
+          word_f16(c[g].w, one, s, m, s16, m16, r + 12);
         } else {
           const uint32_t s = twice(sb, g) * 16u + (kScaleBias << 4) * 0x10001u;
           const uint32_t m = fma_bf16x2(s, 0xC308C308u, 0u);  // -136 s
-          word_bf16(c.x, one, s, m, r);
-          word_bf16(c.y, one, s, m, r + 4);
-          word_bf16(c.z, one, s, m, r + 8);
-          word_bf16(c.w, one, s, m, r + 12);
+          word_bf16(c[g].x, one, s, m, r);
+          word_bf16(c[g].y, one, s, m, r + 4);
+          word_bf16(c[g].z, one, s, m, r + 8);
+          word_bf16(c[g].w, one, s, m, r + 12);
         }
         const uint32_t line = to + buf * Sm::kBlock + (uint32_t)(g / 2) * (kTile * 128);
 #pragma unroll
@@ -543,8 +563,6 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
       fence_async_smem();  // (the item's queries too)
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[buf]);
-      fetch(pos + kTile, page);
-      page = page_of(pos + 2 * kTile, k + 2 < n_tiles);
     }
     if (!ok) break;
   }
@@ -648,7 +666,7 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
   const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32 lanes of tensor memory, in bits 16 up
   const uint32_t s_at = lanes + kTmemS + (uint32_t)x * 128u, o_at = lanes + kTmemO + (uint32_t)(x * D);
   const int32_t share = a.q_heads / a.kv.heads;
-  uint32_t used[2] = {0, 0}, halves = 0;  // steps of the blocks, and items of halves, so far
+  uint32_t used = 0, used_other = 0, halves = 0;  // steps of the block and of the other one, and items of halves, so far
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // a warp agrees on it
     if (ok) ok = __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &sh.dead));
@@ -668,57 +686,51 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
     int32_t limit = it.last + it.step * row - it.begin - it.k0 * kTile;  // last token that it sees, from the tile's start
     float nm = INFINITY, l = 0.0f;  // kLift - m: what a scaled score is shifted by (infinity: no score yet), and the sum
     bool first = true;
-    for (int32_t k = two ? 0 : x; k < n_tiles; k += two ? 1 : 2, ++used[x]) {
-      if (!wait(&sh.s_full[x], used[x] & 1u)) break;
+    for (int32_t k = two ? 0 : x; k < n_tiles; k += two ? 1 : 2, ++used) {
+      if (!wait(&sh.s_full[x], used & 1u)) break;
       fence_after();
       if (some) {
         const int32_t lim = limit - k * kTile;
         float sum = 0.0f;  // of the tile's weights
-        // 32 tokens' weights, over the scores they come from
-        auto weigh = [&](float(&s)[32], int c, auto with_mask) {
-          uint32_t w[16];
-          float part;
-          auto weights = [&] {
-            const uint64_t c2 = pair_of(a.c, a.c), nm2 = pair_of(nm, nm);
-            uint64_t sums[2] = {0, 0};
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              float u, v;
-              halves_of(fma_pair(pair_of(s[y], s[y + 1]), c2, nm2), u, v);
-              if (with_mask) {
-                if (c + y > lim) u = -INFINITY;
-                if (c + y + 1 > lim) v = -INFINITY;
-              }
-              u = ex2(u);
-              v = ex2(v);
-              sums[y / 2 % 2] = add_pair(sums[y / 2 % 2], pair_of(u, v));
-              w[y / 2] = pack_f16x2(u, v);
-            }
-            float u, v;
-            halves_of(add_pair(sums[0], sums[1]), u, v);
-            part = u + v;
-          };
-          weights();
-          if (__any_sync(0xFFFFFFFFu, part > kTopSum)) {
-            const Moved moved = move_reference<D>(sh, c, lim, a.c, s_at, o_at, !first, x, used[x], nm);
-            nm = moved.nm;
-            ok &= moved.ok;
-            l *= moved.f;
-            sum *= moved.f;
-            tmem_ld32(s_at + (uint32_t)c, s);
-            tmem_loaded(s);
-            weights();
-          }
-          sum += part;
-          tmem_st16(s_at + (uint32_t)c, w);
-        };
+        // (rolled: five kinds of warps share a scheduler's instruction cache)
         auto tile = [&](auto with_mask) {
+          const uint64_t c2 = pair_of(a.c, a.c);
 #pragma unroll 1
           for (int c = 0; c < kTile; c += 32) {
-            float s[32];
-            tmem_ld32(s_at + (uint32_t)c, s);
-            tmem_loaded(s);
-            weigh(s, c, with_mask);
+            float part;
+            uint32_t w[16];
+#pragma unroll 1
+            for (bool moved = false;; moved = true) {
+              float s[32];
+              tmem_ld32(s_at + (uint32_t)c, s);
+              tmem_loaded(s);
+              const uint64_t nm2 = pair_of(nm, nm);
+              uint64_t sums[2] = {0, 0};
+#pragma unroll
+              for (int y = 0; y < 32; y += 2) {
+                float u, v;
+                halves_of(fma_pair(pair_of(s[y], s[y + 1]), c2, nm2), u, v);
+                if (with_mask) {
+                  if (c + y > lim) u = -INFINITY;
+                  if (c + y + 1 > lim) v = -INFINITY;
+                }
+                u = ex2(u);
+                v = ex2(v);
+                sums[y / 2 % 2] = add_pair(sums[y / 2 % 2], pair_of(u, v));
+                w[y / 2] = pack_f16x2(u, v);
+              }
+              float u, v;
+              halves_of(add_pair(sums[0], sums[1]), u, v);
+              part = u + v;
+              if (moved || !__any_sync(0xFFFFFFFFu, part > kTopSum)) break;
+              const Moved m = move_reference<D>(sh, c, lim, a.c, s_at, o_at, !first, x, used, nm);
+              nm = m.nm;
+              ok &= m.ok;
+              l *= m.f;
+              sum *= m.f;
+            }
+            sum += part;
+            tmem_st16(s_at + (uint32_t)c, w);  // over the scores they come from
           }
         };
         if (__any_sync(0xFFFFFFFFu, lim < kTile - 1)) tile(std::true_type{});
@@ -733,15 +745,15 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
 #ifdef SDCP_TEST_WAIT_EXPIRY
       // Test build only (the flag is never set in the library): every fourth CTA keeps the weights of its
       // first step to itself, so that the waits of its warps run out on purpose.
-      if (lane == 0 && (blockIdx.x % 4 != 0 || used[x] != 0)) mbar_arrive(&sh.p_full[x]);
+      if (lane == 0 && (blockIdx.x % 4 != 0 || used != 0)) mbar_arrive(&sh.p_full[x]);
 #else
       if (lane == 0) mbar_arrive(&sh.p_full[x]);
 #endif
     }
     // O of the pairs: by the block's own threads, all channels, or half of the channels by each group's
-    used[x ^ 1] += (uint32_t)(two ? n_tiles : x == 0 ? n_tiles / 2 : (n_tiles + 1) / 2);
-    if (ok && (two || x == 0 || n_tiles > 1)) wait(&sh.pv_done[x], (used[x] - 1u) & 1u);
-    if (ok && !two && (x == 1 || n_tiles > 1)) wait(&sh.pv_done[x ^ 1], (used[x ^ 1] - 1u) & 1u);
+    used_other += (uint32_t)(two ? n_tiles : x == 0 ? n_tiles / 2 : (n_tiles + 1) / 2);
+    if (ok && (two || x == 0 || n_tiles > 1)) wait(&sh.pv_done[x], (used - 1u) & 1u);
+    if (ok && !two && (x == 1 || n_tiles > 1)) wait(&sh.pv_done[x ^ 1], (used_other - 1u) & 1u);
     if (!ok) break;
     fence_after();
     float f0 = nm == INFINITY && l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f, top = nm, all = l;
@@ -817,7 +829,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   unsigned char* const s_q = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* const s_k = s_q + 2 * Sm::kBlock;
   unsigned char* const s_v = s_k + 2 * Sm::kBlock;
-  unsigned char* const s_c = s_v + 2 * Sm::kBlock;
   __shared__ SharedState sh;
 
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -864,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   if (tid == 0) {
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_free[i], kProductWarp);
+      mbar_init(&sh.item_free[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_free[i], 1);
@@ -885,16 +896,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
-  if (warp < kKeyWarp) {
-    soften<D>(a, sh, warp >> 2, tmem);
-  } else if (warp < kValueWarp) {
-    turn<D, false>(a, sh, s_q, s_k, s_c);
-  } else if (warp < kProductWarp) {
-    turn<D, true>(a, sh, s_q, s_v, s_c + Sm::kCodes);
+  if (warp >= kValueWarp) {
+    turn<D, true>(a, sh, s_q, s_v);
+  } else if (warp >= kKeyWarp) {
+    turn<D, false>(a, sh, s_q, s_k);
+  } else if (warp >= kSoftWarp) {
+    soften<D>(a, sh, (warp - kSoftWarp) >> 2, tmem);
   } else {
-    Walk walk;
-    walk.begin(a, line, sh.entry, sh.base);
-    multiply<D>(a, sh, line, walk, s_q, s_k, s_v, tmem);
+    if (warp == kProductWarp) {
+      Walk walk;
+      walk.begin(a, line, sh.entry, sh.base);
+      multiply<D>(a, sh, line, walk, s_q, s_k, s_v, tmem);
+    }
   }
   __syncwarp();
   fence_before();
