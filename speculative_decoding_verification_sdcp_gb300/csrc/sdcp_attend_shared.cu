@@ -94,8 +94,14 @@ struct Line {
 
 struct Header {
   uint32_t error;   // non-zero: a bounded wait gave up
-  uint32_t pad;
-  int64_t total;    // length of the line
+};
+
+// The item that a CTA begins and others go on with: its parts are the CTA's `first_slot` and the first of the
+// CTAs after it, up to `last`.  n = 0: none.
+struct Cut {
+  int32_t n, first_slot, last;  // n: pairs
+  int32_t row, head, g0;        // output row of the first pair, first head of its cached head, and the pair's place among these
+  int32_t joined, pad;          // as an item's
 };
 
 struct SharedArgs {
@@ -117,12 +123,13 @@ struct SharedArgs {
   int32_t* common;        // [B] leading pages a session has in common with its group's first
   Entry* entries;         // [groups + B]: groups, then sessions
   int64_t* units;         // [groups + B] length on the line
-  int64_t* base;          // [groups + B] place on the line
-  int32_t* first_slot;    // [ctas] where a CTA's last item goes on in others: its part
+  Cut* cuts;              // [ctas]
   float* parts;           // [ctas * 2] of Part
   float* acc;             // [2][rows * q_heads] of O, where a pair has two parts
-  float2* acc_ml;         // [2][rows * q_heads] references and sums
+  float2* acc_ml;         // [2][rows * q_heads] references and sums (or kDone in place of a session's sum)
 };
+constexpr float kDone = -1.0f;  // not joined: the output is there, or the row is no session's
+constexpr int64_t kFewPairs = 8192;
 
 template <int D> struct Part {
   float o[kMostPairs][D];
@@ -136,6 +143,9 @@ __global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const Share
   __shared__ int32_t common;
   let_next_start();
   const int32_t b = (int32_t)blockIdx.x;
+  const int64_t pairs = (a.s.total + a.s.B) * a.q_heads;
+  for (int64_t x = (int64_t)b * kCheckThreads + threadIdx.x; x < pairs; x += (int64_t)gridDim.x * kCheckThreads) a.acc_ml[pairs + x] = make_float2(0.0f, kDone);
+  if (b >= a.s.B) return;
   const bool kernel_before = a.s.B > kScanSessions || a.groups > kScanSessions;
   if (kernel_before) wait_for_previous();
   int32_t st = kv_session_status(a.kv, a.s, b, a.status);
@@ -175,10 +185,7 @@ __global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const Share
     a.group_of[b] = g;
     a.common[b] = st == SDCP_S_OK ? common : 0;
     if (st != SDCP_S_OK) a.units[a.groups + b] = 0;
-    if (b == 0) {
-      a.header->error = 0u;
-      a.header->total = 0;
-    }
+    if (b == 0) a.header->error = 0u;
   }
 }
 
@@ -306,7 +313,8 @@ struct Walk {
     it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
     it.whole = units == all;
     it.joined = en.joined ? (e < a.groups ? 1 : 2) : 0;
-    if (!it.whole && unit0 == 0) a.first_slot[blockIdx.x] = it.slot;  // the CTA's last item, and others go on with it
+    if (!it.whole && unit0 == 0)  // the CTA's last item, and others go on with it
+      a.cuts[blockIdx.x] = Cut{it.n, it.slot, line.cta_of(t + (int64_t)(all - 1) * cost), en.row0 + it.i0, kvh * share, it.g0, it.joined, 0};
     t += (int64_t)units * cost;
     advance();
     return true;
@@ -776,10 +784,10 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
     const float scale = direct ? __fdividef(1.0f, all) : 1.0f;
     const int64_t pairs_all = (a.s.total + a.s.B) * a.q_heads;
     Part<D>* const part = reinterpret_cast<Part<D>*>(a.parts) + it.slot;
-    float* const to = it.whole ? a.acc + ((it.joined == 2 ? pairs_all : 0) + place) * D : part->o[at];
+    float* const to = it.whole ? a.acc + ((it.joined == 1 ? 0 : pairs_all) + place) * D : part->o[at];
     if (live && !direct && (two || x == 0)) {
       if (it.whole) {
-        a.acc_ml[(it.joined == 2 ? pairs_all : 0) + place] = make_float2(-top, all);
+        a.acc_ml[(it.joined == 1 ? 0 : pairs_all) + place] = make_float2(-top, all);
       } else {
         part->m[at] = -top;
         part->l[at] = all;
@@ -857,11 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
   }
   const long long start = before + incl - mine;
   const Line line(all, a.ctas);
-  if (cta == 0) {  // for the joining
-    long long at = start;
-    for (int32_t e = e0; e < e1; at += a.units[e++]) a.base[e] = at;
-    if (tid == 0) a.header->total = all;
-  }
+  if (tid == 0) a.cuts[cta].n = 0;
   if (cta >= line.ctas || all == 0) return;
   const int64_t here = line.first(cta);
   if (here >= start && here < start + mine) {
@@ -917,112 +921,122 @@ __global__ void __launch_bounds__(kThreads, 1) attend_shared_kernel(const Shared
 }
 
 // ---- the joining of parts -----------------------------------------------------------------
+// First the parts of items that were cut, then the two parts of pairs that have a group's and a session's.
+// Four channels a lane, so a pair is a warp's, or half of one's.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinAhead = 4;  // parts whose O a warp has in flight
+constexpr int kJoinAhead = 4;  // parts, or pairs, that a warp has in flight
 
-// The parts of a pair in one entry: where they are, in the line's order.
-template <int D> struct Source {
-  int32_t n = 0;       // parts
-  int32_t cta, slot0;  // of the first
-  int64_t place;       // of a single part among the sums of joined pairs; < 0: in the CTAs' parts
-  int32_t col;
-  __device__ __forceinline__ const float* o(const SharedArgs& a, int32_t x) const {
-    return place >= 0 ? a.acc + place * D : reinterpret_cast<const Part<D>*>(a.parts)[x == 0 ? slot0 : 2 * (cta + x)].o[col];
-  }
-  __device__ __forceinline__ float2 ml(const SharedArgs& a, int32_t x) const {
-    if (place >= 0) return a.acc_ml[place];
-    const Part<D>& p = reinterpret_cast<const Part<D>*>(a.parts)[x == 0 ? slot0 : 2 * (cta + x)];
-    return make_float2(p.m[col], p.l[col]);
-  }
-};
+// How much of a pair's sum a part with this reference and sum holds: 0 where it holds nothing of the pair.
+__device__ __forceinline__ float factor_of(const float2& w, float m) { return w.x != -INFINITY || w.y != 0.0f ? (w.x == m ? 1.0f : ex2(w.x - m)) : 0.0f; }
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* to, float x, float y, float z, float w) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x, y), hi = __floats2bfloat162_rn(z, w);
+  *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
 
-// A warp a pair of a row and a head: the sum of its parts, where it has more than one.
+// A CTA's last item and a pair of it: the sum of the parts, in the line's order, to where a whole item's would be.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedArgs a) {
-  constexpr int kPer = D / 32;
-  const int lane = (int)(threadIdx.x & 31u);
-  const int64_t id = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), pairs_all = (a.s.total + a.s.B) * a.q_heads;
+__global__ void __launch_bounds__(kJoinThreads) shared_cuts_kernel(const SharedArgs a) {
+  constexpr int kLanes = D / 4, kOnce = 32 / kLanes;
+  const int lane = (int)(threadIdx.x & 31u), own = lane / kLanes, sub = lane % kLanes;
+  const int32_t id = (int32_t)(blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)) * kOnce + own, cta = id / kMostPairs, j = id % kMostPairs;
+  let_next_start();
+  wait_for_previous();
+  if (cta >= a.ctas || a.header->error != 0u) return;
+  const Cut cut = a.cuts[cta];
+  if (j - own >= cut.n) return;  // (a warp's pairs are of one item)
+  const bool live = j < cut.n;
+  const Part<D>* const parts = reinterpret_cast<const Part<D>*>(a.parts);
+  const int32_t n = cut.last - cta + 1;
+  auto part = [&](int32_t x) -> const Part<D>& { return parts[x == 0 ? cut.first_slot : 2 * (cta + x)]; };
+  auto state = [&](int32_t x) { return x < n && live ? make_float2(part(x).m[j], part(x).l[j]) : make_float2(-INFINITY, 0.0f); };
+  auto over_pair = [&](float v, auto op) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  };
+  float2 w = state(sub);
+  float m = w.x;
+  for (int32_t x = sub + kLanes; x < n; x += kLanes) m = fmaxf(m, state(x).x);
+  m = over_pair(m, [](float x, float y) { return fmaxf(x, y); });
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f;
+  for (int32_t x0 = 0; x0 < n; x0 += kLanes) {
+    if (x0 > 0) w = state(x0 + sub);
+    const float f = factor_of(w, m);
+    if (f != 0.0f) sum += w.y * f;
+    const int32_t here = min(kLanes, n - x0);
+    for (int32_t x = 0; x < here; x += kJoinAhead) {
+      float4 v[kJoinAhead];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u)
+        if (x + u < here && live) v[u] = *reinterpret_cast<const float4*>(&part(x0 + x + u).o[j][sub * 4]);
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const float fx = __shfl_sync(0xFFFFFFFFu, f, own * kLanes + ((x + u) & (kLanes - 1)));
+        if (x + u < here && fx != 0.0f) {  // (an O that was not written has no weight)
+          o.x += v[u].x * fx;
+          o.y += v[u].y * fx;
+          o.z += v[u].z * fx;
+          o.w += v[u].w * fx;
+        }
+      }
+    }
+  }
+  sum = over_pair(sum, [](float x, float y) { return x + y; });
+  if (!live) return;
+  const int32_t share = a.q_heads / a.kv.heads, r = (cut.g0 + j) / share;
+  const int64_t place = ((int64_t)cut.row + r) * a.q_heads + cut.head + (cut.g0 + j - r * share);
+  if (cut.joined == 0) {
+    store_bf16(a.out + place * D + sub * 4, __fdividef(o.x, sum), __fdividef(o.y, sum), __fdividef(o.z, sum), __fdividef(o.w, sum));
+  } else {
+    const int64_t to = (cut.joined == 1 ? 0 : (a.s.total + a.s.B) * a.q_heads) + place;
+    *reinterpret_cast<float4*>(a.acc + to * D + sub * 4) = o;
+    if (sub == 0) a.acc_ml[to] = make_float2(m, sum);
+  }
+}
+
+// The pairs that have two parts; a warp asks for those of a few pairs at once.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedArgs a, int32_t steps) {
+  constexpr int kLanes = D / 4, kOnce = 32 / kLanes;
+  const int lane = (int)(threadIdx.x & 31u), own = lane / kLanes, c = lane % kLanes * 4;
+  const int64_t warp = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), pairs_all = (a.s.total + a.s.B) * a.q_heads;
   wait_for_previous();
   if (a.header->error != 0u) {
     for (int64_t b = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; b < a.s.B; b += (int64_t)gridDim.x * kJoinThreads)
       a.status[b] = SDCP_S_INTERNAL;
     return;
   }
-  if (id >= pairs_all || a.header->total == 0) return;
-  const int64_t row = id / a.q_heads;
-  const int32_t h = (int32_t)(id - row * a.q_heads), share = a.q_heads / a.kv.heads, kvh = h / share;
-  const int32_t b = find_session(a.s.offsets, a.s.B, row, true);
-  if (a.status[b] != SDCP_S_OK) return;
-  const Line line(a.header->total, a.ctas);
-  auto source = [&](int32_t id_of, const Entry& e, int64_t offset) {
-    Source<D> s;
-    const Lengths len(e);
-    const int32_t c = (int32_t)(row - e.row0) * share + (h - kvh * share), chunk = c / kMostPairs;
-    const int32_t cost = chunk < e.full ? kTwoBlocks : cost_of(e.rest), all = e.tiles + kItemUnits;
-    const int64_t t0 = a.base[id_of] + kvh * len.head + chunk * len.item;
-    s.cta = line.cta_of(t0);
-    s.n = line.cta_of(t0 + (int64_t)(all - 1) * cost) - s.cta + 1;
-    s.col = c - chunk * kMostPairs;
-    s.place = s.n == 1 ? offset + row * a.q_heads + h : -1;
-    s.slot0 = s.n == 1 ? 0 : a.first_slot[s.cta];
-    return s;
-  };
-  const Entry mine = a.entries[a.groups + b];
-  if (row < mine.row0 || row >= (int64_t)mine.row0 + mine.rows) return;  // (offsets that do not begin at 0)
-  Source<D> one = source(a.groups + b, mine, pairs_all), two;
-  if (mine.joined) {
-    const int32_t g = a.group_of[b];
-    two = source(g, a.entries[g], 0);
-  } else if (one.n == 1) {
-    return;  // written already
-  }
-  const int32_t n = one.n + two.n;
-  auto ml_of = [&](int32_t x) { return x < one.n ? one.ml(a, x) : two.ml(a, x - one.n); };
-  float m = -INFINITY;
-  for (int32_t x = lane; x < n; x += 32) m = fmaxf(m, ml_of(x).x);
-  m = warp_max(m);
-  using Chunk = typename std::conditional<D == 128, float4, float2>::type;  // a lane's channels
-  float o[kPer], sum = 0.0f;
+  const int64_t first = warp * steps * kOnce + own;
+  float2 w[kJoinAhead][2];
+  float4 v[kJoinAhead][2];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
-  for (int32_t x0 = 0; x0 < n; x0 += 32) {
-    float f = 0.0f;
-    if (x0 + lane < n) {
-      const float2 w = ml_of(x0 + lane);
-      f = w.x != -INFINITY || w.y != 0.0f ? (w.x == m ? 1.0f : ex2(w.x - m)) : 0.0f;  // 0 where it holds nothing of the pair
-      if (f != 0.0f) sum += w.y * f;
-    }
-    const int32_t here = min(32, n - x0);
-    for (int32_t x = 0; x < here; x += kJoinAhead) {
-      __align__(16) float v[kJoinAhead][kPer];
-#pragma unroll
-      for (int u = 0; u < kJoinAhead; ++u) {
-        const int32_t y = x0 + x + u;
-        if (x + u < here && __shfl_sync(0xFFFFFFFFu, f, (x + u) & 31) != 0.0f)
-          *reinterpret_cast<Chunk*>(v[u]) = *reinterpret_cast<const Chunk*>((y < one.n ? one.o(a, y) : two.o(a, y - one.n)) + lane * kPer);
-      }
-#pragma unroll
-      for (int u = 0; u < kJoinAhead; ++u) {
-        const float fx = __shfl_sync(0xFFFFFFFFu, f, (x + u) & 31);
-        if (x + u < here && fx != 0.0f) {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) o[k] += v[u][k] * fx;
-        }
-      }
+  for (int u = 0; u < kJoinAhead; ++u) {
+    const int64_t pair = first + u * kOnce;
+    const bool some = u < steps && pair < pairs_all;
+    w[u][1] = some ? a.acc_ml[pairs_all + pair] : make_float2(0.0f, kDone);
+    w[u][0] = some ? a.acc_ml[pair] : make_float2(0.0f, 0.0f);
+    if (some) {  // (asked for before it is known whether they are there)
+      v[u][1] = *reinterpret_cast<const float4*>(a.acc + (pairs_all + pair) * D + c);
+      v[u][0] = *reinterpret_cast<const float4*>(a.acc + pair * D + c);
     }
   }
-  sum = warp_reduce(sum, [](float x, float y) { return x + y; });
-  __nv_bfloat16* const out = a.out + (row * a.q_heads + h) * D;
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2)
-    *reinterpret_cast<__nv_bfloat162*>(out + lane * kPer + k) = __floats2bfloat162_rn(__fdividef(o[k], sum), __fdividef(o[k + 1], sum));
+  for (int u = 0; u < kJoinAhead; ++u) {
+    if (w[u][1].y == kDone) continue;
+    const float m = fmaxf(w[u][0].x, w[u][1].x), f0 = factor_of(w[u][0], m), f1 = factor_of(w[u][1], m);
+    const float sum = (f0 != 0.0f ? w[u][0].y * f0 : 0.0f) + (f1 != 0.0f ? w[u][1].y * f1 : 0.0f);
+    auto both = [&](float x, float y) { return __fdividef((f0 != 0.0f ? x * f0 : 0.0f) + (f1 != 0.0f ? y * f1 : 0.0f), sum); };
+    store_bf16(a.out + (first + u * kOnce) * D + c, both(v[u][0].x, v[u][1].x), both(v[u][0].y, v[u][1].y), both(v[u][0].z, v[u][1].z),
+               both(v[u][0].w, v[u][1].w));
+  }
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The workspace, piece by piece.
 struct Layout {
-  size_t group_status, group_of, common, entries, units, base, first_slot, parts, acc, acc_ml, bytes;
+  size_t group_status, group_of, common, entries, units, cuts, parts, acc, acc_ml, bytes;
   Layout(int64_t B, int64_t total, int64_t groups, int64_t q_heads, int64_t dim) {
     size_t at = 256;  // the header
     auto take = [&](size_t n) {
@@ -1036,8 +1050,7 @@ struct Layout {
     common = take((size_t)B * 4);
     entries = take((size_t)(groups + B) * sizeof(Entry));
     units = take((size_t)(groups + B) * 8);
-    base = take((size_t)(groups + B) * 8);
-    first_slot = take(kMaxSms * 4);
+    cuts = take(kMaxSms * sizeof(Cut));
     parts = take((size_t)kMaxSms * 2 * (dim == 128 ? sizeof(Part<128>) : sizeof(Part<64>)));
     acc = take(pairs * 2 * (size_t)dim * 4);
     acc_ml = take(pairs * 2 * 8);
@@ -1073,14 +1086,22 @@ template <int D> cudaError_t launch_shared(const SharedArgs& a, cudaStream_t st)
   if (a.group_offsets != nullptr) e = launch_offsets_check(a.group_offsets, a.groups, a.group_status, st);
   if (e != cudaSuccess) return e;
   const bool kernel_before = a.s.B > kScanSessions || a.groups > kScanSessions;
-  e = launch_after_if(kernel_before, shared_check_kernel, (unsigned)a.s.B, kCheckThreads, 0, st, a);
+  // (blocks beyond the sessions help to mark the pairs)
+  const int64_t marks = ((a.s.total + a.s.B) * a.q_heads + 8 * kCheckThreads - 1) / (8 * kCheckThreads);
+  const unsigned blocks = (unsigned)max((int64_t)a.s.B, min(marks, (int64_t)2 * kMaxSms));
+  e = launch_after_if(kernel_before, shared_check_kernel, blocks, kCheckThreads, 0, st, a);
   if (e != cudaSuccess) return e;
   e = launch_after(shared_plan_kernel, (unsigned)a.groups, kCheckThreads, 0, st, a);
   if (e != cudaSuccess) return e;
   e = launch_after(attend_shared_kernel<D>, (unsigned)a.ctas, kThreads, SharedSmem<D>::kBytes, st, a);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = (a.s.total + a.s.B) * a.q_heads, per = kJoinThreads / 32;
-  return launch_after(shared_join_kernel<D>, (unsigned)((pairs + per - 1) / per), kJoinThreads, 0, st, a);
+  e = launch_after(shared_cuts_kernel<D>, (unsigned)(a.ctas * kMostPairs / (32 / (D / 4)) / (kJoinThreads / 32)), kJoinThreads, 0, st, a);
+  if (e != cudaSuccess) return e;
+  // Many pairs: a few a warp; few are spread over the warps that there are.
+  const int64_t pairs = (a.s.total + a.s.B) * a.q_heads, once = 32 / (D / 4), per = kJoinThreads / 32;
+  const int32_t steps = pairs > kFewPairs ? kJoinAhead : 1;
+  const int64_t warps = (pairs + once * steps - 1) / (once * steps);
+  return launch_after(shared_join_kernel<D>, (unsigned)((warps + per - 1) / per), kJoinThreads, 0, st, a, steps);
 }
 
 }  // namespace
@@ -1121,8 +1142,8 @@ extern "C" int sdcp_attend_shared_kv(const sdcp_kv_cache* cache, int32_t B, cons
   const SharedArgs a{kv, s, group_offsets, groups, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
                      static_cast<__nv_bfloat16*>(out), status, D, min(di.sms, kMaxSms), reinterpret_cast<Header*>(w),
                      reinterpret_cast<int32_t*>(w + at.group_status), reinterpret_cast<int32_t*>(w + at.group_of), reinterpret_cast<int32_t*>(w + at.common),
-                     reinterpret_cast<Entry*>(w + at.entries), reinterpret_cast<int64_t*>(w + at.units), reinterpret_cast<int64_t*>(w + at.base),
-                     reinterpret_cast<int32_t*>(w + at.first_slot), reinterpret_cast<float*>(w + at.parts), reinterpret_cast<float*>(w + at.acc),
+                     reinterpret_cast<Entry*>(w + at.entries), reinterpret_cast<int64_t*>(w + at.units), reinterpret_cast<Cut*>(w + at.cuts),
+                     reinterpret_cast<float*>(w + at.parts), reinterpret_cast<float*>(w + at.acc),
                      reinterpret_cast<float2*>(w + at.acc_ml)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? launch_shared<128>(a, st) : launch_shared<64>(a, st);
