@@ -239,14 +239,40 @@ __device__ __forceinline__ int32_t slot_need(const PoolView& p, int32_t kv_len, 
 }
 constexpr int32_t kAlone = 8;  // entries that a thread does by itself; rows with more are the block's
 
+// What a thread knows of its slot, from one barrier of the cluster to the next.
+struct SlotState {
+  Need n;
+  int32_t kv_len, held;
+  int32_t shared;    // how many of [first, mid) are shared, and which, where the thread does them by itself
+  uint32_t which;
+  int32_t status;
+  long long place;   // of its first new page; < 0: none for it
+  __device__ __forceinline__ bool alone() const { return n.mid - n.first <= kAlone && n.n_fresh() <= kAlone; }
+};
+
+// Bound by latency: three chains of loads (a slot's numbers, its entries, their counts; then the free pages)
+// between barriers of the cluster.  What a slot needs is kept in registers from one to the next where a
+// block has a thread for each of its slots: 192 forked sessions and their 64 parents 14 to 9 us.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads) reserve_kernel(const ReserveArgs a) {
   const PoolView& p = a.p;
   __shared__ long long scratch[kPoolWarps];
-  __shared__ long long sum_need, sum_free, sum_taken, sum_copies;
+  __shared__ long long sum_need, sum_free, sum_taken, sum_copies, sum_long;
   __shared__ int32_t long_slots[kPoolThreads], found[kPoolThreads];
-  __shared__ int32_t n_long, warp_free[kPoolWarps];
+  __shared__ int32_t n_long, any_long, warp_free[kPoolWarps];
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)blockIdx.x;
   const Stretch mine = part_of(p.slots, rank, kCluster, 1), pages = warp_pages(p, rank, warp);
+  const bool once = p.slots <= kCluster * kPoolThreads;  // a thread a slot
+  const int32_t in_page = (1 << p.log_page) - 1;
+  SlotState s;
+  // the slot's numbers; the entries that it has to look at are counted apart
+  auto look = [&](int32_t b) {
+    s = SlotState{Need{0, 0, 0, 0}, 0, 0, 0, 0u, SDCP_S_OK, -1};
+    if (b >= mine.end) return;
+    s.kv_len = a.kv_len[b];
+    s.held = p.held[b];
+    s.status = slot_need(p, s.kv_len, a.upto[b], s.held, &s.n);
+  };
+  if (tid == 0) any_long = 0;
 
   // free pages, and the pages that each slot needs
   const int32_t n_free = count_pages(p, pages, [](int32_t r) { return r == 0 ? 1 : 0; });
@@ -254,24 +280,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
   long long carry = 0;
   for (int32_t b0 = mine.begin; b0 < mine.end; b0 += kPoolThreads) {
     const int32_t b = b0 + tid;
-    Need n{0, 0, 0, 0};
-    int32_t st = SDCP_S_OK, shared = 0;
+    look(b);
     if (tid == 0) n_long = 0;
     __syncthreads();
-    if (b < mine.end) {
-      st = slot_need(p, a.kv_len[b], a.upto[b], p.held[b], &n);
-      if (n.mid - n.first <= kAlone) {
-        for (int32_t i = n.first; i < n.mid; ++i) {
-          const int32_t e = p.row(b)[i];
-          if (!p.inside(e)) st = SDCP_S_BAD_PARAMS;
-          else shared += p.refs[e] > 1;
-        }
-      } else {
-        long_slots[atomicAdd(&n_long, 1)] = tid;
+    if (s.n.mid - s.n.first <= kAlone) {
+      for (int32_t i = s.n.first; i < s.n.mid; ++i) {
+        const int32_t e = p.row(b)[i];
+        if (!p.inside(e)) s.status = SDCP_S_BAD_PARAMS;
+        else if (p.refs[e] > 1) s.which |= 1u << (i - s.n.first);
       }
+      s.shared = __popc(s.which);
+    } else {
+      long_slots[atomicAdd(&n_long, 1)] = tid;
     }
+    if (!s.alone()) any_long = 1;
     __syncthreads();
-    for (int32_t k = 0; k < n_long; ++k) {  // a block at a time: the order does not matter
+    for (int32_t k = 0; k < n_long; ++k) {  // one at a time by the block: the order does not matter
       const int32_t owner = long_slots[k], ob = b0 + owner;
       Need o;
       (void)slot_need(p, a.kv_len[ob], a.upto[ob], p.held[ob], &o);
@@ -284,23 +308,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
       if (tid == 0) found[owner] = all >> 40 ? -1 : (int32_t)all;
       __syncthreads();
     }
-    if (b < mine.end && n.mid - n.first > kAlone) {
-      shared = found[tid];
-      if (shared < 0) st = SDCP_S_BAD_PARAMS;
+    if (s.n.mid - s.n.first > kAlone) {
+      s.shared = found[tid];
+      if (s.shared < 0) s.status = SDCP_S_BAD_PARAMS;
     }
-    const long long need = st == SDCP_S_OK ? (long long)shared + n.n_fresh() : 0;
+    const long long need = s.status == SDCP_S_OK ? (long long)s.shared + s.n.n_fresh() : 0;
     long long all = 0;
     const long long at = carry + block_scan(need, scratch, &all);
     carry += all;
+    s.place = need > 0 ? at : -1;
     if (b < mine.end) {
-      a.start[b] = need > 0 ? at : -1;
-      a.replaced[b] = shared;
-      a.status[b] = st;
+      a.status[b] = s.status;
+      if (!once) {
+        a.start[b] = s.place;
+        a.replaced[b] = s.shared;
+      }
     }
   }
   __syncthreads();
   if (tid == 0) {
     sum_need = carry;
+    sum_long = any_long;
     long long f = 0;
     for (int w = 0; w < kPoolWarps; ++w) f += warp_free[w];
     sum_free = f;
@@ -308,35 +336,40 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
   cluster_meet();
 
   // who gets them, how many copies there are before a slot's, and the free pages in order
-  long long need_before, need_all, free_before, free_all;
+  long long need_before, need_all, free_before, free_all, unused, long_all;
   over_blocks(&sum_need, rank, &need_before, &need_all);
   over_blocks(&sum_free, rank, &free_before, &free_all);
-  long long copies_here = 0, taken_here = 0;
+  over_blocks(&sum_long, rank, &unused, &long_all);
+  constexpr int kCopyBits = 20;  // of a sum of both: the new pages above, the copies (at most one a thread) below
+  long long taken_here = 0, copies_here = 0, copy_place = 0;
   for (int32_t b0 = mine.begin; b0 < mine.end; b0 += kPoolThreads) {
     const int32_t b = b0 + tid;
-    int copy = 0;
-    long long taken = 0;
-    if (b < mine.end && a.start[b] >= 0) {
-      Need n;
-      const int32_t kv_len = a.kv_len[b];
-      (void)slot_need(p, kv_len, a.upto[b], p.held[b], &n);
-      const long long at = need_before + a.start[b];
-      taken = (long long)a.replaced[b] + n.n_fresh();
-      if (at + taken > free_all) {
-        a.status[b] = SDCP_S_LIMIT;
-        a.start[b] = -1;
-        taken = 0;
-      } else {
-        a.start[b] = at;
-        // the round's first page, if it holds tokens already and is shared
-        copy = n.first < n.mid && (kv_len & ((1 << p.log_page) - 1)) != 0 && p.refs[p.row(b)[n.first]] > 1;
+    if (!once) {
+      look(b);
+      if (b < mine.end) {
+        s.place = a.start[b];
+        s.shared = a.replaced[b];
       }
     }
-    long long all = 0, both = 0;
-    (void)block_scan(taken, scratch, &all);
-    taken_here += all;
-    (void)block_scan(copy, scratch, &both);
-    copies_here += both;
+    int copy = 0;
+    long long taken = 0;
+    if (b < mine.end && s.place >= 0) {
+      taken = (long long)s.shared + s.n.n_fresh();
+      s.place += need_before;
+      if (s.place + taken > free_all) {
+        a.status[b] = SDCP_S_LIMIT;
+        s.place = -1;
+        taken = 0;
+      } else if (s.n.first < s.n.mid && (s.kv_len & in_page) != 0) {
+        // the round's first page, if it holds tokens already and is shared
+        copy = once && s.n.mid - s.n.first <= kAlone ? (int)(s.which & 1u) : p.refs[p.row(b)[s.n.first]] > 1;
+      }
+      a.start[b] = s.place;
+    }
+    long long all = 0;
+    copy_place = block_scan(taken << kCopyBits | copy, scratch, &all) & ((1 << kCopyBits) - 1);
+    taken_here += all >> kCopyBits;
+    copies_here += all & ((1 << kCopyBits) - 1);
   }
   if (tid == 0) {
     sum_taken = taken_here;
@@ -356,52 +389,52 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
   }
   cluster_meet();
 
-  // the pages into the rows (no count of a held page changes yet: shared ones are told by it)
-  long long copies_before, copies_all, unused, taken_all;
+  // the pages into the rows
+  long long copies_before, copies_all, taken_all;
   over_blocks(&sum_copies, rank, &copies_before, &copies_all);
   over_blocks(&sum_taken, rank, &unused, &taken_all);
   if (rank == 0 && tid == 0) *a.n_copies = (int32_t)copies_all;
+  // Where each slot is a thread's alone, no count is looked at any more and a replaced page's goes down at once.
+  // Else shared pages are still told by their counts, which change after the last barrier.
+  const bool at_once = long_all == 0 && once;
   for (int32_t b0 = mine.begin; b0 < mine.end; b0 += kPoolThreads) {
     const int32_t b = b0 + tid;
-    Need n{0, 0, 0, 0};
-    long long at = -1;
-    int32_t left = 0;  // tokens that the round's first page holds
+    if (!once) {
+      look(b);
+      s.place = b < mine.end && s.status == SDCP_S_OK && s.n.first < s.n.end ? a.start[b] : -1;
+    }
     if (tid == 0) n_long = 0;
     __syncthreads();
-    if (b < mine.end && a.start[b] >= 0) {
-      const int32_t kv_len = a.kv_len[b];
-      at = a.start[b];
-      left = kv_len & ((1 << p.log_page) - 1);
-      (void)slot_need(p, kv_len, a.upto[b], p.held[b], &n);
-    }
-    int4 record = make_int4(-1, -1, left, 0);
     auto replace = [&](int32_t ob, int32_t i, long long place) {  // entry i of slot ob by the page taken at `place`
       int32_t* const entry = p.row(ob) + i;
       const int32_t page = __ldcg(&a.free_pages[place]), old = *entry;
       *entry = page;
       p.refs[page] = 1;
-      a.dropped[place] = old;
+      if (at_once) atomicSub(&p.refs[old], 1);
+      else a.dropped[place] = old;
       return make_int2(old, page);
     };
     auto take = [&](int32_t ob, int32_t i, long long place) {
       const int32_t page = __ldcg(&a.free_pages[place]);
       p.row(ob)[i] = page;
       p.refs[page] = 1;
-      a.dropped[place] = -1;
+      if (!at_once) a.dropped[place] = -1;
     };
-    const bool alone = n.mid - n.first <= kAlone && n.n_fresh() <= kAlone;
-    if (at >= 0 && n.first < n.mid && left != 0 && p.refs[p.row(b)[n.first]] > 1) {
-      const int2 r = replace(b, n.first, at);  // the first of them, whoever does the rest
+    auto is_shared = [&](int32_t i) { return once && s.n.mid - s.n.first <= kAlone ? (s.which >> (i - s.n.first) & 1u) != 0u : p.refs[p.row(b)[i]] > 1; };
+    // the first page by the slot's own thread, whoever does the rest
+    int4 record = make_int4(-1, -1, s.kv_len & in_page, 0);
+    const bool first_done = s.place >= 0 && s.n.first < s.n.mid && record.z != 0 && is_shared(s.n.first);
+    if (first_done) {
+      const int2 r = replace(b, s.n.first, s.place);
       record.x = r.x;
       record.y = r.y;
     }
-    const bool first_done = record.x >= 0;
-    if (at >= 0 && alone) {
-      long long place = at + (first_done ? 1 : 0);
-      for (int32_t i = n.first + (first_done ? 1 : 0); i < n.mid; ++i)
-        if (p.refs[p.row(b)[i]] > 1) replace(b, i, place++);
-      for (int32_t i = n.fresh; i < n.end; ++i) take(b, i, place++);
-    } else if (at >= 0) {
+    if (s.place >= 0 && s.alone()) {
+      long long place = s.place + (first_done ? 1 : 0);
+      for (int32_t i = s.n.first + (first_done ? 1 : 0); i < s.n.mid; ++i)
+        if (is_shared(i)) replace(b, i, place++);
+      for (int32_t i = s.n.fresh; i < s.n.end; ++i) take(b, i, place++);
+    } else if (s.place >= 0) {
       long_slots[atomicAdd(&n_long, 1)] = tid;
       found[tid] = first_done ? 1 : 0;
     }
@@ -422,16 +455,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
 #pragma unroll 4
       for (int32_t i = o.fresh + tid; i < o.end; i += kPoolThreads) take(ob, i, place + (i - o.fresh));
     }
+    if (!once) {
+      long long all = 0;
+      copy_place = block_scan(first_done ? 1 : 0, scratch, &all);
+      if (first_done) a.copies[copies_before + copy_place] = record;
+      copies_before += all;
+    } else if (first_done) {
+      a.copies[copies_before + copy_place] = record;
+    }
     __syncthreads();  // rows are read by their held[] until here
-    if (at >= 0) p.held[b] = max(p.held[b], n.end);
-    long long all = 0;
-    const long long before = block_scan(first_done ? 1 : 0, scratch, &all);
-    if (first_done) a.copies[copies_before + before] = record;
-    copies_before += all;
+    if (s.place >= 0) p.held[b] = max(s.held, s.n.end);
   }
   cluster_meet();
 
   // the replaced pages lose a holder
+  if (at_once) return;
   for (long long i = (long long)rank * kPoolThreads + tid; i < taken_all; i += kCluster * kPoolThreads) {
     const int32_t old = __ldcg(&a.dropped[i]);
     if (old >= 0) atomicSub(&p.refs[old], 1);

@@ -502,6 +502,8 @@ class KvPool:
             _is(t, torch.int32, what)
         if page_table.dim() != 2 or held.shape != page_table.shape[:1] or refs.shape != (n_pages,):
             raise ValueError("page_table must be [n_slots, max_pages], held [n_slots] and refs [n_pages]")
+        if not page_table.get_device() == held.get_device() == refs.get_device():
+            raise ValueError("page_table, held and refs must be on one device")
         self.page_table, self.held, self.refs = page_table, held, refs
         self.n_pages, self.page_tokens = n_pages, page_tokens
         self.n_slots, self.max_pages = page_table.shape
@@ -509,15 +511,19 @@ class KvPool:
                                held.data_ptr(), refs.data_ptr())
         self._at = ctypes.byref(self.desc)
 
-    def _slots(self, *named):
+    def _slots(self, what, *arrays):
         """The arrays of one entry a slot among a call's arguments."""
-        for t, what in named:
-            if _is(t, torch.int32, what).shape != (self.n_slots,):
+        for t in arrays:
+            if t.dtype is not torch.int32 or not t.is_contiguous():
+                raise TypeError("%s must be contiguous torch.int32 tensors" % what)
+            if t.numel() != self.n_slots:
                 raise ValueError("%s must have an entry for each of the %d slots" % (what, self.n_slots))
 
 
 def _copy_list(copies, n_copies):
-    if _is(copies, torch.int32, "copies").dim() != 2 or copies.shape[1] != 4 or _is(n_copies, torch.int32, "n_copies").numel() < 1:
+    if copies.dtype is not torch.int32 or n_copies.dtype is not torch.int32 or not copies.is_contiguous() or not n_copies.is_contiguous():
+        raise TypeError("copies and n_copies must be contiguous torch.int32 tensors")
+    if copies.dim() != 2 or copies.shape[1] != 4 or n_copies.numel() < 1:
         raise ValueError("copies must be [max_copies, 4] and n_copies [1]")
     return copies.shape[0]
 
@@ -529,8 +535,8 @@ def alloc_pool_workspace(pool) -> torch.Tensor:
 def sdcp_fork_kv(pool, parent, length, status, stream=None):
     """Slot b with parent[b] >= 0 (-1: none) takes the pages of its parent's first length[b] tokens, shared
     with it; parent, length and status (written): int32 [n_slots]."""
-    pool._slots((parent, "parent"), (length, "length"), (status, "status"))
-    _call(lib.sdcp_fork_kv, "sdcp_fork_kv", (status, parent, length, pool.page_table, pool.held, pool.refs), stream,
+    pool._slots("parent, length and status", parent, length, status)
+    _call(lib.sdcp_fork_kv, "sdcp_fork_kv", (status, parent, length, pool.refs), stream,
           pool._at, parent.data_ptr(), length.data_ptr(), status.data_ptr())
 
 
@@ -538,10 +544,10 @@ def sdcp_reserve_kv(pool, kv_len, upto, copies, n_copies, status, workspace, str
     """Pages for positions kv_len[b] .. upto[b] - 1 of each slot, shared ones that lie there replaced.
     copies int32 [max_copies >= n_slots, 4] and n_copies int32 [1] receive the copies to make
     (sdcp_copy_pages); kv_len, upto and status (written): int32 [n_slots]."""
-    pool._slots((kv_len, "kv_len"), (upto, "upto"), (status, "status"))
+    pool._slots("kv_len, upto and status", kv_len, upto, status)
     most = _copy_list(copies, n_copies)
     _call(lib.sdcp_reserve_kv, "sdcp_reserve_kv",
-          (status, kv_len, upto, copies, n_copies, workspace, pool.page_table, pool.held, pool.refs), stream,
+          (status, kv_len, upto, copies, n_copies, workspace, pool.refs), stream,
           pool._at, kv_len.data_ptr(), upto.data_ptr(), copies.data_ptr(), most, n_copies.data_ptr(), status.data_ptr(),
           workspace.data_ptr(), workspace.numel())
 
@@ -560,8 +566,8 @@ def sdcp_copy_pages(cache, copies, n_copies, status, stream=None):
 def sdcp_release_kv(pool, keep, status, stream=None):
     """Each slot keeps the pages of its first keep[b] tokens (negative: all) and gives the others back;
     keep and status (written): int32 [n_slots]."""
-    pool._slots((keep, "keep"), (status, "status"))
-    _call(lib.sdcp_release_kv, "sdcp_release_kv", (status, keep, pool.page_table, pool.held, pool.refs), stream,
+    pool._slots("keep and status", keep, status)
+    _call(lib.sdcp_release_kv, "sdcp_release_kv", (status, keep, pool.refs), stream,
           pool._at, keep.data_ptr(), status.data_ptr())
 
 
@@ -571,7 +577,7 @@ def sdcp_compact_kv(pool, copies, n_copies, n_live, workspace, stream=None):
     most = _copy_list(copies, n_copies)
     if _is(n_live, torch.int32, "n_live").numel() < 1:
         raise ValueError("n_live must be [1]")
-    _call(lib.sdcp_compact_kv, "sdcp_compact_kv", (n_live, copies, n_copies, workspace, pool.page_table, pool.held, pool.refs), stream,
+    _call(lib.sdcp_compact_kv, "sdcp_compact_kv", (n_live, copies, n_copies, workspace, pool.refs), stream,
           pool._at, copies.data_ptr(), most, n_copies.data_ptr(), n_live.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
