@@ -45,10 +45,14 @@ constexpr float kLift = 8.0f;         // a weight is 2^kLift at its reference
 constexpr float kTopSum = 32768.0f;   // and 32 tokens' weights sum to this at most
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // tensor memory: S (and the weights) of two blocks, O of two
 
-// What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.
+// What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.  Graph
+// replays of the measured calls below, us with 5, 8, 3 / 5, 10, 3 / 5, 8, 5 / 8, 13, 2: groups of eight
+// 193 / 213 / 199 / 216, ragged 126 / 140 / 138 / 141, one document 174 / 183 / 178 / 199.
 constexpr int32_t kOneBlock = 5, kTwoBlocks = 8, kItemUnits = 3;
-// A group shares its pages from this many tokens on.
-constexpr int32_t kLeastShared = kTile;
+// What a pair's second part costs, in the same measure: 1 / kPairsAUnit.  A group's pages are attended together
+// where that saves more than the parts cost: 64 sessions of 9 rows in groups of eight, 64 heads, with 512 / 2048
+// shared tokens take 103 / 124 us together, 88 / 130 by themselves; of a row in pairs, 72 / 95 and 70 / 112.
+constexpr int32_t kPairsAUnit = 3;
 
 // Rows over a stretch of tokens: of a group over its shared pages, or of a session over what is behind them.
 struct Entry {
@@ -62,6 +66,10 @@ struct Entry {
   int32_t joined;          // its pairs have another part
 };
 __device__ __forceinline__ int32_t cost_of(int32_t pairs) { return pairs > kPairs ? kTwoBlocks : kOneBlock; }
+// of a tile with all items of a cached head
+__device__ __forceinline__ int64_t cost_of_all(int64_t pairs) {
+  return pairs / kMostPairs * kTwoBlocks + (pairs % kMostPairs > 0 ? cost_of((int32_t)(pairs % kMostPairs)) : 0);
+}
 struct Lengths {  // on the line
   int64_t item, rest, head;
   __device__ __forceinline__ explicit Lengths(const Entry& e) {
@@ -202,6 +210,7 @@ __device__ __forceinline__ void plan_entry(const SharedArgs& a, int32_t id, Entr
 // A block a group: the pages that its sessions share, its entry and theirs.
 __global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const SharedArgs a) {
   __shared__ int32_t pages, low, high;  // of the members that are not refused
+  __shared__ unsigned long long apart;  // what a tile costs that each of them attends for itself
   let_next_start();
   wait_for_previous();
   const int32_t g = (int32_t)blockIdx.x;
@@ -210,23 +219,32 @@ __global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const Shared
     pages = INT_MAX;
     low = INT_MAX;
     high = -1;
+    apart = 0;
   }
   __syncthreads();
+  const int32_t share = a.q_heads / a.kv.heads;
+  unsigned long long cost = 0;
   int32_t least = INT_MAX, lowest = INT_MAX, highest = -1;
   for (int32_t b = b0 + (int32_t)threadIdx.x; b < b1; b += kCheckThreads)
     if (a.status[b] == SDCP_S_OK) {
       least = min(least, a.common[b]);
       lowest = min(lowest, b);
       highest = b;
+      cost += (unsigned long long)cost_of_all((int64_t)(a.s.offsets[b + 1] - a.s.offsets[b] + 1) * share);
     }
   if (highest >= 0) {
     atomicMin(&pages, least);
     atomicMin(&low, lowest);
     atomicMax(&high, highest);
+    atomicAdd(&apart, cost);
   }
   __syncthreads();
-  const int64_t all = high > low ? (int64_t)pages << a.kv.log_page : 0;
-  const int32_t shared = all >= kLeastShared ? (int32_t)all : 0;
+  int32_t shared = 0;
+  if (high > low && pages > 0) {
+    const int64_t tokens = (int64_t)pages << a.kv.log_page, tiles = (tokens + kTile - 1) / kTile;
+    const int64_t pairs = (int64_t)(a.s.offsets[high + 1] + high + 1 - a.s.offsets[low] - low) * share, together = cost_of_all(pairs);
+    if (tiles * ((int64_t)apart - together) > kItemUnits * together + pairs / kPairsAUnit) shared = (int32_t)tokens;
+  }
   if (threadIdx.x == 0) {
     if (shared > 0) {
       const int32_t row0 = a.s.offsets[low] + low;  // (a refused one's offsets may be outside the batch)
@@ -255,7 +273,7 @@ struct Item {
   int32_t whole;                // all of the item's tiles are here
   int32_t joined;               // 0: alone; 1: a group's part; 2: a session's
 };
-// A CTA's way along the line, walked by the thread that issues the products, items ahead of it.
+// A CTA's way along the line, walked by the warp that issues the products, items ahead of it.
 struct Walk {
   int64_t t, t_end, t_first;
   Entry en;

@@ -45,7 +45,8 @@ int pool_view(const sdcp_kv_pool* p, PoolView* out) {
 
 // ---- rows: fork, release, the new places after a compaction -----------------------------
 // A block a slot, bound by latency: a chain of four loads, then the row's entries, kEntries of them a thread
-// in flight.  The block is as large as the longest row that the pool allows can use.
+// in flight.  The block is as large as the longest row that the pool allows can use.  (192 rows of 8 .. 129
+// entries forked: 4.8 us; 63 rows of 7000 entries given back: 8.5 us, 7 MB; both with cold caches.)
 constexpr int kEntries = 8;
 int row_threads(int32_t max_pages) {
   int t = 128;
@@ -150,11 +151,19 @@ __global__ void __launch_bounds__(1024) renumber_kernel(const PoolView p, const 
 // What a call takes depends on all slots before and all pages below, so one cluster does it: each of its
 // blocks has a stretch of the slots and one of the pages, and a few sums are exchanged between its
 // barriers.  (Kernels of their own for the steps would cost a launch each.)
-constexpr int kCluster = 8;
+constexpr int kMostBlocks = 8;
+// One block where it has a thread for each slot and few pages to look over (no barrier beyond its own): pages
+// reserved for 10 slots and for 258 of a pool of 5400 pages, 9.5 and 11.5 us with one block, 13 and 15 with
+// eight; a pool of 12000 pages compacted, 10 us with one, 7 with eight.
+constexpr int32_t kFewPages = 1 << 13;
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
-__device__ __forceinline__ void cluster_meet() {
+template <int kBlocks> __device__ __forceinline__ void cluster_meet() {
+  if (kBlocks == 1) {
+    __syncthreads();
+    return;
+  }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -167,11 +176,11 @@ __device__ __forceinline__ long long of_block(const long long* x, int rank) {
   return v;
 }
 // The sums of x over the blocks before this one, and over all.
-__device__ __forceinline__ void over_blocks(const long long* x, int rank, long long* before, long long* all) {
+template <int kBlocks> __device__ __forceinline__ void over_blocks(const long long* x, int rank, long long* before, long long* all) {
   *before = *all = 0;
 #pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    const long long v = of_block(x, r);
+  for (int r = 0; r < kBlocks; ++r) {
+    const long long v = kBlocks == 1 ? *x : of_block(x, r);
     if (r < rank) *before += v;
     *all += v;
   }
@@ -189,8 +198,8 @@ __device__ __forceinline__ Stretch part_of(int64_t n, int32_t part, int32_t part
   const int64_t each = ((n + parts - 1) / parts + unit - 1) / unit * unit;
   return Stretch{(int32_t)min(n, part * each), (int32_t)min(n, (part + 1) * each)};
 }
-__device__ __forceinline__ Stretch warp_pages(const PoolView& p, int rank, int warp) {
-  return part_of(p.n_pages, rank * kPoolWarps + warp, kCluster * kPoolWarps, 32);
+template <int kBlocks> __device__ __forceinline__ Stretch warp_pages(const PoolView& p, int rank, int warp) {
+  return part_of(p.n_pages, rank * kPoolWarps + warp, kBlocks * kPoolWarps, 32);
 }
 constexpr int kPagesAhead = 8;  // loads of a lane in flight
 // The number of a warp's pages that `which` holds for.
@@ -252,15 +261,15 @@ struct SlotState {
 
 // Bound by latency: three chains of loads (a slot's numbers, its entries, their counts; then the free pages)
 // between barriers of the cluster.  What a slot needs is kept in registers from one to the next where a
-// block has a thread for each of its slots: 192 forked sessions and their 64 parents 14 to 9 us.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads) reserve_kernel(const ReserveArgs a) {
+// block has a thread for each of its slots (258 slots: 18.5 to 15 us, cold, with eight blocks).
+template <int kCluster> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads) reserve_kernel(const ReserveArgs a) {
   const PoolView& p = a.p;
   __shared__ long long scratch[kPoolWarps];
   __shared__ long long sum_need, sum_free, sum_taken, sum_copies, sum_long;
   __shared__ int32_t long_slots[kPoolThreads], found[kPoolThreads];
   __shared__ int32_t n_long, any_long, warp_free[kPoolWarps];
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)blockIdx.x;
-  const Stretch mine = part_of(p.slots, rank, kCluster, 1), pages = warp_pages(p, rank, warp);
+  const Stretch mine = part_of(p.slots, rank, kCluster, 1), pages = warp_pages<kCluster>(p, rank, warp);
   const bool once = p.slots <= kCluster * kPoolThreads;  // a thread a slot
   const int32_t in_page = (1 << p.log_page) - 1;
   SlotState s;
@@ -333,13 +342,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     for (int w = 0; w < kPoolWarps; ++w) f += warp_free[w];
     sum_free = f;
   }
-  cluster_meet();
+  cluster_meet<kCluster>();
 
   // who gets them, how many copies there are before a slot's, and the free pages in order
   long long need_before, need_all, free_before, free_all, unused, long_all;
-  over_blocks(&sum_need, rank, &need_before, &need_all);
-  over_blocks(&sum_free, rank, &free_before, &free_all);
-  over_blocks(&sum_long, rank, &unused, &long_all);
+  over_blocks<kCluster>(&sum_need, rank, &need_before, &need_all);
+  over_blocks<kCluster>(&sum_free, rank, &free_before, &free_all);
+  over_blocks<kCluster>(&sum_long, rank, &unused, &long_all);
   constexpr int kCopyBits = 20;  // of a sum of both: the new pages above, the copies (at most one a thread) below
   long long taken_here = 0, copies_here = 0, copy_place = 0;
   for (int32_t b0 = mine.begin; b0 < mine.end; b0 += kPoolThreads) {
@@ -387,12 +396,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
       at += __popc(who);
     }
   }
-  cluster_meet();
+  cluster_meet<kCluster>();
 
   // the pages into the rows
   long long copies_before, copies_all, taken_all;
-  over_blocks(&sum_copies, rank, &copies_before, &copies_all);
-  over_blocks(&sum_taken, rank, &unused, &taken_all);
+  over_blocks<kCluster>(&sum_copies, rank, &copies_before, &copies_all);
+  over_blocks<kCluster>(&sum_taken, rank, &unused, &taken_all);
   if (rank == 0 && tid == 0) *a.n_copies = (int32_t)copies_all;
   // Where each slot is a thread's alone, no count is looked at any more and a replaced page's goes down at once.
   // Else shared pages are still told by their counts, which change after the last barrier.
@@ -466,7 +475,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     __syncthreads();  // rows are read by their held[] until here
     if (s.place >= 0) p.held[b] = max(s.held, s.n.end);
   }
-  cluster_meet();
+  cluster_meet<kCluster>();
 
   // the replaced pages lose a holder
   if (at_once) return;
@@ -486,13 +495,13 @@ struct CompactArgs {
 
 // With L pages live, a free page below L is hole number (page - live pages below it), and a live page at or
 // past L is move number (live pages above it): move k goes to hole k.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads) compact_kernel(const CompactArgs a) {
+template <int kCluster> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads) compact_kernel(const CompactArgs a) {
   const PoolView& p = a.p;
   __shared__ long long sum_live;
   __shared__ int32_t warp_live[kPoolWarps];
   __shared__ int32_t n_moves;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)blockIdx.x;
-  const Stretch pages = warp_pages(p, rank, warp);
+  const Stretch pages = warp_pages<kCluster>(p, rank, warp);
   let_next_start();
   const int32_t n = count_pages(p, pages, [](int32_t r) { return r > 0 ? 1 : 0; });
   if (lane == 0) warp_live[warp] = n;
@@ -502,9 +511,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     for (int w = 0; w < kPoolWarps; ++w) s += warp_live[w];
     sum_live = s;
   }
-  cluster_meet();
+  cluster_meet<kCluster>();
   long long before, all;
-  over_blocks(&sum_live, rank, &before, &all);
+  over_blocks<kCluster>(&sum_live, rank, &before, &all);
   const int32_t live = (int32_t)all;
   int32_t at = (int32_t)before;
   for (int w = 0; w < warp; ++w) at += warp_live[w];
@@ -538,7 +547,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
     *a.n_live = live;
     if (live == p.n_pages) *a.n_copies = 0;
   }
-  cluster_meet();
+  cluster_meet<kCluster>();
   if (tid == 0) n_moves = __ldcg(a.n_copies);
   __syncthreads();
   for (int32_t k = rank * kPoolThreads + tid; k < n_moves; k += kCluster * kPoolThreads) {
@@ -550,7 +559,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPoolThreads)
 }
 
 // ---- copies -----------------------------------------------------------------------------
-// A warp a block (one head's keys or values of a page), its 16-byte pieces in flight together.
+// A warp a block (one head's keys or values of a page), its 16-byte pieces in flight together.  Bound by memory:
+// 2970 whole pages of 70 KB, 207 MB read and written, 60 us, 6.9 TB/s; 1300 parts of pages of 139 KB, 88 MB, 28 us.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 8;
 
@@ -678,7 +688,9 @@ extern "C" int sdcp_reserve_kv(const sdcp_kv_pool* pool, const int32_t* kv_len, 
   long long* const start = reinterpret_cast<long long*>(w);
   w += round256((size_t)p.slots * 8);
   const ReserveArgs a{p, kv_len, upto, reinterpret_cast<int4*>(copies), n_copies, status, start, reinterpret_cast<int32_t*>(w), free_pages, dropped};
-  reserve_kernel<<<kCluster, kPoolThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p.slots <= kPoolThreads && p.n_pages <= kFewPages) reserve_kernel<1><<<1, kPoolThreads, 0, st>>>(a);
+  else reserve_kernel<kMostBlocks><<<kMostBlocks, kPoolThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? SDCP_OK : SDCP_E_LAUNCH;
 }
 
@@ -694,7 +706,9 @@ extern "C" int sdcp_compact_kv(const sdcp_kv_pool* pool, sdcp_page_copy* copies,
   if (!device_info(&di)) return SDCP_E_DEVICE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int32_t* const to = static_cast<int32_t*>(workspace);
-  compact_kernel<<<kCluster, kPoolThreads, 0, st>>>(CompactArgs{p, reinterpret_cast<int32_t*>(copies), max_copies, n_copies, n_live, to});
+  const CompactArgs a{p, reinterpret_cast<int32_t*>(copies), max_copies, n_copies, n_live, to};
+  if (p.n_pages <= kFewPages) compact_kernel<1><<<1, kPoolThreads, 0, st>>>(a);
+  else compact_kernel<kMostBlocks><<<kMostBlocks, kPoolThreads, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SDCP_E_LAUNCH;
   if (p.slots == 0) return SDCP_OK;
   return launch_after(renumber_kernel, (unsigned)p.slots, (unsigned)row_threads(p.max_pages), 0, st, p, (const int32_t*)n_live, (const int32_t*)to) == cudaSuccess

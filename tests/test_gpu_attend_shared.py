@@ -77,24 +77,33 @@ CASES = [dict(sizes=[1], common=[0], ms=[0], lens=[0], P=16, Hkv=1, share=1, D=6
          dict(sizes=[2], common=[300], ms=[1, 0], lens=[4800, 4823], P=16, Hkv=1, share=1, D=64)]        # one item over many blocks
 
 
+def stretched(case, k):
+    """The case with pages and contexts k times as long: short stretches are attended session by session."""
+    return {**case, "P": case["P"] * k, "lens": [n * k for n in case["lens"]]}
+
+
+@pytest.mark.parametrize("k", [1, 8])
 @pytest.mark.parametrize("ci", range(len(CASES)))
-def test_against_plain(ci):
-    c = Shared(seed=170 + ci, **CASES[ci])
+def test_against_plain(ci, k):
+    if CASES[ci]["P"] * k > 1024:
+        k = 1024 // CASES[ci]["P"]
+    c = Shared(seed=170 + ci, **stretched(CASES[ci], k))
     c.check(*c.run(gap=8 * (ci % 3)))
     if len(c.group_offsets) == 2:
         x, st = c.run(groups=False, workspace_fill=0)
         c.check(x, st)
 
 
+@pytest.mark.parametrize("P", [16, 128])
 @pytest.mark.parametrize("n,groups", [(300, 40), (300, 290), (60, 1)])
-def test_many_sessions_and_groups(n, groups):
+def test_many_sessions_and_groups(n, groups, P):
     """More sessions, and more groups, than a block looks over by itself."""
     r = np.random.default_rng(n + groups)
     cuts = np.sort(r.integers(0, n + 1, groups - 1)).tolist()
     sizes = np.diff([0] + cuts + [n]).tolist()
     common = [int(r.integers(0, 14)) for _ in sizes]
-    lens = [common[g] * 16 + int(r.integers(0, 150)) for g, k in enumerate(sizes) for _ in range(k)]
-    c = Shared(sizes, common, r.integers(0, 4, n).tolist(), lens, P=16, Hkv=1, share=4, D=64, seed=n)
+    lens = [common[g] * P + int(r.integers(0, 150)) for g, k in enumerate(sizes) for _ in range(k)]
+    c = Shared(sizes, common, r.integers(0, 4, n).tolist(), lens, P=P, Hkv=1, share=4, D=64, seed=n)
     c.check(*c.run())
 
 
@@ -124,8 +133,9 @@ def test_rising_scores_move_the_reference(members):
     c.check(*c.run())
 
 
-def test_a_row_with_nan_or_infinities_keeps_to_itself():
-    c = Shared([2, 1], [10, 0], [3, 2, 1], [200, 177, 20], P=16, Hkv=2, share=4, D=128, seed=8)
+@pytest.mark.parametrize("k", [1, 8])
+def test_a_row_with_nan_or_infinities_keeps_to_itself(k):
+    c = Shared([2, 1], [10, 0], [3, 2, 1], [200 * k, 177 * k, 20], P=16 * k, Hkv=2, share=4, D=128, seed=8)
     c.q[1, 2, 5] = np.nan
     c.q[5, 7, 0] = np.inf
     c.q[5, 7, 1] = -np.inf
@@ -134,11 +144,12 @@ def test_a_row_with_nan_or_infinities_keeps_to_itself():
     c.check(*c.run(), nan_rows={(1, 2), (5, 7), (8, 0)})
 
 
-def test_sessions_that_are_refused_are_zero_and_leave_their_group():
+@pytest.mark.parametrize("k", [1, 8])
+def test_sessions_that_are_refused_are_zero_and_leave_their_group(k):
     from speculative_decoding_verification_sdcp_gb300 import sdcp
 
     def case(change, bad, want):
-        c = Shared([4], [10], [2, 3, 1, 0], [165, 160, 180, 300], P=16, Hkv=2, share=2, D=64, seed=9)
+        c = Shared([4], [10], [2, 3, 1, 0], [165 * k, 160 * k, 180 * k, 300 * k], P=16 * k, Hkv=2, share=2, D=64, seed=9)
         change(c)
         out, st = c.run()
         c.check(out, st, bad)
@@ -165,10 +176,11 @@ def test_offsets_out_of_order():
     assert st.tolist() == [sdcp.S_BAD_PARAMS] * 2 and (out == 0).all()
 
 
-def test_last_offsets_past_the_batch():
+@pytest.mark.parametrize("k", [1, 8])
+def test_last_offsets_past_the_batch(k):
     """The last session's own pair is out of range: it is refused, the others' rows are theirs alone."""
     from speculative_decoding_verification_sdcp_gb300 import sdcp
-    c = Shared([3], [10], [2, 3, 1], [165, 160, 180], P=16, Hkv=1, share=4, D=64, seed=2)
+    c = Shared([3], [10], [2, 3, 1], [165 * k, 160 * k, 180 * k], P=16 * k, Hkv=1, share=4, D=64, seed=2)
     c.off = c.off.copy()
     c.off[3] += 1000
     out, st = c.run()
@@ -186,8 +198,8 @@ def test_another_stream_and_repeats_are_bit_equal():
 
 def test_captured_and_replayed_with_new_contents():
     from speculative_decoding_verification_sdcp_gb300 import sdcp
-    a = Shared([2, 2], [12, 9], [1, 2, 0, 3], [200, 195, 150, 160], P=16, Hkv=2, share=4, D=64, seed=11)
-    b = Shared([2, 2], [9, 20], [1, 2, 0, 3], [150, 170, 330, 321], P=16, Hkv=2, share=4, D=64, seed=12)
+    a = Shared([2, 2], [90, 9], [1, 2, 0, 3], [1600, 1560, 150, 160], P=16, Hkv=2, share=4, D=64, seed=11)
+    b = Shared([2, 2], [9, 80], [1, 2, 0, 3], [150, 170, 1330, 1321], P=16, Hkv=2, share=4, D=64, seed=12)
     wide = max(a.table.shape[1], b.table.shape[1])
     n = max(a.n_pages, b.n_pages)
     for c in (a, b):
@@ -214,7 +226,7 @@ def test_captured_and_replayed_with_new_contents():
 
 def test_pages_past_2_32_bytes():
     from speculative_decoding_verification_sdcp_gb300 import sdcp
-    c = Shared([2], [3], [2, 0], [200, 230], P=64, Hkv=8, share=1, D=128, seed=12)
+    c = Shared([2], [23], [2, 0], [1500, 1530], P=64, Hkv=8, share=1, D=128, seed=12)
     x, _ = c.run()
     n = (5 << 30) // int(sdcp.lib.sdcp_kv_page_bytes(64, 8, 128))
     big = torch.empty((n, 8, 2, 64 * 68), dtype=torch.uint8, device=DEV)
