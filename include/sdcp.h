@@ -589,6 +589,8 @@ size_t sdcp_pool_workspace_bytes(int32_t n_pages, int32_t n_slots);
  *               outside 0..max_pages, or one of these entries is outside the pool).
  * workspace     device scratch of sdcp_pool_workspace_bytes bytes, 256-byte aligned, no initialisation
  *               needed.
+ * A refused session may still hold shared pages where it was to write: keep it out of sdcp_append_kv (a
+ * kv_len of -1 there refuses it and writes nothing).
  */
 int sdcp_reserve_kv(const sdcp_kv_pool* pool, const int32_t* kv_len, const int32_t* upto,
                     sdcp_page_copy* copies, int32_t max_copies, int32_t* n_copies, int32_t* status,
