@@ -533,7 +533,7 @@ int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* offsets, 
  *   sdcp_fork_kv (new continuations), sdcp_reserve_kv (room for the round), for each layer
  *   sdcp_copy_pages and the layer itself, the verdict, sdcp_release_kv (what was rejected or has ended).
  * All are deterministic and asynchronous on `stream`; free pages are taken lowest first.  Calls on one
- * pool must not overlap.
+ * pool must not overlap, nor calls with one workspace.
  */
 typedef struct sdcp_kv_pool {    /* host struct */
   uint32_t struct_size;          /* sizeof(sdcp_kv_pool) */
@@ -695,7 +695,7 @@ size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32
  *               group_offsets[g+1] - 1; from 0, non-decreasing, to B.  NULL with n_groups 0: all sessions
  *               are one group.
  * workspace     device scratch of sdcp_attend_shared_workspace_bytes bytes, 256-byte aligned, no
- *               initialisation needed.
+ *               initialisation needed; calls that may run at once (streams, graphs) need one each.
  * Everything else, the arithmetic and the statuses among it, as for sdcp_attend_kv; group offsets that are
  * not in order refuse every session with SDCP_S_BAD_PARAMS, and a session that is refused leaves its
  * group.  (total_drafts + B) * q_heads is below 2^31.  A row's sum of weights is of the weights before

@@ -32,10 +32,10 @@
 // until its end is seen and S may be written again, the weights being in its place); the two blocks run beside
 // each other, so a step takes half of that, against 1024 cycles of the tensor cores (39 % of the time).
 // Measured (graph replays): 64 sessions of 9 rows and 64 / 8 heads of 128 channels, one prompt of 6000 tokens:
-// 170 us, 119 GFLOP at 0.70 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 193 us, 0.67; 16 sessions of 5
-// rows and 32 / 8 heads, 100001 tokens: 175 us, 0.75; sessions attended by themselves 230, 249 and 540 us.
-// Tried and slower: each tile's tokens halved between two groups of softmax warps (187 us for the first of
-// these), a second warp for the second product (172), registers split between the groups (204).
+// 172 us, 119 GFLOP at 0.69 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 196 us, 0.65; 16 sessions of 5
+// rows and 32 / 8 heads, 100001 tokens: 178 us, 0.74; sessions attended by themselves 230, 249 and 540 us.
+// Tried and slower (the first of these, 168 us then): each tile's tokens halved between two groups of softmax
+// warps, 187 us; a second warp for the second product, 172; registers split between the groups, 204 (of 195).
 #include <climits>
 #include <mutex>
 #include <type_traits>
@@ -337,7 +337,7 @@ struct Walk {
     it.last = en.last;
     it.step = en.step;
     it.end = en.last + en.step * (it.i0 + (it.g0 + it.n - 1) / share) + 1;
-    const int32_t real = (it.end - it.begin + kTile - 1) / kTile;
+    const int32_t real = (it.end - it.begin - 1) / kTile + 1;  // (ends may be next to 2^31)
     it.k0 = max(unit0 - kItemUnits, 0);
     it.k1 = min(max(unit0 + units - kItemUnits, 0), real);
     it.slot = (int32_t)blockIdx.x * 2 + (t == t_first ? 0 : 1);
@@ -390,8 +390,8 @@ template <int D> __device__ __forceinline__ void plan_item(const SharedArgs& a, 
 }
 
 // ---- the products: a warp, whose registers of a product are uniform; one lane issues ----------
-// (Issued from a branch that one thread takes, each product had its operands moved to uniform registers
-// anew: 180 cycles each against 64 that it takes.)
+// (Issued from a branch that one thread takes, each product has its operands moved to uniform registers anew:
+// the calls above took 20 to 30 % longer.)
 __device__ __forceinline__ void issue_smem_a(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{ .reg .pred p, e; elect.sync _|e, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
@@ -732,7 +732,7 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
         float sum = 0.0f;  // of the tile's weights
         // (rolled: five kinds of warps share a scheduler's instruction cache)
         auto tile = [&](auto with_mask) {
-          const uint64_t c2 = pair_of(a.c, a.c);
+          const uint64_t c2 = pair_of(a.c, a.c), zero2 = pair_of(0.0f, 0.0f);
 #pragma unroll 1
           for (int c = 0; c < kTile; c += 32) {
             float part;
@@ -747,7 +747,10 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
 #pragma unroll
               for (int y = 0; y < 32; y += 2) {
                 float u, v;
-                halves_of(fma_pair(pair_of(s[y], s[y + 1]), c2, nm2), u, v);
+                // The scaled score is rounded before the reference is taken off, as it was for the reference: with
+                // one rounding the largest of huge scores would be off by a rounding of itself, out of any
+                // range.  (As a sum with zero: a product and a sum of two numbers become one instruction.  2 %.)
+                halves_of(add_pair(fma_pair(pair_of(s[y], s[y + 1]), c2, zero2), nm2), u, v);
                 if (with_mask) {
                   if (c + y > lim) u = -INFINITY;
                   if (c + y + 1 > lim) v = -INFINITY;

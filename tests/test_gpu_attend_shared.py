@@ -268,3 +268,57 @@ def test_large_batches_against_the_attention_of_sessions(m, members, prefix, D):
     # |v| <= 7 * the largest scale of the pages; scores as small as these leave A below 2^7
     most = 7 * ref.scale_of(111)
     assert bool(((x.double() - y.double()).abs() <= 2 * (2.0**-8 * x.double().abs() + (2.0**-10 + 2.0**-11) * most)).all())
+
+
+@pytest.mark.parametrize("share", [130, 300])
+def test_more_heads_on_a_cached_one_than_a_block_has_pairs(share):
+    c = Shared([2], [13], [1, 0], [1700, 1664], P=128, Hkv=1, share=share, D=64, seed=31)
+    c.check(*c.run())
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: what each gives by itself."""
+    from speculative_decoding_verification_sdcp_gb300 import sdcp
+    cases = [Shared([4], [40], [3, 0, 8, 1], [1290, 1400, 1281, 1300], P=32, Hkv=2, share=8, D=D, seed=32 + D) for D in (64, 128)]
+    alone = [c.run()[0] for c in cases]
+    streams, tensors = [torch.cuda.Stream() for _ in cases], [c.tensors() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, t in zip(cases, streams, tensors):
+            sdcp.sdcp_attend_shared_kv(*t, scale=c.scale, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for c, t, want in zip(cases, tensors, alone):
+        assert torch.equal(t[7].view(torch.int16), want.view(torch.int16)) and t[8].tolist() == [0] * 4
+
+
+def test_rows_behind_the_batch_stay():
+    from speculative_decoding_verification_sdcp_gb300 import sdcp
+    c = Shared([3], [13], [1, 0, 2], [1700, 1664, 1669], P=128, Hkv=1, share=4, D=128, seed=33)
+    t = c.tensors()
+    more = lambda x, v: torch.cat([x, torch.full_like(x[:2], v)])  # noqa: E731
+    t[6], t[7] = more(t[6], float("nan")), more(t[7], 7.0)
+    sdcp.sdcp_attend_shared_kv(*t, scale=c.scale)
+    assert bool((t[7][-2:] == 7.0).all())
+    c.check(t[7][:-2], t[8].cpu().numpy())
+
+
+def test_a_wide_range_of_magnitudes():
+    """Queries of 2^-120 .. 2^100.  Where the largest score leads by more than scores round, its token has all the weight."""
+    c = Shared([2], [13], [3, 3], [1700, 1669], P=128, Hkv=1, share=4, D=64, seed=34, scale=1.0)
+    for r in range(8):
+        c.q[r] = ref.bf16(c.q[r] * np.float32(2.0) ** [-120, -60, -20, -5, 0, 8, 20, 100][r])
+    out, st = c.run()
+    assert st.tolist() == [0, 0]
+    c.check(out, st)
+    got, alone = out.double().cpu().numpy(), 0
+    v = ref.block_values(c.pages[c.table[1, :14]], c.P, c.D).transpose(2, 1, 0, 3, 4).reshape(2, -1, c.D)
+    for r in (6, 7):
+        for h in range(4):
+            q = c.q[r, h].astype(np.float64)
+            seen = v[0, :1669 + r - 3]
+            s, a = seen @ q, (np.abs(seen) @ np.abs(q)).max()
+            top = np.sort(s)[-2:]
+            if top[1] - top[0] > 2.0**-17 * a + 100:
+                want, alone = v[1, s.argmax()], alone + 1
+                assert (np.abs(got[r, h] - want) <= 2.0**-8 * np.abs(want)).all()
+    assert alone >= 4
