@@ -615,6 +615,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&r)[32]) {
                : "r"(at)
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+               : "r"(at)
+               : "memory");
+}
 // The loads are done, and r is what they brought (named, so that no use of it is moved before).
 __device__ __forceinline__ void tmem_loaded(float (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -653,12 +659,12 @@ __device__ __noinline__ Moved move_reference(SharedState& sh, int c, int32_t lim
                                              uint32_t used, float nm) {
   float m = -INFINITY;
 #pragma unroll 1
-  for (int d = c; d < kTile; d += 8) {
-    float r[8];
-    tmem_ld8(s_at + (uint32_t)d, r);
-    tmem_wait_ld();
+  for (int d = c; d < kTile; d += 32) {
+    float r[32];
+    tmem_ld32(s_at + (uint32_t)d, r);
+    tmem_loaded(r);
 #pragma unroll
-    for (int y = 0; y < 8; ++y) m = fmaxf(m, d + y > lim ? -INFINITY : r[y] * scale);  // NaN left out
+    for (int y = 0; y < 32; ++y) m = fmaxf(m, d + y > lim ? -INFINITY : r[y] * scale);  // NaN left out
   }
   const float old = nm;
   nm = fminf(nm, kLift - ceilf(m));
@@ -829,30 +835,31 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
     const uint32_t o0 = two ? o_at : lanes + kTmemO, o1 = lanes + kTmemO + (uint32_t)D;
     const int c0 = two ? 0 : x * (D / 2), c1 = two ? D : c0 + D / 2;
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 8) {
-      float o[8], w[8];
-      tmem_ld8(o0 + (uint32_t)c, o);
-      if (!two) tmem_ld8(o1 + (uint32_t)c, w);
+    for (int c = c0; c < c1; c += 16) {
+      float o[16], w[16];
+      tmem_ld16(o0 + (uint32_t)c, o);
+      if (!two) tmem_ld16(o1 + (uint32_t)c, w);
       tmem_wait_ld();
       if (live) {
 #pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        o[y] = f0 != 0.0f ? o[y] * f0 : 0.0f;
-        if (!two && f1 != 0.0f) o[y] += w[y] * f1;
-        o[y] *= scale;
-      }
-      if (direct) {
-        uint32_t b[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
-          b[y] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int y = 0; y < 16; ++y) {
+          o[y] = f0 != 0.0f ? o[y] * f0 : 0.0f;
+          if (!two && f1 != 0.0f) o[y] += w[y] * f1;
+          o[y] *= scale;
         }
-        *reinterpret_cast<uint4*>(a.out + place * D + c) = make_uint4(b[0], b[1], b[2], b[3]);
-      } else {
-        *reinterpret_cast<float4*>(to + c) = make_float4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<float4*>(to + c + 4) = make_float4(o[4], o[5], o[6], o[7]);
-      }
+        if (direct) {
+          uint32_t b[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * y], o[2 * y + 1]);
+            b[y] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) reinterpret_cast<uint4*>(a.out + place * D + c)[y] = make_uint4(b[4 * y], b[4 * y + 1], b[4 * y + 2], b[4 * y + 3]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) reinterpret_cast<float4*>(to + c)[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
       }
       __syncwarp();
     }
