@@ -32,7 +32,7 @@
 // until its end is seen and S may be written again, the weights being in its place); the two blocks run beside
 // each other, so a step takes half of that, against 1024 cycles of the tensor cores (39 % of the time).
 // Measured (graph replays): 64 sessions of 9 rows and 64 / 8 heads of 128 channels, one prompt of 6000 tokens:
-// 172 us, 119 GFLOP at 0.69 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 196 us, 0.65; 16 sessions of 5
+// 172 us, 119 GFLOP at 0.69 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 194 us, 0.66; 16 sessions of 5
 // rows and 32 / 8 heads, 100001 tokens: 178 us, 0.74; sessions attended by themselves 230, 249 and 540 us.
 // Tried and slower (the first of these, 168 us then): each tile's tokens halved between two groups of softmax
 // warps, 187 us; a second warp for the second product, 172; registers split between the groups, 204 (of 195).
