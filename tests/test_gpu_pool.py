@@ -254,3 +254,36 @@ def test_a_captured_branch_and_release():
         graph.replay()
     x.same(sts[2], [0] * 12)
     assert torch.equal(copies, first) and n.item() == 5 and all(set(s.tolist()) == {0} for s in sts)
+
+
+def test_a_captured_compaction():
+    """Compact and copy in one graph, replayed on two fillings of the pool and on a compact one."""
+    from speculative_decoding_verification_sdcp_gb300 import sdcp
+    x = Both(200, 16, 12, 10)
+    cache = sdcp.KvCache(200, 16, 2, 64, DEV)
+    (copies, n), live, st = x._list(101), ints([-9]), ints([-9])
+
+    def calls():
+        sdcp.sdcp_compact_kv(x.pool, copies, n, live, x.ws)
+        sdcp.sdcp_copy_pages(cache, copies, n, st)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    r = np.random.default_rng(4)
+    for _ in range(2):
+        x.reserve([0] * 12, r.integers(0, 160, 12).tolist())
+        x.release([int(k) for k in r.integers(-40, 60, 12)])
+        x.reserve([16 * h for h in x.plain.held], [16 * h + int(k) for h, k in zip(x.plain.held, r.integers(0, 50, 12))])
+        cache.pages.random_(0, 256)
+        for again in range(2):
+            rows = [[cache.pages[p].clone() for p in x.plain.table[b][:x.plain.held[b]]] for b in range(12)]
+            want, listed = x.plain.compact(101)
+            graph.replay()
+            x.same(ints([]), [])
+            assert live.tolist() == [want] and n.tolist() == [len(listed)] and st.tolist() == [0] and (len(listed) == 0 or not again)
+            for b in range(12):  # every row still finds its bytes
+                assert all(torch.equal(cache.pages[p], y) for p, y in zip(x.plain.table[b], rows[b]))
+        x.release([0] * 12)
