@@ -36,6 +36,7 @@
 // rows and 32 / 8 heads, 100001 tokens: 178 us, 0.74; sessions attended by themselves 230, 249 and 540 us.
 // Tried and slower (the first of these, 168 us then): each tile's tokens halved between two groups of softmax
 // warps, 187 us; a second warp for the second product, 172; registers split between the groups, 204 (of 195).
+#include <cfloat>
 #include <climits>
 #include <mutex>
 #include <type_traits>
@@ -55,6 +56,9 @@ constexpr int kMaxSms = 160;          // sizes the workspace
 constexpr int kItems = 4;             // planned ahead
 constexpr float kLift = 8.0f;         // a weight is 2^kLift at its reference
 constexpr float kTopSum = 32768.0f;   // and 32 tokens' weights sum to this at most
+// kLift - m before there is a reference.  Finite, so that a score of minus infinity (a product beyond binary32)
+// has no weight then either; any other score's weight is infinite and sets the reference.
+constexpr float kNoScore = FLT_MAX;
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // tensor memory: S (and the weights) of two blocks, O of two
 
 // What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.  Graph
@@ -668,7 +672,7 @@ __device__ __noinline__ Moved move_reference(SharedState& sh, int c, int32_t lim
   }
   const float old = nm;
   nm = fminf(nm, kLift - ceilf(m));
-  const float by = nm - old;  // a whole number (NaN: both infinite, nothing changes)
+  const float by = nm - old;  // a whole number, or far below -126
   const float f = nm == old ? 1.0f : by > -126.0f ? __int_as_float((127 + (int)by) << 23) : 0.0f;
   bool ok = true;
 #pragma unroll 1
@@ -728,7 +732,7 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
     const int32_t row = it.i0 + (it.g0 + min(at, it.n - 1)) / share;     // of the entry's rows
     const bool live = at < it.n, some = __any_sync(0xFFFFFFFFu, live);
     int32_t limit = it.last + it.step * row - it.begin - it.k0 * kTile;  // last token that it sees, from the tile's start
-    float nm = INFINITY, l = 0.0f;  // kLift - m: what a scaled score is shifted by (infinity: no score yet), and the sum
+    float nm = kNoScore, l = 0.0f;  // kLift - m: what a scaled score is shifted by, and the sum
     bool first = true;
     for (int32_t k = two ? 0 : x; k < n_tiles; k += two ? 1 : 2, ++used) {
       if (!wait(&sh.s_full[x], used & 1u)) break;
@@ -803,6 +807,7 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
     if (ok && !two && (x == 1 || n_tiles > 1)) wait(&sh.pv_done[x ^ 1], (used_other - 1u) & 1u);
     if (!ok) break;
     fence_after();
+    if (nm == kNoScore && l == 0.0f) nm = INFINITY;  // a sum of nothing
     float f0 = nm == INFINITY && l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f, top = nm, all = l;
     if (!two) {
       sh.ml[halves & 1u][x][pair] = make_float2(nm, l);
