@@ -309,12 +309,15 @@ template <int kCluster> __global__ void __cluster_dims__(kCluster, 1, 1) __launc
       Need o;
       (void)slot_need(p, a.kv_len[ob], a.upto[ob], p.held[ob], &o);
       long long here = 0, all = 0;
+      bool bad = false;
       for (int32_t i = o.first + tid; i < o.mid; i += kPoolThreads) {
         const int32_t e = p.row(ob)[i];
-        here += !p.inside(e) ? 1LL << 40 : p.refs[e] > 1 ? 1 : 0;
+        if (!p.inside(e)) bad = true;
+        else if (p.refs[e] > 1) ++here;
       }
       (void)block_scan(here, scratch, &all);
-      if (tid == 0) found[owner] = all >> 40 ? -1 : (int32_t)all;
+      bad = __syncthreads_or(bad) != 0;
+      if (tid == 0) found[owner] = bad ? -1 : (int32_t)all;
       __syncthreads();
     }
     if (s.n.mid - s.n.first > kAlone) {

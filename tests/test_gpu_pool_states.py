@@ -1,0 +1,21 @@
+"""The calls on pages where a pool was filled by hand, where a row is very long, and where pages run out."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_pool import DEV, _built, ints  # noqa: F401  (_built: a fixture, the library is built)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("entries", [2**24, 2**24 + 1])
+def test_a_long_row_without_a_usable_entry_is_refused(entries):
+    """However many entries are outside the pool, the slot is left as it was; another gets its page."""
+    from speculative_decoding_verification_sdcp_gb300 import sdcp
+    pool = sdcp.KvPool(10, 16, 2, entries, DEV)
+    pool.held[0] = entries
+    copies, n, st = torch.full((2, 4), -7, dtype=torch.int32, device=DEV), ints([-9]), ints([-9, -9])
+    sdcp.sdcp_reserve_kv(pool, ints([0, 0]), ints([entries * 16, 16]), copies, n, st, sdcp.alloc_pool_workspace(pool).fill_(255))
+    assert st.tolist() == [sdcp.S_BAD_PARAMS, sdcp.S_OK] and n.tolist() == [0]
+    assert pool.held.tolist() == [entries, 1] and pool.refs.tolist() == [1] + [0] * 9
+    assert bool((pool.page_table[0] == -1).all()) and pool.page_table[1, 0].item() == 0 and bool((pool.page_table[1, 1:] == -1).all())
