@@ -698,8 +698,8 @@ size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32
  *               initialisation needed; calls that may run at once (streams, graphs) need one each.
  * Everything else, the arithmetic and the statuses among it, as for sdcp_attend_kv; group offsets that are
  * not in order refuse every session with SDCP_S_BAD_PARAMS, and a session that is refused leaves its
- * group.  (total_drafts + B) * q_heads is below 2^31.  A row's sum of weights is of the weights before
- * their rounding to binary16.
+ * group.  (total_drafts + B) * q_heads is below 2^31, and n_groups + B at most 2^30.  A row's sum of
+ * weights is of the weights before their rounding to binary16.
  */
 int sdcp_attend_shared_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offsets,
                           int64_t total_drafts, const int32_t* kv_len, int32_t n_groups,

@@ -54,6 +54,7 @@ constexpr int kProductWarp = 0, kSoftWarp = 4, kKeyWarp = 12, kValueWarp = 16;  
 constexpr int kThreads = 20 * 32;
 constexpr int kMaxSms = 160;          // sizes the workspace
 constexpr int kItems = 4;             // planned ahead
+constexpr int64_t kMostEntries = 1 << 30;  // groups and sessions together: places in their list stay in 32 bits
 constexpr float kLift = 8.0f;         // a weight is 2^kLift at its reference
 constexpr float kTopSum = 32768.0f;   // and 32 tokens' weights sum to this at most
 // kLift - m before there is a reference.  Finite, so that a score of minus infinity (a product beyond binary32)
@@ -1159,6 +1160,7 @@ extern "C" size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_dr
   if (B < 0 || total_drafts < 0 || n_groups < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
   if (total_drafts > (int64_t)INT32_MAX / 2 - B || q_heads > (1 << 20) || (total_drafts + B) * q_heads > (int64_t)INT32_MAX) return 0;
+  if ((int64_t)n_groups + B > kMostEntries) return 0;
   return Layout(B, total_drafts, n_groups > 0 ? n_groups : 1, q_heads, head_dim).bytes;
 }
 
