@@ -425,7 +425,10 @@ __device__ __forceinline__ bool wait_both(bool want_a, uint64_t* a, uint32_t par
   unsigned long long t0 = 0;
   for (uint32_t n = 1;; ++n) {
     if (!done) done = mbar_try_wait(bar, parity);
-    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    if (__all_sync(0xFFFFFFFFu, done)) {
+      __syncwarp();  // a lane has looked at one of the two; a vote alone does not order what it saw before the others' work
+      return true;
+    }
     if (n % 1024u == 0u) {
       if (t0 == 0) t0 = global_ns();
       if (__any_sync(0xFFFFFFFFu, *dead != 0 || global_ns() - t0 > kWaitNs)) return false;
