@@ -530,7 +530,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
           if (cb < n16) {
             float x[8];
             tmem_ld8(s_at + (uint32_t)cb * 16u, x);
-            tmem_wait_ld();
+            tmem_loaded(x);
             block(cb, x, with_mask);
           }
       };
@@ -554,7 +554,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
             const int j0 = cb * 16 + wg * 8;
             float x[8];
             tmem_ld8(s_at + (uint32_t)cb * 16u, x);
-            tmem_wait_ld();
+            tmem_loaded(x);
 #pragma unroll
             for (int y = 0; y < 8; ++y) x[y] = (uint32_t)sh.last[j0 + y] - pos >= win ? -INFINITY : x[y] * a.c;
             const float m = warp_fold8(x, lane, [](float p, float q) { return fmaxf(p, q); });  // NaN left out
@@ -567,7 +567,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
               const int j0 = cb * 16 + wg * 8;
               float x[8];
               tmem_ld8(s_at + (uint32_t)cb * 16u, x);
-              tmem_wait_ld();
+              tmem_loaded(x);
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
                 const bool hidden = masked && (uint32_t)sh.last[j0 + y] - pos >= win;
@@ -599,7 +599,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
               float o[8];
               const uint32_t o_at = my_lanes + Sh::kTmemO + (uint32_t)j0;
               tmem_ld8(o_at, o);
-              tmem_wait_ld();
+              tmem_loaded(o);
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
                 l[cb * 8 + y] *= sh.f[j0 + y];
@@ -649,7 +649,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, AttendShared<k
       const int j0 = cb * 16 + wg * 8;
       float o[8];
       tmem_ld8(my_lanes + Sh::kTmemO + (uint32_t)j0, o);
-      tmem_wait_ld();
+      tmem_loaded(o);
       if (tok < D) {
         if (!it.whole) {
 #pragma unroll

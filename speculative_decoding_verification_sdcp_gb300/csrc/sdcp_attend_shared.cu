@@ -617,25 +617,6 @@ __device__ __forceinline__ void turn(const SharedArgs& a, SharedState& sh, unsig
 }
 
 // ---- the softmax: four warps a block of pairs, a pair a thread --------------------------------
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-               : "r"(at)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
-               : "r"(at)
-               : "memory");
-}
-// The loads are done, and r is what they brought (named, so that no use of it is moved before).
-__device__ __forceinline__ void tmem_loaded(float (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
-               :
-               : "memory");
-}
 // Two numbers of binary32 in an instruction.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
   uint64_t d;
@@ -685,7 +666,7 @@ __device__ __noinline__ Moved move_reference(SharedState& sh, int c, int32_t lim
     for (int e = 0; e < 16; e += 8) {
       float r[8];
       tmem_ld8(s_at + (uint32_t)(d + e), r);
-      tmem_wait_ld();
+      tmem_loaded(r);
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         const float lo = __half2float(__ushort_as_half((unsigned short)(__float_as_uint(r[y]) & 0xFFFFu)));
@@ -702,7 +683,7 @@ __device__ __noinline__ Moved move_reference(SharedState& sh, int c, int32_t lim
     for (int d = 0; d < D; d += 8) {
       float o[8];
       tmem_ld8(o_at + (uint32_t)d, o);
-      tmem_wait_ld();
+      tmem_loaded(o);
 #pragma unroll
       for (int y = 0; y < 8; ++y) o[y] *= f;
       tmem_st8(o_at + (uint32_t)d, o);
@@ -848,7 +829,8 @@ __device__ __forceinline__ void soften(const SharedArgs& a, SharedState& sh, int
       float o[16], w[16];
       tmem_ld16(o0 + (uint32_t)c, o);
       if (!two) tmem_ld16(o1 + (uint32_t)c, w);
-      tmem_wait_ld();
+      tmem_loaded(o);
+      if (!two) tmem_loaded(w);
       if (live) {
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
