@@ -632,7 +632,8 @@ int sdcp_release_kv(const sdcp_kv_pool* pool, const int32_t* keep, int32_t* stat
  * n_copies      device out, [1] int32: the moves made.
  * n_live        device out, [1] int32: L.
  * workspace     as for sdcp_reserve_kv.
- * Entries outside the pool stay as they are; rows are looked at up to held[b] (at most max_pages) entries.
+ * Entries outside the pool, and those that name a free page, stay as they are; rows are looked at up to held[b]
+ * (at most max_pages) entries.
  */
 int sdcp_compact_kv(const sdcp_kv_pool* pool, sdcp_page_copy* copies, int32_t max_copies,
                     int32_t* n_copies, int32_t* n_live, void* workspace, size_t workspace_bytes,

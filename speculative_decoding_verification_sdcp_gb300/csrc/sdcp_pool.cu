@@ -493,7 +493,7 @@ struct CompactArgs {
   int32_t* copies;  // [max_copies][4]
   int32_t max_copies;
   int32_t *n_copies, *n_live;
-  int32_t* to;  // [n_pages] the new place of a live page at or past n_live
+  int32_t* to;  // [n_pages] the new place of a page at or past n_live (its own, unless it is moved)
 };
 
 // With L pages live, a free page below L is hole number (page - live pages below it), and a live page at or
@@ -532,9 +532,9 @@ template <int kCluster> __global__ void __cluster_dims__(kCluster, 1, 1) __launc
       at += __popc(who);
       if (r[k] == INT_MIN && i >= pages.end) continue;
       if (i == live) *a.n_copies = min(live - below, a.max_copies);
+      if (i >= live) a.to[i] = i;  // (free ones too: a row filled by hand may name one)
       if (i >= live && r[k] > 0) {
         const int32_t k_move = live - below - 1;
-        a.to[i] = i;
         if (k_move < a.max_copies) {
           a.copies[(int64_t)k_move * 4] = i;
           a.copies[(int64_t)k_move * 4 + 2] = 1 << p.log_page;

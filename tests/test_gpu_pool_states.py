@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_pool import DEV, _built, ints  # noqa: F401  (_built: a fixture, the library is built)
+from test_gpu_pool import DEV, Both, _built, ints  # noqa: F401  (_built: a fixture, the library is built)
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,16 @@ def test_a_long_row_without_a_usable_entry_is_refused(entries):
     assert st.tolist() == [sdcp.S_BAD_PARAMS, sdcp.S_OK] and n.tolist() == [0]
     assert pool.held.tolist() == [entries, 1] and pool.refs.tolist() == [1] + [0] * 9
     assert bool((pool.page_table[0] == -1).all()) and pool.page_table[1, 0].item() == 0 and bool((pool.page_table[1, 1:] == -1).all())
+
+
+@pytest.mark.parametrize("n_pages", [40, 9000])
+def test_an_entry_that_names_a_free_page_stays(n_pages):
+    """Compaction renumbers pages that it moves, and no other entry."""
+    x = Both(n_pages, 16, 4, 12)
+    x.reserve([0] * 4, [16 * 12, 16 * 8, 16 * 12, 16])
+    x.release([16, -1, 0, -1])  # holes before the second slot's pages
+    x.plain.held[2] = 4
+    x.plain.table[2][:4] = [n_pages - 1, 30, 2, n_pages + 5]  # free ones past the live pages and before, one outside the pool
+    x.load()
+    assert x.compact(20)[0] == 10
+    assert x.plain.table[2][:4] == [n_pages - 1, 30, 2, n_pages + 5]
