@@ -144,8 +144,8 @@ struct SharedArgs {
   int32_t ctas;
   Header* header;
   int32_t* group_status;  // [groups] where there are many: whether the group offsets are in order
-  int32_t* group_of;      // [B]
-  int32_t* common;        // [B] leading pages a session has in common with its group's first
+  int32_t* lead;          // [B] the session of its group that a session's pages were compared with
+  int32_t* common;        // [B] leading pages it has in common with that one
   Entry* entries;         // [groups + B]: groups, then sessions
   int64_t* units;         // [groups + B] length on the line
   Cut* cuts;              // [ctas]
@@ -163,9 +163,10 @@ template <int D> struct Part {
 };
 
 // ---- plan ---------------------------------------------------------------------------------
-// A block a session: its status, its group, and the pages that it has in common with the group's first.
+// A block a session: its status, its group, and the pages that it has in common with `lead`, the group's first
+// session whose numbers do not refuse it (an ended one's length is -1).
 __global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const SharedArgs a) {
-  __shared__ int32_t common;
+  __shared__ int32_t common, lead;
   let_next_start();
   const int32_t b = (int32_t)blockIdx.x;
   const int64_t pairs = (a.s.total + a.s.B) * a.q_heads;
@@ -174,15 +175,14 @@ __global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const Share
   const bool kernel_before = a.s.B > kScanSessions || a.groups > kScanSessions;
   if (kernel_before) wait_for_previous();
   int32_t st = kv_session_status(a.kv, a.s, b, a.status);
-  int32_t g = 0, first = 0;
+  int32_t first = 0;
   if (a.group_offsets != nullptr) {
     bool bad = a.group_offsets[0] != 0 || a.group_offsets[a.groups] != a.s.B;
     bad |= a.groups <= kScanSessions ? !offsets_in_order(a.group_offsets, a.groups) : a.group_status[0] != SDCP_S_OK;
     if (__syncthreads_or(bad)) {
       st = SDCP_S_BAD_PARAMS;
     } else {
-      g = find_session(a.group_offsets, a.groups, b, false);
-      first = a.group_offsets[g];
+      first = a.group_offsets[find_session(a.group_offsets, a.groups, b, false)];
     }
   }
   if (st != SDCP_S_OK) {  // its rows become zero (what another session has of them is written later)
@@ -193,21 +193,47 @@ __global__ void __launch_bounds__(kCheckThreads) shared_check_kernel(const Share
   } else {
     // (pages that all rows of the round see whole)
     const int32_t n = a.s.start[b] >> a.kv.log_page;
-    if (threadIdx.x == 0) common = n;
-    __syncthreads();
     const int32_t* const mine = a.kv.page_table + (int64_t)b * a.kv.max_pages;
-    const int32_t* const other = a.kv.page_table + (int64_t)first * a.kv.max_pages;
-    if (first != b)
-      for (int32_t p = (int32_t)threadIdx.x; p < n; p += kCheckThreads)
-        if (mine[p] != other[p]) {
-          atomicMin(&common, p);
+    auto compare = [&](int32_t f) {
+      const int32_t* const other = a.kv.page_table + (int64_t)f * a.kv.max_pages;
+      if (f != b)
+        for (int32_t p = (int32_t)threadIdx.x; p < n; p += kCheckThreads)
+          if (mine[p] != other[p]) {
+            atomicMin(&common, p);
+            break;
+          }
+    };
+    auto refused = [&](int32_t lo, int32_t hi, int32_t start) {
+      int64_t end;
+      return kv_session_end(a.kv, a.s, lo, hi, start, &end) != SDCP_S_OK;
+    };
+    if (threadIdx.x == 0) {
+      common = n;
+      lead = first;
+    }
+    __syncthreads();
+    const int32_t lo = a.s.offsets[first], hi = a.s.offsets[first + 1], start = a.s.start[first];  // (on their way during the comparison)
+    compare(first);
+    if (refused(lo, hi, start)) {
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        common = n;
+        lead = b;
+      }
+      __syncthreads();
+      for (int32_t f = first + 1 + (int32_t)threadIdx.x; f < b; f += kCheckThreads)
+        if (!refused(a.s.offsets[f], a.s.offsets[f + 1], a.s.start[f])) {
+          atomicMin(&lead, f);
           break;
         }
+      __syncthreads();
+      compare(lead);
+    }
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     a.status[b] = st;
-    a.group_of[b] = g;
+    a.lead[b] = st == SDCP_S_OK ? lead : b;
     a.common[b] = st == SDCP_S_OK ? common : 0;
     if (st != SDCP_S_OK) a.units[a.groups + b] = 0;
     if (b == 0) a.header->error = 0u;
@@ -241,11 +267,14 @@ __global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const Shared
   __syncthreads();
   const int32_t share = a.q_heads / a.kv.heads;
   unsigned long long cost = 0;
-  int32_t least = INT_MAX, lowest = INT_MAX, highest = -1;
+  int32_t least = INT_MAX, lowest = INT_MAX, highest = -1, lead = -1;
+  bool leads_differ = false;
   for (int32_t b = b0 + (int32_t)threadIdx.x; b < b1; b += kCheckThreads)
     if (a.status[b] == SDCP_S_OK) {
       least = min(least, a.common[b]);
       lowest = min(lowest, b);
+      leads_differ |= highest >= 0 && a.lead[b] != lead;
+      lead = a.lead[b];
       highest = b;
       cost += (unsigned long long)cost_of_all((int64_t)(a.s.offsets[b + 1] - a.s.offsets[b] + 1) * share);
     }
@@ -256,6 +285,25 @@ __global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const Shared
     atomicAdd(&apart, cost);
   }
   __syncthreads();
+  // A lead that an entry of its row refused (rare: no call leaves such a row): the pages compared anew, with the first
+  // that is not refused.
+  if (__syncthreads_or(highest >= 0 && (lead != low || leads_differ))) {
+    const int32_t* const first = a.kv.page_table + (int64_t)low * a.kv.max_pages;
+    if (threadIdx.x == 0) pages = a.s.start[low] >> a.kv.log_page;
+    for (int32_t b = low + 1; b < b1; ++b) {
+      __syncthreads();
+      if (a.status[b] != SDCP_S_OK) continue;
+      const int32_t n = min(pages, a.s.start[b] >> a.kv.log_page);
+      const int32_t* const row = a.kv.page_table + (int64_t)b * a.kv.max_pages;
+      int32_t same = n;
+#pragma unroll 4
+      for (int32_t p = (int32_t)threadIdx.x; p < n; p += kCheckThreads)
+        if (row[p] != first[p]) same = min(same, p);
+      __syncthreads();
+      atomicMin(&pages, same);
+    }
+    __syncthreads();
+  }
   int32_t shared = 0;
   if (high > low && pages > 0) {
     const int64_t tokens = (int64_t)pages << a.kv.log_page, tiles = (tokens + kTile - 1) / kTile;
@@ -265,7 +313,7 @@ __global__ void __launch_bounds__(kCheckThreads) shared_plan_kernel(const Shared
   if (threadIdx.x == 0) {
     if (shared > 0) {
       const int32_t row0 = a.s.offsets[low] + low;  // (a refused one's offsets may be outside the batch)
-      plan_entry(a, g, Entry{row0, a.s.offsets[high + 1] + high + 1 - row0, 0, shared - 1, 0, b0, 0, 0, 0, 1});
+      plan_entry(a, g, Entry{row0, a.s.offsets[high + 1] + high + 1 - row0, 0, shared - 1, 0, low, 0, 0, 0, 1});
     } else {
       a.units[g] = 0;
     }
@@ -1067,7 +1115,7 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The workspace, piece by piece.
 struct Layout {
-  size_t group_status, group_of, common, entries, units, cuts, parts, acc, acc_ml, bytes;
+  size_t group_status, lead, common, entries, units, cuts, parts, acc, acc_ml, bytes;
   Layout(int64_t B, int64_t total, int64_t groups, int64_t q_heads, int64_t dim) {
     size_t at = 256;  // the header
     auto take = [&](size_t n) {
@@ -1077,7 +1125,7 @@ struct Layout {
     };
     const size_t pairs = (size_t)(total + B) * (size_t)q_heads;
     group_status = take((size_t)groups * 4);
-    group_of = take((size_t)B * 4);
+    lead = take((size_t)B * 4);
     common = take((size_t)B * 4);
     entries = take((size_t)(groups + B) * sizeof(Entry));
     units = take((size_t)(groups + B) * 8);
@@ -1173,7 +1221,7 @@ extern "C" int sdcp_attend_shared_kv(const sdcp_kv_cache* cache, int32_t B, cons
   const KvSessions s{B, m_offsets, total_drafts, 1, kv_len, 0, INT32_MAX};
   const SharedArgs a{kv, s, group_offsets, groups, static_cast<const __nv_bfloat16*>(q), q_stride, q_heads, scale * 1.4426950408889634f,
                      static_cast<__nv_bfloat16*>(out), status, D, min(di.sms, kMaxSms), reinterpret_cast<Header*>(w),
-                     reinterpret_cast<int32_t*>(w + at.group_status), reinterpret_cast<int32_t*>(w + at.group_of), reinterpret_cast<int32_t*>(w + at.common),
+                     reinterpret_cast<int32_t*>(w + at.group_status), reinterpret_cast<int32_t*>(w + at.lead), reinterpret_cast<int32_t*>(w + at.common),
                      reinterpret_cast<Entry*>(w + at.entries), reinterpret_cast<int64_t*>(w + at.units), reinterpret_cast<Cut*>(w + at.cuts),
                      reinterpret_cast<float*>(w + at.parts), reinterpret_cast<float*>(w + at.acc),
                      reinterpret_cast<float2*>(w + at.acc_ml)};

@@ -36,6 +36,13 @@ struct KvSessions {
   int32_t limit;           // positions below this only (the rotary table); INT32_MAX: none
 };
 
+// What a session's own numbers say of it, and one past its last position.
+__device__ __forceinline__ int32_t kv_session_end(const KvView& kv, const KvSessions& s, int32_t lo, int32_t hi, int32_t start, int64_t* end) {
+  if (lo < 0 || hi < lo || (int64_t)hi > s.total || start < 0) return SDCP_S_BAD_PARAMS;
+  *end = (int64_t)start + (hi - lo) + s.extra;
+  return *end > start && *end > min((int64_t)kv.max_pages << kv.log_page, (int64_t)s.limit) ? SDCP_S_LIMIT : SDCP_S_OK;
+}
+
 // The status of session b, found by a whole block of kCheckThreads: the batch's offsets in order, its own
 // in range, a start that is not negative, the last position inside the page table's row and the limit,
 // every page that the rows touch inside the pool.  A kernel of one block a session writes status[] before
@@ -45,10 +52,10 @@ __device__ __forceinline__ int32_t kv_session_status(const KvView& kv, const KvS
   const int32_t lo = s.offsets[b], hi = s.offsets[b + 1], start = s.start[b];
   if (s.B > kScanSessions) wait_for_previous();  // (it writes status[] too)
   bool bad = s.B <= kScanSessions ? !offsets_in_order(s.offsets, s.B) : status[b] != SDCP_S_OK;
-  if (lo < 0 || hi < lo || (int64_t)hi > s.total || start < 0) return SDCP_S_BAD_PARAMS;
-  const int64_t end = (int64_t)start + (hi - lo) + s.extra;  // one past the last position
+  int64_t end;
+  const int32_t st = kv_session_end(kv, s, lo, hi, start, &end);
+  if (st != SDCP_S_OK) return st;
   if (end == start) return __syncthreads_or(bad) ? SDCP_S_BAD_PARAMS : SDCP_S_OK;  // no rows
-  if (end > min((int64_t)kv.max_pages << kv.log_page, (int64_t)s.limit)) return SDCP_S_LIMIT;
   const int64_t first = s.window < 0 ? start : s.window == 0 ? 0 : max((int64_t)0, (int64_t)start + 1 - s.window);
   for (int64_t p = (first >> kv.log_page) + threadIdx.x; p <= (end - 1) >> kv.log_page; p += kCheckThreads) {
     const int32_t page = kv.page_table[(int64_t)b * kv.max_pages + p];
