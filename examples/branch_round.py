@@ -46,8 +46,9 @@ class Branches(verify_round.Rounds):
         # the prompts but their last tokens, by each session's first slot; the others fork it
         self.kv_len = [0] * slots
         rows = [p[:-1] if s % branches == 0 else [] for s, p in enumerate(self.history)]
-        status = self.score(rows, grouped=False)[3]
-        self._checked(status, "the prompts")
+        if any(rows):  # (nothing, of prompts of one token)
+            status = self.score(rows, grouped=False)[3]
+            self._checked(status, "the prompts")
         self.kv_len = [len(p) - 1 for p in self.history]
         forked = self._int([0] * slots)
         sdcp.sdcp_fork_kv(self.pool, self._int([-1 if s % branches == 0 else s - s % branches for s in range(slots)]), self._int(self.kv_len), forked)
