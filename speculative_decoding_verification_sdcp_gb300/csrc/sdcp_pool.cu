@@ -658,7 +658,7 @@ extern "C" int sdcp_release_kv(const sdcp_kv_pool* pool, const int32_t* keep, in
 }
 
 extern "C" size_t sdcp_pool_workspace_bytes(int32_t n_pages, int32_t n_slots) {
-  if (n_pages < 1 || n_slots < 0) return 0;
+  if (n_pages < 1 || n_slots < 0 || n_pages > kMostEntries || n_slots > kMostEntries) return 0;
   return 2 * round256((size_t)n_pages * 4) + round256((size_t)n_slots * 8) + round256((size_t)n_slots * 4);
 }
 
