@@ -522,10 +522,11 @@ int sdcp_read_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* offsets, 
 /*
  * A pool keeps who holds which page, in three device arrays that these calls alone change: slot b (a
  * session, or a place for one) has row b of page_table, whose first held[b] entries are pages; refs[p]
- * is the number of rows that hold page p, 0 for a free one.  An empty pool is held = 0, refs = 0.  Rows
- * may share pages (sdcp_fork_kv); a page is written only while one row holds it (sdcp_reserve_kv).  The
- * arrays serve all layers of a model: each layer's cache has the same n_pages and page_tokens, its batch
- * rows are rows of page_table, and only sdcp_copy_pages, the bytes themselves, runs once for each.
+ * is the number of rows that hold page p, 0 for a free one, never negative.  An empty pool is held = 0,
+ * refs = 0.  Rows may share pages (sdcp_fork_kv); a page is written only while one row holds it
+ * (sdcp_reserve_kv).  The arrays serve all layers of a model: each layer's cache has the same n_pages and
+ * page_tokens, its batch rows are rows of page_table, and only sdcp_copy_pages, the bytes themselves, runs
+ * once for each.
  *
  * The calls work on all slots at once; arrays of one entry a slot say what is to happen to it.  No call
  * reads a number back: counts stay on the device (n_copies), and a slot whose request is refused is left
@@ -677,7 +678,9 @@ int sdcp_attend_kv(const sdcp_kv_cache* cache, int32_t B, const int32_t* m_offse
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace sdcp_attend_shared_kv needs (n_groups 0: as 1); 0 for invalid sizes.  What
- * suffices for a batch does for any with no more sessions, drafts and groups (and the same heads). */
+ * suffices for a batch does for any with no more sessions, drafts and groups (and the same heads).  Four
+ * times the bytes of out (two sums in binary32 for each row and head, whether or not anything is shared),
+ * 16 bytes for each row and head, some 60 for each session and group, and 43 MB (22 MB for 64 channels). */
 size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32_t n_groups,
                                           int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 
@@ -688,7 +691,7 @@ size_t sdcp_attend_shared_workspace_bytes(int32_t B, int64_t total_drafts, int32
  * the group agree, as far as every one of them has cached whole pages.  These pages are read and turned
  * once for the group's rows together; the rest of each session for its own rows.  Where that would save
  * less than joining the two costs (few sessions, short stretches), the group's sessions are attended by
- * themselves.  What a group is only decides how the sum is cut: the output is sdcp_attend_kv's up to rounding
+ * themselves, as this call does it.  What a group is only decides how the sum is cut: the output is sdcp_attend_kv's up to rounding
  * for any grouping.  (A batch that shares little is faster with sdcp_attend_kv: eight sessions of a row each
  * gain from about 2000 shared tokens on, two from about 10000.)
  *

@@ -32,8 +32,8 @@
 // until its end is seen and S may be written again, the weights being in its place); the two blocks run beside
 // each other, so a step takes half of that, against 1024 cycles of the tensor cores (39 % of the time).
 // Measured (graph replays): 64 sessions of 9 rows and 64 / 8 heads of 128 channels, one prompt of 6000 tokens:
-// 172 us, 119 GFLOP at 0.69 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 194 us, 0.66; 16 sessions of 5
-// rows and 32 / 8 heads, 100001 tokens: 178 us, 0.74; sessions attended by themselves 230, 249 and 540 us.
+// 173 us, 119 GFLOP at 0.69 PFLOP/s; prompts of 4000 .. 8200 for groups of eight: 194 us, 0.66; 16 sessions of 5
+// rows and 32 / 8 heads, 100001 tokens: 178 us, 0.74; by the attention of sessions by themselves 230, 249 and 541 us.
 // Tried and slower (the first of these, 168 us then): each tile's tokens halved between two groups of softmax
 // warps, 187 us; a second warp for the second product, 172; registers split between the groups, 204 (of 195).
 #include <cfloat>
@@ -63,12 +63,12 @@ constexpr float kNoScore = FLT_MAX;
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // tensor memory: S (and the weights) of two blocks, O of two
 
 // What a tile costs on the line (through one block, through two), and an item's start and end, in tiles.  Graph
-// replays of the measured calls below, us with 5, 8, 3 / 5, 10, 3 / 5, 8, 5 / 8, 13, 2: groups of eight
-// 193 / 213 / 199 / 216, ragged 126 / 140 / 138 / 141, one document 174 / 183 / 178 / 199.
+// replays of the measured calls above and of ragged groups, us with 5, 8, 3 / 5, 10, 3 / 5, 8, 5 / 8, 13, 2: groups of
+// eight 193 / 213 / 201 / 215, ragged 132 / 136 / 143 / 138, one document 177 / 180 / 179 / 191, one prompt 172 / 192 / 177 / 192.
 constexpr int32_t kOneBlock = 5, kTwoBlocks = 8, kItemUnits = 3;
 // What a pair's second part costs, in the same measure: 1 / kPairsAUnit.  A group's pages are attended together
 // where that saves more than the parts cost: 64 sessions of 9 rows in groups of eight, 64 heads, with 512 / 2048
-// shared tokens take 103 / 124 us together, 88 / 130 by themselves; of a row in pairs, 72 / 95 and 70 / 112.
+// shared tokens take 105 / 126 us together, 92 / 135 by themselves; of a row in pairs, 74 / 98 and 74 / 116.
 constexpr int32_t kPairsAUnit = 3;
 
 // Rows over a stretch of tokens: of a group over its shared pages, or of a session over what is behind them.

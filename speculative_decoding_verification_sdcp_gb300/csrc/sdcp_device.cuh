@@ -334,8 +334,8 @@ __device__ __forceinline__ unsigned long long global_ns() {
 constexpr uint32_t kSuspendNs = 100000;
 #ifdef SDCP_TEST_WAIT_EXPIRY
 // Test build only (the flag is never set in the library): waits give up after 20 ms, and the
-// row kernel leaves one ring stage unfilled (sdcp_rows.cu) and the attention hand-overs of weights out
-// (sdcp_attend.cu), so waits run out on purpose.
+// row kernel leaves one ring stage unfilled (sdcp_rows.cu) and both kinds of attention hand-overs of weights out
+// (sdcp_attend.cu, sdcp_attend_shared.cu), so waits run out on purpose.
 constexpr unsigned long long kWaitNs = 20000000ull;
 #else
 constexpr unsigned long long kWaitNs = 2000000000ull;
