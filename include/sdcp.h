@@ -661,7 +661,7 @@ size_t sdcp_attend_workspace_bytes(int32_t B, int64_t total_drafts, int32_t q_he
  * scale         finite; usually 1 / sqrt(head_dim).
  * window        0 = none, else the number of positions a row sees, itself included.
  * out           device out, [total_drafts + B][q_heads][head_dim] bfloat16, contiguous, 16-byte
- *               aligned.
+ *               aligned.  Must not overlap q.
  * status        device out, [B] int32, as for sdcp_append_kv (only the pages a row attends are
  *               looked at; there is no rotary table's limit here); the rows of a session that
  *               is not SDCP_S_OK are zero, which a model turns into ordinary logits: see

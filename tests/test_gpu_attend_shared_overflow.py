@@ -34,3 +34,18 @@ def test_a_score_of_minus_infinity_has_no_weight(members, common, best, D):
     for b in range(members):
         want = ref.block_values(c.pages[c.table[b, best // 128], 0, 1], 128, D)[best % 128]
         assert (np.abs(got[2 * b:2 * b + 2] - want) <= 2.0**-8 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("members,common", [(1, 0), (2, 13), (40, 13)])
+def test_a_query_with_an_infinity_gives_nan_in_its_row_alone(members, common):
+    """All its scores are infinite, of one sign: no weight at all, or infinite ones."""
+    c = Shared([members], [common], [1] * members, [1700 + b for b in range(members)], P=128, Hkv=1, share=4, D=64, seed=members, scale=1.0, q_scale=0.1)
+    for b in range(members):
+        for t in range(c.lens[b] + 2):
+            page, slot = c.pages[c.table[b, t // 128], 0, 0], t % 128
+            for g in range(2):
+                page[(g * 128 + slot) * 16:(g * 128 + slot) * 16 + 16] = 0xFF
+    some = range(0, 2 * members, 3)
+    for r in some:
+        c.q[r, r % 4, r % 64] = -np.inf if r % 2 == 0 else np.inf
+    c.check(*c.run(), nan_rows={(r, r % 4) for r in some})
